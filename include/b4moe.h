@@ -346,6 +346,136 @@ size_t b4_linear_workspace_bytes(const b4_moe_config* cfg);
 b4_status b4_linear(const b4_moe_config* cfg, const uint16_t* x, const uint8_t* w, const uint8_t* s,
                     const float* gs, uint16_t* out, void* workspace, size_t workspace_bytes, b4_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * FP4 x FP4 (W4A4): block-scaled quantisation, the product of two quantised
+ * operands, the product grouped by expert with ragged sizes, and the MoE layer
+ * built of them.  The pages have no counterpart: their layer keeps activations
+ * in 16 bits.
+ *
+ * A quantised operand of R rows and K columns:
+ *   codes   [R][ld] uint8, ld = K/2 rounded up to 16 bytes, element 2j of a row in
+ *           the low nibble of byte j (the checkpoint layout when K is a multiple of
+ *           32); bytes past K/2 are not read.
+ *   scales  B4_FP4_SCALES_TILED: 512-byte tiles of 128 rows x 4 scale blocks,
+ *           [row tile][ceil(K / 4g)][row % 32][row / 32 % 4][block % 4], g = 16
+ *           (NVFP4, E4M3) or 32 (MXFP4, E8M0).  Scales of blocks past K must be zero
+ *           (a NaN there would meet zero codes and still be NaN); rows past the
+ *           operand's may hold anything.  B4_FP4_SCALES_ROWS: [R][K/g], the
+ *           checkpoint layout b4_prepare_weights reads.
+ *   gs      fp32 (NVFP4 only): the value of an element is gs * scale * e2m1(code).
+ * Groups.  A stack holds num_groups matrices of m rows each, every one starting at
+ * a row tile of its own (e * ceil(m / 128)).  A ragged operand (offsets given) holds
+ * the rows offsets[e] .. offsets[e + 1] of group e, offsets [num_groups + 1] int32
+ * ascending on the device as b4_route_pack writes it, m its row capacity; group e's
+ * scales start at row tile offsets[e] / 128 + e.
+ *
+ * Every call validates on the host before it launches, enqueues on `stream`, and
+ * neither allocates nor synchronises (capture-safe).  Results are bitwise
+ * reproducible. */
+typedef enum b4_dtype { B4_DTYPE_BF16 = 0, B4_DTYPE_F16 = 1, B4_DTYPE_F32 = 2 } b4_dtype;
+
+/* Global scales of the quantised rows.  NONE: MXFP4.  GIVEN: gs[num_groups] is an
+ * input (static calibration).  ROW: gs[rows] is an output, 2^j with j >= -126 the
+ * least power of two with amax_row <= 6 * 448 * 2^j (1 for a zero row).  A power of
+ * two costs the E4M3 scales no precision.  TENSOR: gs[num_groups] is an output,
+ * amax / (6 * 448) of each matrix of a stack (1 for a zero matrix), as checkpoints
+ * of NVFP4 weights hold it. */
+typedef enum b4_fp4_gs {
+  B4_FP4_GS_NONE = 0,
+  B4_FP4_GS_GIVEN = 1,
+  B4_FP4_GS_ROW = 2,
+  B4_FP4_GS_TENSOR = 3
+} b4_fp4_gs;
+
+typedef enum b4_fp4_scale_layout { B4_FP4_SCALES_TILED = 0, B4_FP4_SCALES_ROWS = 1 } b4_fp4_scale_layout;
+
+typedef struct b4_fp4_config {
+  int32_t m;            /* rows per matrix of a stack, or row capacity of a ragged operand; >= 0 */
+  int32_t n;            /* rows of each weight matrix (outputs); any value >= 1; unused by b4_fp4_quantize */
+  int32_t k;            /* quantised columns: multiple of 16 (NVFP4) or 32 (MXFP4) */
+  int32_t num_groups;   /* 1 .. B4_MAX_LOCAL_EXPERTS */
+  int32_t format;       /* b4_format */
+  int32_t x_dtype;      /* b4_dtype of x and values */
+  int32_t out_dtype;    /* b4_dtype of the product */
+  int32_t activation;   /* -1: none; else b4_activation applied to x first: the gated ones read rows of
+                           2 k elements, gate then up; RELU2 rows of k */
+  int32_t gs_mode;      /* b4_fp4_gs */
+  int32_t scale_layout; /* b4_fp4_scale_layout of the quantiser's output */
+  int32_t row_div;      /* with `rows`: row i of the operand is x row rows[i] / row_div (top_k for packed routes) */
+  int32_t x_rows;       /* with `rows`: x rows outside [0, x_rows) read as zeros (0: not checked above) */
+  float swiglu_alpha, swiglu_beta, swiglu_limit; /* B4_ACT_SWIGLU_OAI only */
+  int64_t x_stride;     /* elements between rows of x; 0: the row's own width */
+  int64_t out_stride;   /* elements between rows of out; 0: n */
+} b4_fp4_config;
+
+/* Bytes of the codes and of the scales of the operand that cfg describes (rows:
+ * num_groups * m of a stack, m when ragged != 0).  0 for an invalid cfg. */
+size_t b4_fp4_codes_bytes(const b4_fp4_config* cfg, int32_t ragged);
+size_t b4_fp4_scale_bytes(const b4_fp4_config* cfg, int32_t ragged);
+
+/* Quantises rows of x (after the activation, in fp32):
+ *   NVFP4  s = e4m3(amax_block / (6 gs)), d = s gs, c = e2m1(h / d), c = 0 where d = 0
+ *   MXFP4  s = 2^j, j >= -127 the least with amax_block <= 6 * 2^j, c = e2m1(h / s)
+ * every step IEEE fp32, conversions to nearest even, saturating.  rows (or NULL)
+ * gathers: a negative entry gives a zero row.  values (or NULL) receives
+ * gs * scale * e2m1(code) in x's type, [rows][k].  A NaN in a block makes its scale
+ * NaN; under ROW and TENSOR an infinity or NaN makes gs non-finite and the values it
+ * scales NaN; under GIVEN and MXFP4 an infinity saturates (MXFP4: scale 2^127).
+ * Tiled scales of a stack are written in full, the missing rows of its last row
+ * tiles as zeros; those of a ragged operand only where rows are live, and its rows
+ * past offsets[num_groups] are not written at all.
+ * TENSOR takes neither rows nor offsets.  1 launch (TENSOR: a memset and 3). */
+b4_status b4_fp4_quantize(const b4_fp4_config* cfg, const void* x, const int32_t* rows, const int32_t* offsets,
+                          float* gs, uint8_t* codes, uint8_t* scales, void* values, b4_stream_t stream);
+
+/* Row-major scales of a checkpoint, [num_groups][m][k / g], into tiles. */
+b4_status b4_fp4_tile_scales(const b4_fp4_config* cfg, const uint8_t* src, uint8_t* dst, b4_stream_t stream);
+
+/* out[t][n] = gs_a gs_w[e] sum_k (scale e2m1)_a[t][k] (scale e2m1)_w[e][n][k] for the
+ * rows t of group e, accumulated in fp32 by the tensor cores and rounded once.
+ *
+ * a_codes, a_scales  quantised activations (tiled scales); a_gs by gs_mode: per row
+ *               (ROW), per group (GIVEN, TENSOR), NULL (MXFP4).
+ * w_codes       [num_groups][n][ld]; w_scales tiles of the stack of n-row matrices;
+ *               w_gs [num_groups] (NVFP4).
+ * offsets       NULL: a stack of m rows per group.
+ * out           [rows][out_stride].  Ragged without out_rows: written in full, rows
+ *               past offsets[num_groups] as zeros.
+ * out_rows      NULL, or the output row of each operand row ([m] int32; entries
+ *               outside [0, m) are dropped): packed routes go back to route order.
+ * device_status NULL, or 2 uint32 that the caller has zeroed: B4_ERR_TIMEOUT and the
+ *               wait site if a bounded wait ran out, untouched otherwise.
+ * 1 launch.  Does not read x, x_rows, x_stride, row_div, activation, scale_layout. */
+b4_status b4_fp4_matmul(const b4_fp4_config* cfg, const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gs,
+                        const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gs, const int32_t* offsets,
+                        const int32_t* out_rows, void* out, uint32_t* device_status, b4_stream_t stream);
+
+/* b4_fp4_quantize of x into the workspace, then b4_fp4_matmul: 2 launches, the
+ * second set up under the first.  num_groups is 1 unless offsets is given.
+ * x_gs: [num_groups] with GIVEN, NULL otherwise (TENSOR is refused).
+ * workspace: >= b4_fp4_linear_workspace_bytes(cfg), 256-byte aligned; holds the
+ * status word that b4_check_status reads. */
+size_t b4_fp4_linear_workspace_bytes(const b4_fp4_config* cfg);
+b4_status b4_fp4_linear(const b4_fp4_config* cfg, const void* x, const float* x_gs, const int32_t* rows,
+                        const int32_t* offsets, const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gs,
+                        const int32_t* out_rows, void* out, void* workspace, size_t workspace_bytes,
+                        b4_stream_t stream);
+
+/* The fused MoE layer with 4-bit activations: route packing, x rows gathered and
+ * quantised, grouped FC1 (bf16 out), activation and quantisation, grouped FC2 stored
+ * in route order (bf16), and the weighted sum of each token's valid routes in fp32
+ * with one rounding.  cfg, routing and activations as b4_fused_moe (cfg->path is
+ * ignored); weights as quantised operands: w13 [E_l][2 I or I][ld(H)] with gate rows
+ * first, w2 [E_l][H][ld(I)], tiled scales, gs13 / gs2 [E_l] (NVFP4).  NVFP4
+ * activations take per-row global scales.  The intermediate roundings to bf16 (FC1's
+ * output, each route's FC2 output) are far below the 4-bit activations' own.
+ * 6 launches. */
+size_t b4_fused_moe_a4_workspace_bytes(const b4_moe_config* cfg, int32_t activation);
+b4_status b4_fused_moe_a4(const b4_moe_config* cfg, const uint16_t* x, const uint8_t* w13, const uint8_t* s13,
+                          const float* gs13, const uint8_t* w2, const uint8_t* s2, const float* gs2,
+                          const int32_t* topk_ids, const float* topk_weights, int32_t activation, uint16_t* out,
+                          void* workspace, size_t workspace_bytes, b4_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* b4_status_string(int32_t status);
 

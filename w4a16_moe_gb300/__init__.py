@@ -40,6 +40,14 @@ DECODE_MAX_M = 64
 NOALLOC_SCRATCH_BYTES = 64 << 20
 FORMATS = {"nvfp4_e4m3_k16": NVFP4, "mxfp4_e8m0_k32": MXFP4}
 ACTIVATIONS = {"silu": SILU, "relu2": RELU2, "swiglu_oai": SWIGLU_OAI}
+# FP4 operators: element types, global-scale modes and scale layouts
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+GS_NONE = 0
+GS_GIVEN = 1
+GS_ROW = 2
+GS_TENSOR = 3
+SCALES_TILED = 0
+SCALES_ROWS = 1
 # the gpt-oss models' clamped-swiglu parameters (alpha, beta, limit)
 SWIGLU_OAI_DEFAULTS = (1.702, 1.0, 7.0)
 
@@ -67,6 +75,28 @@ class _Config(ctypes.Structure):
     ]
 
 
+class _Fp4Config(ctypes.Structure):
+    _fields_ = [
+        ("m", ctypes.c_int32),
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("gs_mode", ctypes.c_int32),
+        ("scale_layout", ctypes.c_int32),
+        ("row_div", ctypes.c_int32),
+        ("x_rows", ctypes.c_int32),
+        ("swiglu_alpha", ctypes.c_float),
+        ("swiglu_beta", ctypes.c_float),
+        ("swiglu_limit", ctypes.c_float),
+        ("x_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -78,6 +108,7 @@ def _load():
     S = ctypes.c_size_t
     I32 = ctypes.c_int32
     CP = ctypes.POINTER(_Config)
+    FP = ctypes.POINTER(_Fp4Config)
     sigs = {
         "b4_route_capacity_tokens": (I32, [I32]),
         "b4_workspace_bytes": (S, [CP, I32]),
@@ -92,6 +123,15 @@ def _load():
         "b4_wait_self_test": (I32, [P, S, ctypes.c_uint32, P]),
         "b4_set_timing_events": (I32, [ctypes.POINTER(P), I32]),
         "b4_set_trace": (I32, [P, S]),
+        "b4_fp4_codes_bytes": (S, [FP, I32]),
+        "b4_fp4_scale_bytes": (S, [FP, I32]),
+        "b4_fp4_quantize": (I32, [FP, P, P, P, P, P, P, P, P]),
+        "b4_fp4_tile_scales": (I32, [FP, P, P, P]),
+        "b4_fp4_matmul": (I32, [FP, P, P, P, P, P, P, P, P, P, P, P]),
+        "b4_fp4_linear_workspace_bytes": (S, [FP]),
+        "b4_fp4_linear": (I32, [FP, P, P, P, P, P, P, P, P, P, P, S, P]),
+        "b4_fused_moe_a4_workspace_bytes": (S, [CP, I32]),
+        "b4_fused_moe_a4": (I32, [CP, P, P, P, P, P, P, P, P, P, I32, P, P, S, P]),
         "b4_status_string": (ctypes.c_char_p, [I32]),
         "b4_last_error": (ctypes.c_char_p, []),
     }
@@ -117,6 +157,15 @@ EXPORTED = (
     "b4_wait_self_test",
     "b4_set_timing_events",
     "b4_set_trace",
+    "b4_fp4_codes_bytes",
+    "b4_fp4_scale_bytes",
+    "b4_fp4_quantize",
+    "b4_fp4_tile_scales",
+    "b4_fp4_matmul",
+    "b4_fp4_linear_workspace_bytes",
+    "b4_fp4_linear",
+    "b4_fused_moe_a4_workspace_bytes",
+    "b4_fused_moe_a4",
     "b4_status_string",
     "b4_last_error",
 )
@@ -304,6 +353,236 @@ def linear(cfg: MoEConfig, x, w, s, gs, out, workspace, stream=None):
     c = cfg._c()
     _check(_lib.b4_linear(ctypes.byref(c), _ptr(x), _ptr(w), _ptr(s), _ptr(gs), _ptr(out), _ptr(workspace),
                           workspace.numel(), _stream(stream)))
+
+
+# ------------------------------------------------------- FP4 x FP4 operators
+
+
+class Fp4Config:
+    """Shape of one call of the FP4 operators (``b4_fp4_config`` in b4moe.h); read-only once made.
+
+    ``m`` rows (per matrix of a stack, or the row capacity with ``offsets``), ``n`` outputs, ``k`` quantised
+    columns.  ``activation``: None, or SILU / RELU2 / SWIGLU_OAI applied to x first.  ``gs_mode`` defaults to
+    GS_ROW for NVFP4 and GS_NONE for MXFP4.
+    """
+
+    def __init__(self, m, k, n=1, num_groups=1, format=NVFP4, x_dtype=torch.bfloat16, out_dtype=torch.bfloat16,
+                 activation=None, gs_mode=None, scale_layout=SCALES_TILED, row_div=1, x_rows=0,
+                 swiglu=SWIGLU_OAI_DEFAULTS, x_stride=0, out_stride=0):
+        for t, name in ((x_dtype, "x_dtype"), (out_dtype, "out_dtype")):
+            if t not in DTYPES:
+                raise TypeError(f"{name} must be one of {list(DTYPES)}, got {t}")
+        if gs_mode is None:
+            gs_mode = GS_ROW if format == NVFP4 else GS_NONE
+        self.m, self.k, self.n, self.num_groups = int(m), int(k), int(n), int(num_groups)
+        self.format, self.gs_mode, self.x_dtype, self.out_dtype = format, gs_mode, x_dtype, out_dtype
+        self.scale_layout = scale_layout
+        self.gated = activation in (SILU, SWIGLU_OAI)
+        self.width = 2 * self.k if self.gated else self.k
+        self.x_stride = int(x_stride) or self.width
+        self.out_stride = int(out_stride) or self.n
+        self.ld = (self.k // 2 + 15) // 16 * 16
+        self._struct = _Fp4Config(self.m, self.n, self.k, self.num_groups, format, DTYPES[x_dtype], DTYPES[out_dtype],
+                                  -1 if activation is None else activation, gs_mode, scale_layout, int(row_div),
+                                  int(x_rows), *swiglu, int(x_stride), int(out_stride))
+        self._ref = ctypes.byref(self._struct)
+
+    def rows(self, ragged):
+        return self.m if ragged else self.m * self.num_groups
+
+
+def _fp4_x(cfg, x, rows, offsets):
+    """x as the config describes it: a 2-D view of rows, or any contiguous shape with that many elements.
+    Returns the call's config: with gathered rows, bounded by the rows x holds."""
+    if x.dtype != cfg.x_dtype:
+        raise TypeError(f"x must be {cfg.x_dtype}, got {x.dtype}")
+    if not x.is_contiguous():
+        if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) != cfg.x_stride:
+            raise ValueError("x must be contiguous, or two-dimensional with rows x_stride elements apart")
+        n = x.shape[0]
+        if x.shape[1] < cfg.width:
+            raise ValueError(f"x rows need {cfg.width} elements, got {x.shape[1]}")
+    else:
+        n = 0 if x.numel() < cfg.width else (x.numel() - cfg.width) // cfg.x_stride + 1
+    if rows is None:
+        if n < cfg.rows(offsets is not None):
+            raise ValueError(f"x holds {n} rows, {cfg.rows(offsets is not None)} needed")
+    elif not 0 < cfg._struct.x_rows <= n:
+        c = _Fp4Config.from_buffer_copy(cfg._struct)
+        c.x_rows = n
+        return ctypes.byref(c)
+    return cfg._ref
+
+
+def _fp4_index(t, n, name):
+    if t is None:
+        return None
+    _need(t, torch.int32, name)
+    if t.numel() < n:
+        raise ValueError(f"{name} needs {n} entries, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _fp4_buffer(t, dtype, n, name):
+    _need(t, dtype, name)
+    if t.numel() < n:
+        raise ValueError(f"{name} needs {n} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def fp4_codes_bytes(cfg: Fp4Config, ragged=False) -> int:
+    n = _lib.b4_fp4_codes_bytes(cfg._ref, int(ragged))
+    if n == 0 and cfg.m:
+        raise B4Error(B4_ERR_INVALID_ARGUMENT, last_error())
+    return int(n)
+
+
+def fp4_scale_bytes(cfg: Fp4Config, ragged=False) -> int:
+    n = _lib.b4_fp4_scale_bytes(cfg._ref, int(ragged))
+    if n == 0 and cfg.m:
+        raise B4Error(B4_ERR_INVALID_ARGUMENT, last_error())
+    return int(n)
+
+
+def _fp4_gs_count(cfg, ragged):
+    return {GS_NONE: 0, GS_ROW: cfg.rows(ragged)}.get(cfg.gs_mode, cfg.num_groups)
+
+
+def fp4_empty(cfg: Fp4Config, device, ragged=False):
+    """Output buffers of ``fp4_quantize``: codes [.., ld], scales (tiles [.., k tiles, 32, 4, 4] or rows) and gs
+    ([groups, m] per row, [groups] otherwise, None for MXFP4)."""
+    g = 16 if cfg.format == NVFP4 else 32
+    lead = () if ragged else (cfg.num_groups,)
+    codes = torch.empty(*lead, cfg.m, cfg.ld, dtype=torch.uint8, device=device)
+    nbytes = fp4_scale_bytes(cfg, ragged)
+    if cfg.scale_layout == SCALES_ROWS:
+        scales = torch.empty(*lead, cfg.m, cfg.k // g, dtype=torch.uint8, device=device)
+    else:
+        kt = -(-cfg.k // (4 * g))
+        scales = torch.empty(*lead, nbytes // (512 * kt * (1 if ragged else cfg.num_groups)), kt, 32, 4, 4,
+                             dtype=torch.uint8, device=device)
+    gs = None
+    if cfg.gs_mode == GS_ROW:
+        gs = torch.empty(*lead, cfg.m, dtype=torch.float32, device=device)
+    elif cfg.gs_mode != GS_NONE:
+        gs = torch.empty(cfg.num_groups, dtype=torch.float32, device=device)
+    return codes, scales, gs
+
+
+def fp4_quantize(cfg: Fp4Config, x, codes, scales, gs=None, values=None, rows=None, offsets=None, stream=None):
+    """Enqueue the quantisation of x rows into ``codes``, ``scales`` and ``gs`` (an input with GS_GIVEN)."""
+    ragged = offsets is not None
+    ref = _fp4_x(cfg, x, rows, offsets)
+    n = cfg.rows(ragged)
+    _check(_lib.b4_fp4_quantize(
+        ref, x.data_ptr(), _fp4_index(rows, n, "rows"), _fp4_index(offsets, cfg.num_groups + 1, "offsets"),
+        None if gs is None else _fp4_buffer(gs, torch.float32, _fp4_gs_count(cfg, ragged), "gs"),
+        _fp4_buffer(codes, torch.uint8, n * cfg.ld, "codes"),
+        _fp4_buffer(scales, torch.uint8, fp4_scale_bytes(cfg, ragged), "scales"),
+        None if values is None else _fp4_buffer(values, cfg.x_dtype, n * cfg.k, "values"), _stream(stream)))
+
+
+def fp4_tile_scales(cfg: Fp4Config, src, dst=None, stream=None):
+    """Row-major scales [groups, m, k/g] of a checkpoint -> the tiles the product reads."""
+    g = 16 if cfg.format == NVFP4 else 32
+    need = fp4_scale_bytes(cfg) if cfg.scale_layout == SCALES_TILED else None
+    if need is None:
+        raise ValueError("fp4_tile_scales writes tiles: the config's scale_layout must be SCALES_TILED")
+    if dst is None:
+        kt = -(-cfg.k // (4 * g))
+        dst = torch.empty(cfg.num_groups, -(-cfg.m // 128), kt, 32, 4, 4, dtype=torch.uint8, device=src.device)
+    _check(_lib.b4_fp4_tile_scales(cfg._ref, _fp4_buffer(src, torch.uint8, cfg.rows(False) * (cfg.k // g), "src"),
+                                   _fp4_buffer(dst, torch.uint8, need, "dst"), _stream(stream)))
+    return dst
+
+
+def _fp4_weights(cfg, codes, scales, gs):
+    g = 64 if cfg.format == NVFP4 else 128
+    tiles = cfg.num_groups * -(-cfg.n // 128) * -(-cfg.k // g)
+    return (_fp4_buffer(codes, torch.uint8, cfg.num_groups * cfg.n * cfg.ld, "w_codes"),
+            _fp4_buffer(scales, torch.uint8, 512 * tiles, "w_scales"),
+            None if gs is None else _fp4_buffer(gs, torch.float32, cfg.num_groups, "w_gs"))
+
+
+def _fp4_out(cfg, out, rows):
+    if out.dtype != cfg.out_dtype:
+        raise TypeError(f"out must be {cfg.out_dtype}, got {out.dtype}")
+    if rows and (out.stride(-1) != 1 or (out.dim() == 2 and out.shape[0] > 1 and out.stride(0) != cfg.out_stride)
+                 or (out.dim() != 2 and not out.is_contiguous())):
+        raise ValueError("out rows must be contiguous and out_stride elements apart")
+    if out.dim() == 2:
+        ok = out.shape[0] >= rows and out.shape[1] >= cfg.n
+    else:
+        ok = rows == 0 or out.numel() >= (rows - 1) * cfg.out_stride + cfg.n
+    if not ok:
+        raise ValueError(f"out needs {rows} rows of {cfg.n} elements")
+    return out.data_ptr()
+
+
+def fp4_matmul(cfg: Fp4Config, a_codes, a_scales, a_gs, w_codes, w_scales, w_gs, out, offsets=None, out_rows=None,
+               device_status=None, stream=None):
+    """Enqueue the product of two quantised operands (``b4_fp4_matmul``)."""
+    ragged = offsets is not None
+    n = cfg.rows(ragged)
+    if device_status is not None:
+        _fp4_buffer(device_status, torch.int32, 2, "device_status")
+    _check(_lib.b4_fp4_matmul(
+        cfg._ref, _fp4_buffer(a_codes, torch.uint8, n * cfg.ld, "a_codes"),
+        _fp4_buffer(a_scales, torch.uint8, fp4_scale_bytes(cfg, ragged), "a_scales"),
+        None if a_gs is None else _fp4_buffer(a_gs, torch.float32, _fp4_gs_count(cfg, ragged), "a_gs"),
+        *_fp4_weights(cfg, w_codes, w_scales, w_gs), _fp4_index(offsets, cfg.num_groups + 1, "offsets"),
+        _fp4_index(out_rows, n, "out_rows"), _fp4_out(cfg, out, n), _ptr(device_status), _stream(stream)))
+
+
+def fp4_linear_workspace_bytes(cfg: Fp4Config) -> int:
+    n = _lib.b4_fp4_linear_workspace_bytes(cfg._ref)
+    if n == 0:
+        raise B4Error(B4_ERR_INVALID_ARGUMENT, last_error())
+    return int(n)
+
+
+def fp4_linear(cfg: Fp4Config, x, w_codes, w_scales, w_gs, out, workspace, x_gs=None, rows=None, offsets=None,
+               out_rows=None, stream=None):
+    """Enqueue quantisation of x and the product with the quantised weights: ``out`` [m, n].
+
+    With ``offsets`` [groups + 1] the rows are grouped by expert; ``rows`` gathers them from x (row i of the
+    operand is x row rows[i] // row_div) and ``out_rows`` scatters the result.
+    """
+    ref = _fp4_x(cfg, x, rows, offsets)
+    _need(workspace, torch.uint8, "workspace")
+    _check(_lib.b4_fp4_linear(
+        ref, x.data_ptr(), None if x_gs is None else _fp4_buffer(x_gs, torch.float32, cfg.num_groups, "x_gs"),
+        _fp4_index(rows, cfg.m, "rows"), _fp4_index(offsets, cfg.num_groups + 1, "offsets"),
+        *_fp4_weights(cfg, w_codes, w_scales, w_gs), _fp4_index(out_rows, cfg.m, "out_rows"),
+        _fp4_out(cfg, out, cfg.m), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+
+
+def fused_moe_a4_workspace_bytes(cfg: MoEConfig, activation: int) -> int:
+    c = cfg._c()
+    n = _lib.b4_fused_moe_a4_workspace_bytes(ctypes.byref(c), int(activation))
+    if n == 0:
+        raise B4Error(B4_ERR_INVALID_ARGUMENT, last_error())
+    return int(n)
+
+
+def fused_moe_a4(cfg: MoEConfig, x, w13, s13, gs13, w2, s2, gs2, topk_ids, topk_weights, activation, out, workspace,
+                 stream=None):
+    """The fused layer with 4-bit activations (``b4_fused_moe_a4``): weights as quantised operands
+    (``fp4_quantize``, or checkpoint codes with ``fp4_tile_scales``); ``out`` [m, H] bf16 is written in full."""
+    _need(x, torch.bfloat16, "x")
+    _need(out, torch.bfloat16, "out")
+    _need(topk_ids, torch.int32, "topk_ids")
+    _need(topk_weights, torch.float32, "topk_weights")
+    _need(workspace, torch.uint8, "workspace")
+    for t, n in ((w13, "w13"), (s13, "s13"), (w2, "w2"), (s2, "s2")):
+        _need(t, torch.uint8, n)
+    for t, n in ((gs13, "gs13"), (gs2, "gs2")):
+        if t is not None:
+            _need(t, torch.float32, n)
+    c = cfg._c()
+    _check(_lib.b4_fused_moe_a4(ctypes.byref(c), _ptr(x), _ptr(w13), _ptr(s13), _ptr(gs13), _ptr(w2), _ptr(s2),
+                                _ptr(gs2), _ptr(topk_ids), _ptr(topk_weights), int(activation), _ptr(out),
+                                _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 def fused_moe_raw(cfg: MoEConfig, ptrs: dict, activation: int, workspace_ptr: int, workspace_bytes_: int,

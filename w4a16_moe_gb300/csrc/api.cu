@@ -342,6 +342,15 @@ cudaError_t ensure_smem_limit(const void* func, size_t bytes) {
   return cudaSuccess;
 }
 
+// The current device's SM count, or the error of a device that is not sm_103
+// (for entry points defined in other translation units).
+b4_status require_device(int* sms) {
+  DevInfo info;
+  const b4_status st = device_info(info);
+  *sms = info.sms;
+  return st;
+}
+
 // Sets the message b4_last_error returns on this thread (for entry points
 // defined in other translation units).
 void set_last_error(const char* fmt, ...) {
