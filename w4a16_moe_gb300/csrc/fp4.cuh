@@ -33,6 +33,9 @@ __host__ __device__ constexpr int fp4_group(int fmt) { return fmt == 0 ? 16 : 32
 __host__ __device__ inline int64_t fp4_ld(int k) { return ((int64_t)k / 2 + 15) / 16 * 16; }
 __host__ __device__ inline int fp4_k_tiles(int k, int fmt) { return cdiv(k, 4 * fp4_group(fmt)); }
 
+// Rows of one activation box of a unit of up to nt rows.
+__host__ __device__ constexpr int fp4_box_rows(int nt) { return nt == 64 ? 32 : 64; }
+
 struct Fp4QuantParams {
   const void* x;
   int64_t x_stride;          // elements between rows
@@ -51,25 +54,26 @@ struct Fp4QuantParams {
   int k_tiles;
   void* values;              // dequantised rows in x's type, [row][K], or null
   int pad_rows;              // also clear the scales of each last row tile's missing rows
-  int vec;                   // x rows are 16-byte aligned
+  int vec;                   // alignment of x's rows: 2 32 bytes, 1 16 bytes, 0 less
+  int values_vec;            // of values: 2 or 1
   uint32_t* status;          // cleared (first kernel of a composite call), or null
 };
 
 struct Fp4GemmParams {
   CUtensorMap tmap_w;        // weight codes [E N][K/2] bytes, box 128 x 128 rows
-  CUtensorMap tmap_a;        // activation codes [rows][K/2] bytes, box 128 x box_rows
+  CUtensorMap tmap_a;        // activation codes [rows][K/2] bytes, box 128 x fp4_box_rows
   const uint8_t* w_scales;
   const uint8_t* a_scales;
   const float* w_gs;         // [E] or null
   const float* a_gs;         // [row] or [E] or null
   int a_gs_per_row;
-  int box_rows;
   int groups, m, n, k;       // m: rows per group (stack) or row capacity (ragged)
   const int32_t* offsets;    // ragged, or null
   const int32_t* out_rows;   // output row of each activation row, or null
   void* out;
   int64_t out_stride;        // elements
   int out_dtype;             // 0 bf16, 1 f16, 2 f32
+  int vec;                   // rows of out are 16-byte aligned and n fills them
   int a_is_new;              // the activation operand comes from the kernel before (programmatic launch)
   uint32_t* status;          // or null
 };

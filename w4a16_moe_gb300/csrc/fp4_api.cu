@@ -125,7 +125,8 @@ Fp4QuantParams quant_params(const b4_fp4_config* c, const void* x, const int32_t
   p.scales = scales;
   p.rowmajor_scales = c->scale_layout == B4_FP4_SCALES_ROWS;
   p.k_tiles = fp4_k_tiles(c->k, c->format);
-  p.vec = aligned(x, 16) && p.x_stride * dtype_bytes(c->x_dtype) % 16 == 0;
+  const int64_t pitch = p.x_stride * dtype_bytes(c->x_dtype);
+  p.vec = aligned(x, 32) && pitch % 32 == 0 ? 2 : aligned(x, 16) && pitch % 16 == 0 ? 1 : 0;
   return p;
 }
 
@@ -143,10 +144,10 @@ b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const u
   const bool ragged = offsets != nullptr;
   Fp4GemmParams p{};
   const int nt = unit_rows(c, ragged);
-  p.box_rows = nt == 64 ? 32 : 64;
   const uint64_t ld = (uint64_t)fp4_ld(c->k);
   if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k / 2, ld, 128) ||
-      !make_tmap_bytes_2d(&p.tmap_a, a_codes, (uint64_t)operand_rows(c, ragged), c->k / 2, ld, p.box_rows))
+      !make_tmap_bytes_2d(&p.tmap_a, a_codes, (uint64_t)operand_rows(c, ragged), c->k / 2, ld,
+                          fp4_box_rows(nt)))
     FP4_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
   p.w_scales = w_scales;
   p.a_scales = a_scales;
@@ -162,6 +163,8 @@ b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const u
   p.out = out;
   p.out_stride = c->out_stride ? c->out_stride : c->n;
   p.out_dtype = c->out_dtype;
+  const int per16 = 16 / dtype_bytes(c->out_dtype);
+  p.vec = aligned(out, 16) && p.out_stride % per16 == 0 && c->n % per16 == 0;
   p.a_is_new = a_is_new;
   p.status = status;
   // most units the call can have: each group ends at most one unit early
@@ -309,6 +312,7 @@ b4_status b4_fp4_quantize(const b4_fp4_config* cfg, const void* x, const int32_t
   if ((st = require_device(&sms)) != B4_OK) return st;
   Fp4QuantParams p = quant_params(cfg, x, rows, offsets, gs, codes, scales);
   p.values = values;
+  p.values_vec = aligned(values, 32) ? 2 : 1;
   p.pad_rows = !offsets && !p.rowmajor_scales;
   return cuda_status(launch_fp4_quantize(p, cfg->x_dtype, sms, true, reinterpret_cast<cudaStream_t>(stream)),
                      "fp4 quantise");

@@ -10,20 +10,23 @@
 //          of two costs E4M3 scales no precision and makes d exact, so ties are
 //          the true ties; per matrix: amax / (6 448).
 //
-// A thread holds 16 consecutive elements: one NVFP4 block, half an MXFP4 block
-// (the pair joins by one shuffle).  Threads of a row stand side by side, so
-// loads are 32-byte pieces of a contiguous stretch and code stores 8-byte
-// pieces; with a per-row global scale the row stays in registers between its
-// maximum and its codes (up to two chunks a thread; longer rows are read again,
-// from L1).  Every step is IEEE fp32 in the order of the formula; h / d is the
-// quotient corrected once by its fused-multiply-add residual (Markstein's
-// scheme: the reciprocal correctly rounded, then r = h - q d exactly, q + r / d),
-// which costs three operations an element where a division costs a dozen.
+// A thread holds chunks of 16 consecutive elements: an NVFP4 block, half an
+// MXFP4 block (the pair joins by one shuffle).  Threads of a row stand side by
+// side, so a chunk is one 32-byte load of a contiguous stretch (two of fp32) and
+// its codes one 8-byte store; a thread loads all of its chunks (four of 16-bit
+// rows, two otherwise) before it uses any, and keeps them between the row's
+// maximum and its codes (longer rows are read again, from L1).  Every step is
+// IEEE fp32 in the order of the formula; h / d is the quotient corrected once by
+// its fused-multiply-add residual (Markstein's scheme: q = h y with y the
+// correctly rounded reciprocal, r = h - q d exactly, q + r y), two elements an
+// instruction, where a division costs a dozen.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
+
+#include <cstring>
 
 #include "fp4.cuh"
 #include "ptx.cuh"
@@ -33,53 +36,152 @@ namespace b4 {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kCached = 2;  // chunks a thread keeps between the row's maximum and its codes
 
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* d, float v) { *d = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_f32(__half* d, float v) { *d = __float2half_rn(v); }
 __device__ __forceinline__ void from_f32(float* d, float v) { *d = v; }
 
-// 16 consecutive elements as fp32.
-template <typename T>
-__device__ __forceinline__ void load16(const T* src, bool vec, float (&h)[16]) {
-  T raw[16];
-  if (vec) {
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// N words (8 or 16) from or to consecutive global memory.  level 2: 32-byte
+// aligned, 1: 16-byte.
+template <int N>
+__device__ __forceinline__ void load_words(const void* src, int level, uint32_t (&w)[N]) {
+  if (level == 2) {
 #pragma unroll
-    for (int i = 0; i < (int)(16 * sizeof(T) / 16); ++i)
-      reinterpret_cast<uint4*>(raw)[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    for (int i = 0; i < N; i += 8)
+      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
+                     "=r"(w[i + 6]), "=r"(w[i + 7])
+                   : "l"(reinterpret_cast<const uint32_t*>(src) + i));
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) raw[i] = src[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) h[i] = to_f32(raw[i]);
-}
-
-// Chunk c of the row after the prologue.
-template <typename T, bool GATED>
-__device__ __forceinline__ void load_chunk(const Fp4QuantParams& p, const T* row, int c, float (&h)[16]) {
-  load16(row + 16 * c, p.vec, h);
-  if constexpr (GATED) {
-    float u[16];
-    load16(row + p.k + 16 * c, p.vec, u);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) h[i] = gated_act(h[i], u[i], p.glu);
-  } else if (p.act == 1) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) h[i] = h[i] < 0.f ? 0.f : h[i] * h[i];  // NaN stays NaN
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i / 4);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
   }
 }
+template <int N>
+__device__ __forceinline__ void store_words(void* dst, int level, const uint32_t (&w)[N]) {
+  if (level == 2) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+      asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]),
+                   "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7]),
+                   "l"(reinterpret_cast<uint32_t*>(dst) + i)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      reinterpret_cast<uint4*>(dst)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
+}
 
-// Bits of the largest magnitude; a NaN's bits exceed every number's, so it stays.
-__device__ __forceinline__ uint32_t amax_bits(const float (&h)[16]) {
+// 16 elements of a row as they are in memory.
+template <typename T>
+struct Raw {
+  static constexpr int kWords = 16 * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* src, int level) {
+    if (level) {
+      load_words(src, level, w);
+    } else {
+      T e[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) e[i] = src[i];
+      memcpy(w, e, sizeof(w));
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ float2 pair(int i) const;  // elements 2i, 2i + 1
+  // Bits of the largest magnitude as fp32; a NaN's bits exceed every number's, so it stays.
+  __device__ __forceinline__ uint32_t amax() const;
+};
+template <>
+__device__ __forceinline__ float2 Raw<__nv_bfloat16>::pair(int i) const {
+  return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 Raw<__half>::pair(int i) const {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+}
+template <>
+__device__ __forceinline__ float2 Raw<float>::pair(int i) const {
+  return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+}
+__device__ __forceinline__ uint32_t amax16x2(const uint32_t (&w)[8]) {
+  uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+  return max(m >> 16, m & 0xffffu);
+}
+template <>
+__device__ __forceinline__ uint32_t Raw<__nv_bfloat16>::amax() const {
+  return amax16x2(w) << 16;
+}
+template <>
+__device__ __forceinline__ uint32_t Raw<__half>::amax() const {
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)amax16x2(w))));
+}
+template <>
+__device__ __forceinline__ uint32_t Raw<float>::amax() const {
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
+  for (int i = 0; i < 16; ++i) a = max(a, w[i] & 0x7fffffffu);
   return a;
 }
+
+// Chunk c of a row: as it is, or through the activation in fp32.
+template <typename T, bool ACT>
+struct Chunk : Raw<T> {
+  __device__ __forceinline__ void get(const Fp4QuantParams& p, const T* row, int c) { this->load(row + 16 * c, p.vec); }
+};
+template <typename T>
+struct Chunk<T, true> : Raw<float> {
+  __device__ __forceinline__ void get(const Fp4QuantParams& p, const T* row, int c) {
+    Raw<T> g, u;
+    g.load(row + 16 * c, p.vec);
+    if (p.act == 0) {
+      u.load(row + p.k + 16 * c, p.vec);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 a = g.pair(i), b = u.pair(i);
+        this->w[2 * i] = __float_as_uint(gated_act(a.x, b.x, p.glu));
+        this->w[2 * i + 1] = __float_as_uint(gated_act(a.y, b.y, p.glu));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // NaN stays NaN
+        const float2 a = g.pair(i);
+        this->w[2 * i] = __float_as_uint(a.x < 0.f ? 0.f : a.x * a.x);
+        this->w[2 * i + 1] = __float_as_uint(a.y < 0.f ? 0.f : a.y * a.y);
+      }
+    }
+  }
+};
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 
@@ -92,16 +194,34 @@ __device__ __forceinline__ float row_gs(uint32_t a) {
   return __uint_as_float((uint32_t)(max(j, -126) + 127) << 23);
 }
 
+// Quotient a / b of a >= 0 by b within [2^-80, 2^100], y = 1 / b correctly rounded.
+__device__ __forceinline__ float corrected_quotient(float a, float b, float y) {
+  const float q = a * y;
+  return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+}
+
+// 6 gs and its reciprocal, for the block scales of a row.
+struct RowScale {
+  float gs, six, inv;
+  bool safe;
+  __device__ __forceinline__ explicit RowScale(float g) : gs(g) {
+    six = __fmul_rn(6.f, g);
+    safe = six >= 0x1p-80f && six <= 0x1p100f;
+    inv = safe ? __frcp_rn(six) : 0.f;
+  }
+};
+
 struct BlockScale {
   uint32_t code;  // the scale's byte
   float d, inv;   // step of the codes and its reciprocal
   int kind;       // 0: all codes zero, 1: corrected reciprocal, 2: true division
 };
 
-__device__ __forceinline__ BlockScale block_scale(int fmt, uint32_t a, float gs) {
+template <int FMT>
+__device__ __forceinline__ BlockScale block_scale(uint32_t a, const RowScale& r) {
   BlockScale b;
   const float amax = __uint_as_float(a);
-  if (fmt != 0) {
+  if constexpr (FMT != 0) {
     const int e = a > kInfBits ? 255
                   : a == kInfBits ? 254
                                   : max((int)(a >> 23) - 2 + ((a & 0x7fffffu) > 0x400000u), 0);
@@ -111,14 +231,13 @@ __device__ __forceinline__ BlockScale block_scale(int fmt, uint32_t a, float gs)
     b.kind = e == 255 ? 0 : 1;
     return b;
   }
-  const float ratio = __fdiv_rn(amax, __fmul_rn(6.f, gs));
+  const float ratio = r.safe && amax * r.inv < 0x1p20f ? corrected_quotient(amax, r.six, r.inv) : __fdiv_rn(amax, r.six);
   b.code = ratio != ratio ? 0x7fu : (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b.code, __NV_E4M3)));
-  b.d = __fmul_rn(s, gs);
-  if (!(b.d > 0.f) || a > kInfBits) {
-    b.kind = 0;
-    b.inv = 0.f;
-  } else {
+  b.d = __fmul_rn(s, r.gs);
+  b.inv = 0.f;
+  b.kind = 0;
+  if (b.d > 0.f && a <= kInfBits) {
     b.inv = __frcp_rn(b.d);
     // the residual is exact while no product leaves the normal range
     b.kind = b.d >= 0x1p-100f && b.d <= 0x1p100f && amax * b.inv < 0x1p20f ? 1 : 2;
@@ -126,29 +245,42 @@ __device__ __forceinline__ BlockScale block_scale(int fmt, uint32_t a, float gs)
   return b;
 }
 
-// E2M1 codes of 16 elements, element 2j in the low nibble of byte j.
-__device__ __forceinline__ uint2 encode(int fmt, const float (&h)[16], const BlockScale& b) {
+// Eight fp32 values as E2M1 codes, the first in the low nibble of byte 0.
+__device__ __forceinline__ uint32_t e2m1x8(float2 a, float2 b, float2 c, float2 d) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\t"
+      "mov.b32 %0, {p, q, r, s};\n\t}"
+      : "=r"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+  return r;
+}
+
+// E2M1 codes of a chunk, element 2j in the low nibble of byte j.
+template <int FMT, typename C>
+__device__ __forceinline__ uint2 encode(const C& h, const BlockScale& b) {
   if (b.kind == 0) return make_uint2(0, 0);
   uint32_t w[2];
+  const uint64_t inv = pack2(b.inv, b.inv), nd = pack2(-b.d, -b.d);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    uint32_t v = 0;
+    float2 q[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float q[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float x = h[8 * half + 2 * j + i];
-        if (b.kind == 2) {
-          q[i] = __fdiv_rn(x, b.d);
-        } else {
-          q[i] = x * b.inv;  // MXFP4: exact, a power of two
-          if (fmt == 0) q[i] = __fmaf_rn(__fmaf_rn(-q[i], b.d, x), b.inv, q[i]);
-        }
+      const float2 x = h.pair(4 * half + j);
+      if (FMT == 0 && b.kind == 2) {
+        q[j] = make_float2(__fdiv_rn(x.x, b.d), __fdiv_rn(x.y, b.d));
+      } else {
+        const uint64_t xx = pack2(x.x, x.y);
+        uint64_t r = mul2(xx, inv);  // MXFP4: exact, a power of two
+        if (FMT == 0) r = fma2(fma2(r, nd, xx), inv, r);
+        q[j] = unpack2(r);
       }
-      v |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(q[0], q[1]), __NV_E2M1, cudaRoundNearest) << (8 * j);
     }
-    w[half] = v;
+    w[half] = e2m1x8(q[0], q[1], q[2], q[3]);
   }
   return make_uint2(w[0], w[1]);
 }
@@ -165,28 +297,37 @@ __device__ __forceinline__ int find_group(const int32_t* offsets, int groups, in
   return min(coarse * step + fine, groups - 1);
 }
 
+// What codes of step d stand for, in x's type (NaN under a NaN scale).
 template <typename T>
-__device__ __forceinline__ void store_values(T* dst, const uint2& w, float d, uint32_t code_nan) {
-  T raw[16];
+__device__ __forceinline__ void store_values(T* dst, int level, const uint2& w, float d, bool is_nan) {
+  T e[16];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint32_t byte = ((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 0xffu;
     const float2 v = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1)));
-    from_f32(&raw[2 * j], code_nan ? __uint_as_float(0x7fffffffu) : __fmul_rn(v.x, d));
-    from_f32(&raw[2 * j + 1], code_nan ? __uint_as_float(0x7fffffffu) : __fmul_rn(v.y, d));
+    from_f32(&e[2 * j], is_nan ? __uint_as_float(0x7fffffffu) : __fmul_rn(v.x, d));
+    from_f32(&e[2 * j + 1], is_nan ? __uint_as_float(0x7fffffffu) : __fmul_rn(v.y, d));
   }
-#pragma unroll
-  for (int i = 0; i < (int)(16 * sizeof(T) / 16); ++i)
-    reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(raw)[i];
+  uint32_t o[16 * sizeof(T) / 4];
+  memcpy(o, e, sizeof(o));
+  store_words(dst, level, o);
+}
+
+// Chunks a thread keeps.
+template <typename T, bool ACT>
+__host__ __device__ constexpr int cached_chunks() {
+  return !ACT && sizeof(T) == 2 ? 4 : 2;
 }
 
 }  // namespace
 
 // tpr_log2: threads per row.  Rows beyond the operand (pad_rows) only clear
 // their scales.
-template <typename T, bool GATED, bool ROW>
+template <typename T, int FMT, bool ACT, bool ROW>
 __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const __grid_constant__ Fp4QuantParams p,
                                                                  int tpr_log2) {
+  constexpr int kCached = cached_chunks<T, ACT>();
+  constexpr int kPerTile = FMT == 0 ? 4 : 8;  // chunks of a scale tile
   __shared__ uint32_t s_max[kQThreads / 32];
   const int tpr = 1 << tpr_log2;
   const int t = threadIdx.x & (tpr - 1);
@@ -210,9 +351,14 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const __grid_co
     tile = (int64_t)(first / 128) + group + lr / 128;
     live = vrow < total && first >= 0 && lr >= 0 && tile < (int64_t)p.m / 128 + p.groups;
   } else {
-    const int64_t per = p.pad_rows ? (int64_t)tiles_per * 128 : p.m;
-    group = (int)(vrow / per);
-    lr = (int)(vrow - group * per);
+    const int per = p.pad_rows ? tiles_per * 128 : p.m;
+    if (p.groups == 1) {
+      lr = (int)vrow;
+      group = vrow < per ? 0 : 1;
+    } else {
+      group = (int)(vrow / per);
+      lr = (int)(vrow - (int64_t)group * per);
+    }
     live = group < p.groups && lr < p.m;
     pad = group < p.groups && lr >= p.m;
     row = (int64_t)group * p.m + lr;
@@ -227,29 +373,27 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const __grid_co
   }
   const T* x = reinterpret_cast<const T*>(p.x) + (zero ? 0 : src * p.x_stride);
   const int chunks = live ? p.k / 16 : 0;
-  const int per_tile = p.fmt == 0 ? 4 : 8;  // chunks of a scale tile
-  const int n_it = cdiv(p.k_tiles * per_tile, tpr);
+  const int filled = zero ? 0 : chunks;  // chunks with anything to read
+  const int n_it = cdiv(p.k_tiles * kPerTile, tpr);
 
-  float h[ROW ? kCached : 1][16];
+  Chunk<T, ACT> h[kCached];
+#pragma unroll
+  for (int it = 0; it < kCached; ++it) {
+    const int c = it * tpr + t;
+    if (c < filled) h[it].get(p, x, c);
+    else h[it].zero();
+  }
   float gs = 1.f;
   if constexpr (ROW) {
     uint32_t a = 0;
 #pragma unroll
-    for (int it = 0; it < kCached; ++it) {
-      const int c = it * tpr + t;
-      if (c < chunks && !zero) load_chunk<T, GATED>(p, x, c, h[it]);
-      else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) h[it][i] = 0.f;
-      }
-      a = max(a, amax_bits(h[it]));
-    }
+    for (int it = 0; it < kCached; ++it) a = max(a, h[it].amax());
     for (int it = kCached; it < n_it; ++it) {
       const int c = it * tpr + t;
-      if (c < chunks && !zero) {
-        float v[16];
-        load_chunk<T, GATED>(p, x, c, v);
-        a = max(a, amax_bits(v));
+      if (c < filled) {
+        Chunk<T, ACT> v;
+        v.get(p, x, c);
+        a = max(a, v.amax());
       }
     }
     for (int o = min(tpr, 32) / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -261,54 +405,48 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const __grid_co
     }
     gs = row_gs(a);
     if (live && t == 0) p.gs[row] = gs;
-  } else if (p.gs_mode != kGsNone && live) {
+  } else if (FMT == 0 && live) {
     gs = __ldg(p.gs + group);
   }
+  const RowScale rs(gs);
 
-  auto emit = [&](int c, const float(&v)[16]) {
-    uint32_t a = amax_bits(v);
-    if (p.fmt != 0) a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  auto emit = [&](int c, const Chunk<T, ACT>& v) {
+    uint32_t a = v.amax();
+    if (FMT != 0) a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
     const bool in = c < chunks;
-    BlockScale b = block_scale(p.fmt, a, gs);
+    BlockScale b = block_scale<FMT>(a, rs);
     if (!in) b.code = 0;
     if (in) {
-      const uint2 w = encode(p.fmt, v, b);
+      const uint2 w = encode<FMT>(v, b);
       *reinterpret_cast<uint2*>(p.codes + row * p.ld + 8 * (int64_t)c) = w;
       if (p.values)
-        store_values(reinterpret_cast<T*>(p.values) + row * p.k + 16 * (int64_t)c, w, b.d,
-                     p.fmt == 0 ? b.code == 0x7fu : b.code == 255u);
+        store_values(reinterpret_cast<T*>(p.values) + row * p.k + 16 * (int64_t)c, p.values_vec, w, b.d,
+                     b.code == (FMT == 0 ? 0x7fu : 255u));
     }
     if (p.rowmajor_scales) {
-      if (in && (p.fmt == 0 || !(c & 1))) {
-        const int nb = p.k / fp4_group(p.fmt);
-        p.scales[row * nb + (p.fmt == 0 ? c : c >> 1)] = (uint8_t)b.code;
-      }
+      if (in && (FMT == 0 || !(c & 1)))
+        p.scales[row * (p.k / (FMT == 0 ? 16 : 32)) + (FMT == 0 ? c : c >> 1)] = (uint8_t)b.code;
     } else {
       // the four scales of a tile row gather into one word
-      const int pos = p.fmt == 0 ? c & 3 : (c >> 1) & 3;
+      const int pos = FMT == 0 ? c & 3 : (c >> 1) & 3;
       uint32_t w = b.code << (8 * pos);
-      if (p.fmt == 0) w |= __shfl_xor_sync(0xffffffffu, w, 1);
+      if (FMT == 0) w |= __shfl_xor_sync(0xffffffffu, w, 1);
       w |= __shfl_xor_sync(0xffffffffu, w, 2);
-      if (p.fmt != 0) w |= __shfl_xor_sync(0xffffffffu, w, 4);
-      const int kt = c / per_tile;
-      if ((c & (per_tile - 1)) == 0 && kt < p.k_tiles && (live || pad))
+      if (FMT != 0) w |= __shfl_xor_sync(0xffffffffu, w, 4);
+      const int kt = c / kPerTile;
+      if ((c & (kPerTile - 1)) == 0 && kt < p.k_tiles && (live || pad))
         *reinterpret_cast<uint32_t*>(p.scales + (tile * p.k_tiles + kt) * kSfTile + (lr & 31) * 16 +
                                      ((lr >> 5) & 3) * 4) = w;
     }
   };
-  if constexpr (ROW) {
 #pragma unroll
-    for (int it = 0; it < kCached; ++it)
-      if (it < n_it) emit(it * tpr + t, h[it]);
-  }
-  for (int it = ROW ? kCached : 0; it < n_it; ++it) {
+  for (int it = 0; it < kCached; ++it)
+    if (it < n_it) emit(it * tpr + t, h[it]);
+  for (int it = kCached; it < n_it; ++it) {
     const int c = it * tpr + t;
-    float v[16];
-    if (c < chunks && !zero) load_chunk<T, GATED>(p, x, c, v);
-    else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    }
+    Chunk<T, ACT> v;
+    if (c < filled) v.get(p, x, c);
+    else v.zero();
     emit(c, v);
   }
 }
@@ -316,7 +454,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const __grid_co
 // ------------------------------------------- one global scale per matrix
 // Largest magnitude of each matrix of a stack, as fp32 bits (order of the
 // atomics does not matter to a maximum), then amax / (6 448) in place.
-template <typename T, bool GATED>
+template <typename T, bool ACT>
 __global__ void __launch_bounds__(kQThreads) fp4_amax_kernel(const __grid_constant__ Fp4QuantParams p) {
   __shared__ uint32_t s_max[kQThreads / 32];
   const int group = blockIdx.y;
@@ -325,10 +463,9 @@ __global__ void __launch_bounds__(kQThreads) fp4_amax_kernel(const __grid_consta
   uint32_t a = 0;
   for (int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kQThreads) {
     const int64_t r = i / per_row;
-    float h[16];
-    load_chunk<T, GATED>(p, reinterpret_cast<const T*>(p.x) + ((int64_t)group * p.m + r) * p.x_stride,
-                         (int)(i - r * per_row), h);
-    a = max(a, amax_bits(h));
+    Chunk<T, ACT> h;
+    h.get(p, reinterpret_cast<const T*>(p.x) + ((int64_t)group * p.m + r) * p.x_stride, (int)(i - r * per_row));
+    a = max(a, h.amax());
   }
   for (int o = 16; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = a;
@@ -427,14 +564,18 @@ cudaError_t launch_pdl(K kern, dim3 grid, dim3 block, size_t smem, bool pdl, cud
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <typename T, bool GATED>
+template <typename T, int FMT, bool ACT>
 cudaError_t quantize_t(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStream_t stream) {
-  // threads per row: two chunks each, at least a warp for ragged rows (their
-  // group is found by the whole warp) and eight for a scale word
-  const int slots = p.k_tiles * (p.fmt == 0 ? 4 : 8);
-  int lg = p.offsets ? 5 : 3;
-  while ((1 << lg) < kQThreads && (1 << lg) * 2 < slots) ++lg;
+  // Threads per row: as many as it takes for a thread to hold its share, and
+  // while all rows together do not fill the GPU once, down to one chunk each;
+  // at least a warp for ragged rows (the whole warp finds their group) and
+  // eight for a scale word.
+  const int slots = p.k_tiles * (FMT == 0 ? 4 : 8);
   const int64_t rows = p.offsets ? p.m : (int64_t)p.groups * (p.pad_rows ? cdiv(p.m, 128) * 128 : p.m);
+  const int64_t live = p.offsets ? p.m : (int64_t)p.groups * p.m;
+  const int share = live * slots <= (int64_t)num_sms * 2048 ? 1 : cached_chunks<T, ACT>();
+  int lg = p.offsets ? 5 : 3;
+  while ((1 << lg) < kQThreads && (1 << lg) * share < slots) ++lg;
   const int64_t grid = (rows + (kQThreads >> lg) - 1) / (kQThreads >> lg);
   if (p.gs_mode == kGsTensor) {
     cudaError_t e = cudaMemsetAsync(p.gs, 0, sizeof(float) * p.groups, stream);
@@ -443,26 +584,32 @@ cudaError_t quantize_t(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStrea
     int gx = (8 * num_sms + p.groups - 1) / p.groups;
     if (gx > work) gx = (int)work;
     if (gx < 1) gx = 1;
-    e = launch_pdl(fp4_amax_kernel<T, GATED>, dim3(gx, p.groups), dim3(kQThreads), 0, false, stream, p);
+    e = launch_pdl(fp4_amax_kernel<T, ACT>, dim3(gx, p.groups), dim3(kQThreads), 0, false, stream, p);
     if (e != cudaSuccess) return e;
     e = launch_pdl(fp4_gs_kernel, dim3(cdiv(p.groups, 256)), dim3(256), 0, false, stream, p.gs, p.groups);
     if (e != cudaSuccess) return e;
   }
-  if (p.gs_mode == kGsRow)
-    return launch_pdl(fp4_quantize_kernel<T, GATED, true>, dim3((unsigned)grid), dim3(kQThreads), 0, pdl, stream, p, lg);
-  return launch_pdl(fp4_quantize_kernel<T, GATED, false>, dim3((unsigned)grid), dim3(kQThreads), 0, pdl, stream, p, lg);
+  if constexpr (FMT == 0)
+    if (p.gs_mode == kGsRow)
+      return launch_pdl(fp4_quantize_kernel<T, FMT, ACT, true>, dim3((unsigned)grid), dim3(kQThreads), 0, pdl, stream, p,
+                        lg);
+  return launch_pdl(fp4_quantize_kernel<T, FMT, ACT, false>, dim3((unsigned)grid), dim3(kQThreads), 0, pdl, stream, p,
+                    lg);
+}
+
+template <typename T>
+cudaError_t quantize_fmt(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStream_t stream) {
+  if (p.act < 0)
+    return p.fmt == 0 ? quantize_t<T, 0, false>(p, num_sms, pdl, stream) : quantize_t<T, 1, false>(p, num_sms, pdl, stream);
+  return p.fmt == 0 ? quantize_t<T, 0, true>(p, num_sms, pdl, stream) : quantize_t<T, 1, true>(p, num_sms, pdl, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_quantize(const Fp4QuantParams& p, int dtype, int num_sms, bool pdl, cudaStream_t stream) {
-  const bool gated = p.act == 0;
-  if (dtype == 0)
-    return gated ? quantize_t<__nv_bfloat16, true>(p, num_sms, pdl, stream)
-                 : quantize_t<__nv_bfloat16, false>(p, num_sms, pdl, stream);
-  if (dtype == 1)
-    return gated ? quantize_t<__half, true>(p, num_sms, pdl, stream) : quantize_t<__half, false>(p, num_sms, pdl, stream);
-  return gated ? quantize_t<float, true>(p, num_sms, pdl, stream) : quantize_t<float, false>(p, num_sms, pdl, stream);
+  if (dtype == 0) return quantize_fmt<__nv_bfloat16>(p, num_sms, pdl, stream);
+  if (dtype == 1) return quantize_fmt<__half>(p, num_sms, pdl, stream);
+  return quantize_fmt<float>(p, num_sms, pdl, stream);
 }
 
 cudaError_t launch_fp4_tile_scales(const uint8_t* src, uint8_t* dst, int groups, int m, int blocks, int k_tiles,
