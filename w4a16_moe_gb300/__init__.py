@@ -231,6 +231,20 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+# torch's handle of a device's current stream without building a Stream object (2 - 3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, t):
+    """Handle of ``stream``, or of the current stream of the tensor's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+    return _stream(None) if _raw_stream is None else _raw_stream(device.index)
+
+
 def route_capacity_tokens(m: int) -> int:
     return int(_lib.b4_route_capacity_tokens(int(m)))
 
@@ -386,27 +400,46 @@ class Fp4Config:
                                   -1 if activation is None else activation, gs_mode, scale_layout, int(row_div),
                                   int(x_rows), *swiglu, int(x_stride), int(out_stride))
         self._ref = ctypes.byref(self._struct)
+        self._sizes = {}
 
     def rows(self, ragged):
         return self.m if ragged else self.m * self.num_groups
 
+    def _operand(self, ragged):
+        """(rows, code bytes, scale bytes, global scales) of the quantised operand."""
+        s = self._sizes.get(ragged)
+        if s is None:
+            n = self.rows(ragged)
+            gs = {GS_NONE: 0, GS_ROW: n}.get(self.gs_mode, self.num_groups)
+            s = self._sizes[ragged] = (n, n * self.ld, fp4_scale_bytes(self, ragged), gs)
+        return s
 
-def _fp4_x(cfg, x, rows, offsets):
+    def _weight_sizes(self):
+        """(code bytes, scale bytes) of the weights."""
+        s = self._sizes.get("w")
+        if s is None:
+            tiles = self.num_groups * -(-self.n // 128) * -(-self.k // (64 if self.format == NVFP4 else 128))
+            s = self._sizes["w"] = (self.num_groups * self.n * self.ld, 512 * tiles)
+        return s
+
+
+def _fp4_x(cfg, x, rows, ragged):
     """x as the config describes it: a 2-D view of rows, or any contiguous shape with that many elements.
     Returns the call's config: with gathered rows, bounded by the rows x holds."""
-    if x.dtype != cfg.x_dtype:
+    if x.dtype is not cfg.x_dtype:
         raise TypeError(f"x must be {cfg.x_dtype}, got {x.dtype}")
-    if not x.is_contiguous():
+    if x.is_contiguous():
+        have = x.numel()
+        n = 0 if have < cfg.width else (have - cfg.width) // cfg.x_stride + 1
+    else:
         if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) != cfg.x_stride:
             raise ValueError("x must be contiguous, or two-dimensional with rows x_stride elements apart")
         n = x.shape[0]
         if x.shape[1] < cfg.width:
             raise ValueError(f"x rows need {cfg.width} elements, got {x.shape[1]}")
-    else:
-        n = 0 if x.numel() < cfg.width else (x.numel() - cfg.width) // cfg.x_stride + 1
     if rows is None:
-        if n < cfg.rows(offsets is not None):
-            raise ValueError(f"x holds {n} rows, {cfg.rows(offsets is not None)} needed")
+        if n < cfg.rows(ragged):
+            raise ValueError(f"x holds {n} rows, {cfg.rows(ragged)} needed")
     elif not 0 < cfg._struct.x_rows <= n:
         c = _Fp4Config.from_buffer_copy(cfg._struct)
         c.x_rows = n
@@ -414,20 +447,14 @@ def _fp4_x(cfg, x, rows, offsets):
     return cfg._ref
 
 
-def _fp4_index(t, n, name):
+def _fp4_buffer(t, dtype, n, name):
+    """Address of a contiguous tensor of at least n elements (None stays None)."""
     if t is None:
         return None
-    _need(t, torch.int32, name)
-    if t.numel() < n:
-        raise ValueError(f"{name} needs {n} entries, got {t.numel()}")
-    return t.data_ptr()
-
-
-def _fp4_buffer(t, dtype, n, name):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
     _need(t, dtype, name)
-    if t.numel() < n:
-        raise ValueError(f"{name} needs {n} elements, got {t.numel()}")
-    return t.data_ptr()
+    raise ValueError(f"{name} needs {n} elements, got {t.numel()}")
 
 
 def fp4_codes_bytes(cfg: Fp4Config, ragged=False) -> int:
@@ -442,10 +469,6 @@ def fp4_scale_bytes(cfg: Fp4Config, ragged=False) -> int:
     if n == 0 and cfg.m:
         raise B4Error(B4_ERR_INVALID_ARGUMENT, last_error())
     return int(n)
-
-
-def _fp4_gs_count(cfg, ragged):
-    return {GS_NONE: 0, GS_ROW: cfg.rows(ragged)}.get(cfg.gs_mode, cfg.num_groups)
 
 
 def fp4_empty(cfg: Fp4Config, device, ragged=False):
@@ -472,22 +495,22 @@ def fp4_empty(cfg: Fp4Config, device, ragged=False):
 def fp4_quantize(cfg: Fp4Config, x, codes, scales, gs=None, values=None, rows=None, offsets=None, stream=None):
     """Enqueue the quantisation of x rows into ``codes``, ``scales`` and ``gs`` (an input with GS_GIVEN)."""
     ragged = offsets is not None
-    ref = _fp4_x(cfg, x, rows, offsets)
-    n = cfg.rows(ragged)
-    _check(_lib.b4_fp4_quantize(
-        ref, x.data_ptr(), _fp4_index(rows, n, "rows"), _fp4_index(offsets, cfg.num_groups + 1, "offsets"),
-        None if gs is None else _fp4_buffer(gs, torch.float32, _fp4_gs_count(cfg, ragged), "gs"),
-        _fp4_buffer(codes, torch.uint8, n * cfg.ld, "codes"),
-        _fp4_buffer(scales, torch.uint8, fp4_scale_bytes(cfg, ragged), "scales"),
-        None if values is None else _fp4_buffer(values, cfg.x_dtype, n * cfg.k, "values"), _stream(stream)))
+    n, code_bytes, scale_bytes, gs_n = cfg._operand(ragged)
+    st = _lib.b4_fp4_quantize(
+        _fp4_x(cfg, x, rows, ragged), x.data_ptr(), _fp4_buffer(rows, torch.int32, n, "rows"),
+        _fp4_buffer(offsets, torch.int32, cfg.num_groups + 1, "offsets"), _fp4_buffer(gs, torch.float32, gs_n, "gs"),
+        _fp4_buffer(codes, torch.uint8, code_bytes, "codes"), _fp4_buffer(scales, torch.uint8, scale_bytes, "scales"),
+        _fp4_buffer(values, cfg.x_dtype, n * cfg.k, "values"), _stream_of(stream, x))
+    if st:
+        _check(st)
 
 
 def fp4_tile_scales(cfg: Fp4Config, src, dst=None, stream=None):
     """Row-major scales [groups, m, k/g] of a checkpoint -> the tiles the product reads."""
     g = 16 if cfg.format == NVFP4 else 32
-    need = fp4_scale_bytes(cfg) if cfg.scale_layout == SCALES_TILED else None
-    if need is None:
+    if cfg.scale_layout != SCALES_TILED:
         raise ValueError("fp4_tile_scales writes tiles: the config's scale_layout must be SCALES_TILED")
+    need = fp4_scale_bytes(cfg)
     if dst is None:
         kt = -(-cfg.k // (4 * g))
         dst = torch.empty(cfg.num_groups, -(-cfg.m // 128), kt, 32, 4, 4, dtype=torch.uint8, device=src.device)
@@ -496,23 +519,17 @@ def fp4_tile_scales(cfg: Fp4Config, src, dst=None, stream=None):
     return dst
 
 
-def _fp4_weights(cfg, codes, scales, gs):
-    g = 64 if cfg.format == NVFP4 else 128
-    tiles = cfg.num_groups * -(-cfg.n // 128) * -(-cfg.k // g)
-    return (_fp4_buffer(codes, torch.uint8, cfg.num_groups * cfg.n * cfg.ld, "w_codes"),
-            _fp4_buffer(scales, torch.uint8, 512 * tiles, "w_scales"),
-            None if gs is None else _fp4_buffer(gs, torch.float32, cfg.num_groups, "w_gs"))
-
-
 def _fp4_out(cfg, out, rows):
-    if out.dtype != cfg.out_dtype:
+    if out.dtype is not cfg.out_dtype:
         raise TypeError(f"out must be {cfg.out_dtype}, got {out.dtype}")
-    if rows and (out.stride(-1) != 1 or (out.dim() == 2 and out.shape[0] > 1 and out.stride(0) != cfg.out_stride)
-                 or (out.dim() != 2 and not out.is_contiguous())):
-        raise ValueError("out rows must be contiguous and out_stride elements apart")
-    if out.dim() == 2:
-        ok = out.shape[0] >= rows and out.shape[1] >= cfg.n
+    shape = out.shape
+    if len(shape) == 2:
+        if rows and (out.stride(1) != 1 or (shape[0] > 1 and out.stride(0) != cfg.out_stride)):
+            raise ValueError("out rows must be contiguous and out_stride elements apart")
+        ok = shape[0] >= rows and shape[1] >= cfg.n
     else:
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous, or two-dimensional with rows out_stride elements apart")
         ok = rows == 0 or out.numel() >= (rows - 1) * cfg.out_stride + cfg.n
     if not ok:
         raise ValueError(f"out needs {rows} rows of {cfg.n} elements")
@@ -522,16 +539,18 @@ def _fp4_out(cfg, out, rows):
 def fp4_matmul(cfg: Fp4Config, a_codes, a_scales, a_gs, w_codes, w_scales, w_gs, out, offsets=None, out_rows=None,
                device_status=None, stream=None):
     """Enqueue the product of two quantised operands (``b4_fp4_matmul``)."""
-    ragged = offsets is not None
-    n = cfg.rows(ragged)
-    if device_status is not None:
-        _fp4_buffer(device_status, torch.int32, 2, "device_status")
-    _check(_lib.b4_fp4_matmul(
-        cfg._ref, _fp4_buffer(a_codes, torch.uint8, n * cfg.ld, "a_codes"),
-        _fp4_buffer(a_scales, torch.uint8, fp4_scale_bytes(cfg, ragged), "a_scales"),
-        None if a_gs is None else _fp4_buffer(a_gs, torch.float32, _fp4_gs_count(cfg, ragged), "a_gs"),
-        *_fp4_weights(cfg, w_codes, w_scales, w_gs), _fp4_index(offsets, cfg.num_groups + 1, "offsets"),
-        _fp4_index(out_rows, n, "out_rows"), _fp4_out(cfg, out, n), _ptr(device_status), _stream(stream)))
+    n, code_bytes, scale_bytes, gs_n = cfg._operand(offsets is not None)
+    w_bytes, ws_bytes = cfg._weight_sizes()
+    st = _lib.b4_fp4_matmul(
+        cfg._ref, _fp4_buffer(a_codes, torch.uint8, code_bytes, "a_codes"),
+        _fp4_buffer(a_scales, torch.uint8, scale_bytes, "a_scales"), _fp4_buffer(a_gs, torch.float32, gs_n, "a_gs"),
+        _fp4_buffer(w_codes, torch.uint8, w_bytes, "w_codes"), _fp4_buffer(w_scales, torch.uint8, ws_bytes, "w_scales"),
+        _fp4_buffer(w_gs, torch.float32, cfg.num_groups, "w_gs"),
+        _fp4_buffer(offsets, torch.int32, cfg.num_groups + 1, "offsets"),
+        _fp4_buffer(out_rows, torch.int32, n, "out_rows"), _fp4_out(cfg, out, n),
+        _fp4_buffer(device_status, torch.int32, 2, "device_status"), _stream_of(stream, a_codes))
+    if st:
+        _check(st)
 
 
 def fp4_linear_workspace_bytes(cfg: Fp4Config) -> int:
@@ -548,13 +567,17 @@ def fp4_linear(cfg: Fp4Config, x, w_codes, w_scales, w_gs, out, workspace, x_gs=
     With ``offsets`` [groups + 1] the rows are grouped by expert; ``rows`` gathers them from x (row i of the
     operand is x row rows[i] // row_div) and ``out_rows`` scatters the result.
     """
-    ref = _fp4_x(cfg, x, rows, offsets)
-    _need(workspace, torch.uint8, "workspace")
-    _check(_lib.b4_fp4_linear(
-        ref, x.data_ptr(), None if x_gs is None else _fp4_buffer(x_gs, torch.float32, cfg.num_groups, "x_gs"),
-        _fp4_index(rows, cfg.m, "rows"), _fp4_index(offsets, cfg.num_groups + 1, "offsets"),
-        *_fp4_weights(cfg, w_codes, w_scales, w_gs), _fp4_index(out_rows, cfg.m, "out_rows"),
-        _fp4_out(cfg, out, cfg.m), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    m = cfg.m
+    w_bytes, ws_bytes = cfg._weight_sizes()
+    st = _lib.b4_fp4_linear(
+        _fp4_x(cfg, x, rows, offsets is not None), x.data_ptr(), _fp4_buffer(x_gs, torch.float32, cfg.num_groups, "x_gs"),
+        _fp4_buffer(rows, torch.int32, m, "rows"), _fp4_buffer(offsets, torch.int32, cfg.num_groups + 1, "offsets"),
+        _fp4_buffer(w_codes, torch.uint8, w_bytes, "w_codes"), _fp4_buffer(w_scales, torch.uint8, ws_bytes, "w_scales"),
+        _fp4_buffer(w_gs, torch.float32, cfg.num_groups, "w_gs"), _fp4_buffer(out_rows, torch.int32, m, "out_rows"),
+        _fp4_out(cfg, out, m), _fp4_buffer(workspace, torch.uint8, 0, "workspace"), workspace.numel(),
+        _stream_of(stream, x))
+    if st:
+        _check(st)
 
 
 def fused_moe_a4_workspace_bytes(cfg: MoEConfig, activation: int) -> int:
