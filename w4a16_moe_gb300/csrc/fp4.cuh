@@ -34,7 +34,7 @@ __host__ __device__ inline int64_t fp4_ld(int k) { return ((int64_t)k / 2 + 15) 
 __host__ __device__ inline int fp4_k_tiles(int k, int fmt) { return cdiv(k, 4 * fp4_group(fmt)); }
 
 // Rows of one activation box of a unit of up to nt rows.
-__host__ __device__ constexpr int fp4_box_rows(int nt) { return nt == 64 ? 32 : 64; }
+__host__ __device__ constexpr int fp4_box_rows(int) { return 32; }
 
 struct Fp4QuantParams {
   const void* x;
@@ -62,6 +62,7 @@ struct Fp4QuantParams {
 struct Fp4GemmParams {
   CUtensorMap tmap_w;        // weight codes [E N][K/2] bytes, box 128 x 128 rows
   CUtensorMap tmap_a;        // activation codes [rows][K/2] bytes, box 128 x fp4_box_rows
+  CUtensorMap tmap_ws, tmap_as;  // scale tiles of both (pair kernel)
   const uint8_t* w_scales;
   const uint8_t* a_scales;
   const float* w_gs;         // [E] or null

@@ -20,7 +20,8 @@ cudaError_t launch_fp4_quantize(const Fp4QuantParams& p, int dtype, int num_sms,
 cudaError_t launch_fp4_tile_scales(const uint8_t* src, uint8_t* dst, int groups, int m, int blocks, int k_tiles,
                                    int num_sms, cudaStream_t stream);
 cudaError_t launch_fp4_combine(const Fp4CombineParams& p, cudaStream_t stream);
-cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, int fmt, int nt, int grid, bool pdl, cudaStream_t stream);
+cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, int fmt, int grid, bool pdl, cudaStream_t stream);
+cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& p, int fmt, int pairs, bool pdl, cudaStream_t stream);
 }  // namespace b4
 
 using namespace b4;
@@ -130,11 +131,11 @@ Fp4QuantParams quant_params(const b4_fp4_config* c, const void* x, const int32_t
   return p;
 }
 
-// Activation rows of a unit: 64, or 192 where groups hold enough rows to fill
-// more of the instruction's N.
+// Activation rows of a unit: 64 (one SM a unit), or 192 (a pair of SMs) where
+// groups hold enough rows to fill more of the instruction's N.
 int unit_rows(const b4_fp4_config* c, bool ragged) {
   const int per = ragged ? c->m / c->num_groups : c->m;
-  return per <= 64 ? 64 : 192;
+  return per <= 64 ? 64 : 256;
 }
 
 b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gs,
@@ -147,7 +148,7 @@ b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const u
   const uint64_t ld = (uint64_t)fp4_ld(c->k);
   if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k / 2, ld, 128) ||
       !make_tmap_bytes_2d(&p.tmap_a, a_codes, (uint64_t)operand_rows(c, ragged), c->k / 2, ld,
-                          fp4_box_rows(nt)))
+                          nt == 64 ? 32 : 64))
     FP4_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
   p.w_scales = w_scales;
   p.a_scales = a_scales;
@@ -169,10 +170,17 @@ b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const u
   p.status = status;
   // most units the call can have: each group ends at most one unit early
   const int64_t tok = ragged ? c->m / nt + c->num_groups : (int64_t)cdiv(c->m, nt) * c->num_groups;
-  const int64_t units = tok * cdiv(c->n, 128);
+  const int64_t units = tok * cdiv(c->n, nt == 64 ? 128 : 256);
   if (units > (1 << 30)) FP4_INVALID("too many units of work: m, n and num_groups too large together");
-  const int grid = (int)(units < sms ? units : sms);
-  return cuda_status(launch_fp4_gemm(p, c->format, nt, grid, a_is_new, stream), "fp4 product");
+  if (nt == 64)
+    return cuda_status(launch_fp4_gemm(p, c->format, (int)(units < sms ? units : sms), a_is_new, stream), "fp4 product");
+  const uint64_t k_tiles = (uint64_t)fp4_k_tiles(c->k, c->format);
+  const uint32_t box = (uint32_t)(c->format == B4_NVFP4_E4M3_K16 ? 4 : 2);
+  if (!make_tmap_tiles(&p.tmap_ws, w_scales, (uint64_t)cdiv(c->n, 128) * c->num_groups * k_tiles, box) ||
+      !make_tmap_tiles(&p.tmap_as, a_scales, (uint64_t)operand_tiles(c, ragged) * k_tiles, box))
+    FP4_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected a scale map");
+  const int pairs = (int)(units < sms / 2 ? units : sms / 2);
+  return cuda_status(launch_fp4_gemm_pair(p, c->format, pairs, a_is_new, stream), "fp4 product");
 }
 
 // Workspace of b4_fp4_linear: the quantised activation operand (m rows, dense or

@@ -1,0 +1,282 @@
+// Device code shared by the FP4 x FP4 product kernels: block-scaled matrix
+// instructions, scale copies, the tables of ragged groups, units of work and
+// the epilogue.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fp4.cuh"
+#include "ptx.cuh"
+#include "tma.cuh"
+
+namespace b4 {
+namespace fp4 {
+
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;                 // two per quarter of the lanes, alternating 32-column chunks
+constexpr int kEpiRow = 80;                  // staged 64-byte row, padded so that eight rows hit eight bank groups
+constexpr int kEpiBytes = kEpiWarps * 32 * kEpiRow;
+constexpr int kWStage = 128 * 128;           // weight codes of a stage: 128 rows x 256 K
+constexpr int kMaxGroups = 1024;
+
+__host__ __device__ constexpr int sf_tiles(int fmt) { return fmt == 0 ? 4 : 2; }  // scale tiles of a stage (per 128 rows)
+
+// Instruction descriptor of the block-scaled kinds: E2M1 operands, both
+// K-major, scales E4M3 (0) or E8M0 (1); bits 4 and 29 take the byte of a scale
+// word that the instruction starts at.
+__device__ __forceinline__ uint32_t idesc_fp4(int fmt, uint32_t m, uint32_t n) {
+  return (1u << 7)               // A: E2M1
+         | (1u << 10)            // B: E2M1
+         | ((n >> 3) << 17)      // N >> 3
+         | ((uint32_t)fmt << 23) // scale type
+         | ((m >> 4) << 24);     // M >> 4
+}
+
+// Shared-memory descriptors as the low word (address >> 4 and the leading
+// offset) and a constant high word: offsets are then 32-bit additions.
+constexpr uint32_t kDescHiSw128 = (1024 >> 4) | (1u << 14) | (2u << 29);  // 8-row atoms of 1024 bytes, 128-byte swizzle
+constexpr uint32_t kDescHiTile = (128 >> 4) | (1u << 14);                 // 8-row core matrices of 128 bytes
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+
+// D (+)= A B^T with block scales from tensor memory; CG CTAs of a pair.
+template <int FMT, int CG>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+#define FP4_MMA(kind)                                                                                              \
+  asm volatile(                                                                                                    \
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %7};\n\tmov.b64 y, {%2, " \
+      "%7};\n\t" kind " [%0], x, y, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                             \
+      "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescHiSw128)                           \
+      : "memory")
+  if constexpr (FMT == 0 && CG == 1) FP4_MMA("tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X");
+  if constexpr (FMT == 1 && CG == 1) FP4_MMA("tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X");
+  if constexpr (FMT == 0 && CG == 2) FP4_MMA("tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X");
+  if constexpr (FMT == 1 && CG == 2) FP4_MMA("tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X");
+#undef FP4_MMA
+}
+
+// One 512-byte scale tile (32 rows of 16 bytes) into four columns of tensor
+// memory, the same in all four lane quarters (of both CTAs of a pair, each from
+// its own shared memory).
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
+  if constexpr (CG == 1)
+    asm volatile("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\ttcgen05.cp.cta_group::1.32x128b.warpx4 [%0], x;\n\t}" ::"r"(taddr),
+                 "r"(lo), "n"(kDescHiTile)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\ttcgen05.cp.cta_group::2.32x128b.warpx4 [%0], x;\n\t}" ::"r"(taddr),
+                 "r"(lo), "n"(kDescHiTile)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------ units
+struct Unit {
+  int group, wtile, first, rows;  // first: packed row; rows: live rows
+  int atile;                      // scale tile of row `first`
+  int shift;                      // 32-row groups of that tile before `first`
+};
+
+// Tables of ragged groups in shared memory: first packed row, and activation
+// tiles of NT rows before the group.
+struct Groups {
+  int first[kMaxGroups + 1];
+  int tiles[kMaxGroups + 1];
+  int warp[kThreads / 32];
+};
+
+// A block scan of the groups' tile counts, four groups a thread; ends with the
+// tables written but not yet synchronised.
+template <int NT>
+__device__ __forceinline__ void build_groups(const Fp4GemmParams& p, Groups& g) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int cnt[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = 4 * threadIdx.x + i;
+    cnt[i] = 0;
+    if (e <= p.groups) {
+      const int lo = min(max(__ldg(p.offsets + e), 0), p.m);
+      g.first[e] = lo;
+      if (e < p.groups) cnt[i] = cdiv(max(min(__ldg(p.offsets + e + 1), p.m) - lo, 0), NT);
+    }
+    sum += cnt[i];
+  }
+  int scan = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) g.warp[warp] = scan;
+  __syncthreads();
+  int before = scan - sum;
+  for (int w = 0; w < warp; ++w) before += g.warp[w];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = 4 * threadIdx.x + i;
+    if (e <= p.groups) g.tiles[e] = before;
+    before += cnt[i];
+  }
+}
+
+// Unit u: weight rows outermost within a group, so that neighbouring units
+// read the same weights.  wtiles: weight units of a group.
+template <int NT>
+__device__ __forceinline__ Unit get_unit(const Fp4GemmParams& p, const Groups& g, int wtiles, int u) {
+  int lo = 0;
+  int t;
+  Unit U;
+  if (p.offsets) {
+    int hi = p.groups - 1;  // last group whose tiles start at or before the unit's
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)g.tiles[mid] * wtiles <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    const int nt = g.tiles[lo + 1] - g.tiles[lo];
+    const int v = u - g.tiles[lo] * wtiles;
+    U.wtile = v / nt;
+    t = v - U.wtile * nt;
+    U.first = g.first[lo] + t * NT;
+    U.rows = min(NT, g.first[lo + 1] - U.first);
+    U.atile = g.first[lo] / 128 + lo + t * NT / 128;
+  } else {
+    const int nt = cdiv(p.m, NT);
+    lo = u / (nt * wtiles);
+    const int v = u - lo * nt * wtiles;
+    U.wtile = v / nt;
+    t = v - U.wtile * nt;
+    U.first = lo * p.m + t * NT;
+    U.rows = min(NT, p.m - t * NT);
+    U.atile = lo * cdiv(p.m, 128) + t * NT / 128;
+  }
+  U.group = lo;
+  U.shift = (t * NT & 127) >> 5;
+  return U;
+}
+
+// Rows of a ragged output past the last group are zero: 64 threads.
+__device__ __forceinline__ void clear_tail(const Fp4GemmParams& p, int live, int thread) {
+  const int width = p.out_dtype == 2 ? 4 : 2;
+  for (int r = live + blockIdx.x; r < p.m; r += gridDim.x) {
+    uint8_t* row = reinterpret_cast<uint8_t*>(p.out) + (int64_t)r * p.out_stride * width;
+    if (p.vec) {
+      for (int c = thread; c < p.n * width / 16; c += 64) reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int c = thread; c < p.n; c += 64) {
+        if (width == 4) reinterpret_cast<uint32_t*>(row)[c] = 0;
+        else reinterpret_cast<uint16_t*>(row)[c] = 0;
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------- epilogue
+__device__ __forceinline__ void store_out(const Fp4GemmParams& p, int64_t at, float v) {
+  if (p.out_dtype == 0) reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  else if (p.out_dtype == 1) reinterpret_cast<__half*>(p.out)[at] = __float2half_rn(v);
+  else reinterpret_cast<float*>(p.out)[at] = v;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (DT == 0) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// Scale and output row (-1: none) of a chunk's 32 rows, one lane each.
+struct RowInfo {
+  float g;
+  int to;
+};
+__device__ __forceinline__ RowInfo row_info(const Fp4GemmParams& p, const Unit& U, int c0, int lane, float gw) {
+  RowInfo r{gw, -1};
+  if (c0 + lane < U.rows) {
+    const int at = U.first + c0 + lane;
+    if (p.a_gs && p.a_gs_per_row) r.g *= __ldg(p.a_gs + at);
+    r.to = at;
+    if (p.out_rows) {
+      r.to = __ldg(p.out_rows + at);
+      if (r.to >= p.m) r.to = -1;
+    }
+  }
+  return r;
+}
+__device__ __forceinline__ float group_scale(const Fp4GemmParams& p, int group) {
+  return (p.w_gs ? __ldg(p.w_gs + group) : 1.f) * (p.a_gs && !p.a_gs_per_row ? __ldg(p.a_gs + group) : 1.f);
+}
+
+// A chunk of 32 activation rows x 32 weight rows (from n0) out of fragments of
+// 8 x 8 (weight row x activation row; lo: weight rows 0 .. 15, hi: 16 .. 31):
+// scaled, rounded, and through a transposing store to the warp's staging area,
+// so that it leaves as 16-byte pieces of output rows (64 bytes a row and warp).
+template <int DT>
+__device__ __forceinline__ void store_staged(const Fp4GemmParams& p, const uint32_t (&lo)[16], const uint32_t (&hi)[16],
+                                             const RowInfo& info, int n0, uint8_t* stage, int lane) {
+  uint32_t h[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 8 * i + 2 * (lane & 3);
+    const float g0 = __shfl_sync(0xffffffffu, info.g, t), g1 = __shfl_sync(0xffffffffu, info.g, t + 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      h[i][j] = pack16<DT>(__uint_as_float(lo[4 * i + 2 * j]) * g0, __uint_as_float(lo[4 * i + 2 * j + 1]) * g1);
+      h[i][2 + j] = pack16<DT>(__uint_as_float(hi[4 * i + 2 * j]) * g0, __uint_as_float(hi[4 * i + 2 * j + 1]) * g1);
+    }
+  }
+  const uint32_t st_addr = smem_u32(stage) + (lane & 7) * kEpiRow + (lane >> 3) * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) stmatrix_x4_trans(st_addr + 8 * i * kEpiRow, h[i][0], h[i][1], h[i][2], h[i][3]);
+  __syncwarp();
+  const int n = n0 + 8 * (lane & 3);
+  uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + n;
+  const uint8_t* src = stage + (lane >> 2) * kEpiRow + 16 * (lane & 3);
+  uint4 w[4];
+  int o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = *reinterpret_cast<const uint4*>(src + 8 * i * kEpiRow);
+    o[i] = __shfl_sync(0xffffffffu, info.to, 8 * i + (lane >> 2));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (o[i] >= 0 && n < p.n) *reinterpret_cast<uint4*>(out + (int64_t)o[i] * p.out_stride) = w[i];
+  __syncwarp();
+}
+
+// The same chunk straight from the fragments, for outputs that are not 16-bit
+// or not 16-byte aligned.
+__device__ __forceinline__ void store_direct(const Fp4GemmParams& p, const uint32_t (&lo)[16], const uint32_t (&hi)[16],
+                                          const RowInfo& info, int n0, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int t = 8 * i + 2 * (lane & 3) + j;
+      const float g = __shfl_sync(0xffffffffu, info.g, t);
+      const int o = __shfl_sync(0xffffffffu, info.to, t);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int n = n0 + 8 * h + (lane >> 2);
+        const uint32_t v = h < 2 ? lo[4 * i + 2 * h + j] : hi[4 * i + 2 * (h - 2) + j];
+        if (o >= 0 && n < p.n) store_out(p, (int64_t)o * p.out_stride + n, __uint_as_float(v) * g);
+      }
+    }
+}
+
+__device__ __forceinline__ void store_chunk(const Fp4GemmParams& p, const uint32_t (&lo)[16], const uint32_t (&hi)[16],
+                                            const RowInfo& info, int n0, uint8_t* stage, int lane) {
+  if (p.vec && p.out_dtype == 0) store_staged<0>(p, lo, hi, info, n0, stage, lane);
+  else if (p.vec && p.out_dtype == 1) store_staged<1>(p, lo, hi, info, n0, stage, lane);
+  else store_direct(p, lo, hi, info, n0, lane);
+}
+
+}  // namespace fp4
+}  // namespace b4
