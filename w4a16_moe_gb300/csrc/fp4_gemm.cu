@@ -54,7 +54,7 @@ struct Cfg {
   static_assert(kAStage % 1024 == 0, "swizzle atoms stay 1024-byte aligned");
 };
 
-template <int FMT, int NT>
+template <int FMT, int NT, int OUT, bool RAGGED>
 __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_constant__ Fp4GemmParams p) {
   using C = Cfg<FMT, NT>;
   constexpr int NS = C::kStages;
@@ -96,13 +96,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
   if (!p.a_is_new) pdl_wait();  // standalone: every input may come from the kernel before
 
   const int wtiles = cdiv(p.n, 128);
-  if (p.offsets) build_groups<NT>(p, groups);
+  if (RAGGED) build_groups<NT>(p, groups);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0) pdl_launch_dependents();
   const uint32_t tmem = *s_tmem;
-  const int n_units = (p.offsets ? groups.tiles[p.groups] : p.groups * cdiv(p.m, NT)) * wtiles;
+  const int n_units = (RAGGED ? groups.tiles[p.groups] : p.groups * cdiv(p.m, NT)) * wtiles;
   const int k64 = cdiv(p.k, 64);                       // matrix instructions along K
   const int stages = cdiv(k64, 4);
   const int k_tiles = cdiv(p.k, 4 * fp4_group(FMT));   // scale tiles along K
@@ -115,10 +115,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     uint32_t ss = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-      const Unit U = get_unit<NT>(p, groups, wtiles, u);
-      const int rows = __shfl_sync(0xffffffffu, U.rows, 0), shift = __shfl_sync(0xffffffffu, U.shift, 0);
-      const int first = __shfl_sync(0xffffffffu, U.first, 0), atile = __shfl_sync(0xffffffffu, U.atile, 0);
-      const int group = __shfl_sync(0xffffffffu, U.group, 0), wtile = __shfl_sync(0xffffffffu, U.wtile, 0);
+      const Unit U = get_unit<NT, RAGGED>(p, groups, wtiles, u);
+      const int rows = (int)warp_uniform(U.rows), shift = (int)warp_uniform(U.shift);
+      const int first = (int)warp_uniform(U.first), atile = (int)warp_uniform(U.atile);
+      const int group = (int)warp_uniform(U.group), wtile = (int)warp_uniform(U.wtile);
       const int boxes = (rows + kBox - 1) / kBox;
       const bool two = C::kABlocks == 2 && shift * 32 + rows > 128;
       const uint8_t* wsf = p.w_scales + ((size_t)group * wtiles + wtile) * tile_pitch;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
       const uint32_t code_bytes = kWStage + boxes * kBox * 128;
       for (int s = 0; s < stages; ++s, ++ss) {
         const uint32_t slot = ss % NS;
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ((ss / NS) & 1) ^ 1, ab, 101));
+        ok = __all_sync(0xffffffffu, wait(&empty[slot], ((ss / NS) & 1) ^ 1, ab, 101));
         if (!ok) break;
         const int kt0 = s * C::kSfTiles;
         const uint32_t sfb = (uint32_t)min(C::kSfTiles, k_tiles - kt0) * kSfTile;
@@ -167,12 +167,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     constexpr uint32_t tm = 0;  // all of tensor memory: it starts at column 0
     const uint32_t w_desc = desc_lo(smem_u32(smem)), a_desc = desc_lo(smem_u32(s_a)), s_desc = desc_lo(smem_u32(s_sf));
     for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
-      const Unit U = get_unit<NT>(p, groups, wtiles, u);
-      const int rows = __shfl_sync(0xffffffffu, U.rows, 0), shift = __shfl_sync(0xffffffffu, U.shift, 0);
+      const Unit U = get_unit<NT, RAGGED>(p, groups, wtiles, u);
+      const int rows = (int)warp_uniform(U.rows), shift = (int)warp_uniform(U.shift);
       const bool two = C::kABlocks == 2 && shift * 32 + rows > 128;
       const uint32_t idesc = idesc_fp4(FMT, 128, (uint32_t)round_up(rows, 16));
       const uint32_t abuf = acc_i & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty_acc[abuf], ((acc_i >> 1) & 1) ^ 1, ab, 102))) break;
+      if (!__all_sync(0xffffffffu, wait(&empty_acc[abuf], ((acc_i >> 1) & 1) ^ 1, ab, 102))) break;
       tc_fence_after();
       const uint32_t d = tm + abuf * NT;
       bool ok = true;
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         const uint32_t slot = ss % NS;
         // with fewer scale buffers than stages, the products that last read this one come first
         if (C::kSfRing < NS && ss >= C::kSfRing)
-          ok = mbar_wait(&empty[(ss - C::kSfRing) % NS], ((ss - C::kSfRing) / NS) & 1, ab, 103);
-        ok = ok && mbar_wait(&full[slot], (ss / NS) & 1, ab, 104);
+          ok = wait(&empty[(ss - C::kSfRing) % NS], ((ss - C::kSfRing) / NS) & 1, ab, 103);
+        ok = ok && wait(&full[slot], (ss / NS) & 1, ab, 104);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     __syncwarp();
   } else if (warp < 4) {
     // ------------------- rows of a ragged output past the last group: zero
-    if (p.offsets && !p.out_rows) {
+    if (RAGGED && !p.out_rows) {
       if (p.a_is_new) pdl_wait();
       clear_tail(p, groups.first[p.groups], threadIdx.x - 64);
     }
@@ -237,11 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     uint8_t* stage = smem + C::epi + (warp - 4) * 32 * kEpiRow;
     uint32_t acc_i = 0;
     for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
-      const Unit U = get_unit<NT>(p, groups, wtiles, u);
+      const Unit U = get_unit<NT, RAGGED>(p, groups, wtiles, u);
       const uint32_t abuf = acc_i & 1;
       const float gw = group_scale(p, U.group);
       RowInfo info = row_info(p, U, 32 * turn, lane, gw);
-      const bool ok = mbar_wait(&full_acc[abuf], (acc_i >> 1) & 1, ab, 105);
+      const bool ok = wait(&full_acc[abuf], (acc_i >> 1) & 1, ab, 105);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + abuf * NT;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         tmem_ld16x256b_x4(taddr + (16u << 16) + c0, hi);
         if (c0 != 32 * turn) info = row_info(p, U, c0, lane, gw);
         tmem_ld_wait();
-        store_chunk(p, lo, hi, info, U.wtile * 128 + 32 * q4, stage, lane);
+        store_chunk<OUT>(p, lo, hi, info, U.wtile * 128 + 32 * q4, stage, lane);
       }
       tc_fence_before();
       __syncwarp();
@@ -266,9 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-template <int FMT, int NT>
+template <int FMT, int OUT, bool RAGGED, int NT = 64>
 cudaError_t launch(const Fp4GemmParams& p, int grid, bool pdl, cudaStream_t stream) {
-  auto kern = fp4_gemm_kernel<FMT, NT>;
+  auto kern = fp4_gemm_kernel<FMT, NT, OUT, RAGGED>;
   const size_t smem = Cfg<FMT, NT>::total;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -288,7 +288,9 @@ cudaError_t launch(const Fp4GemmParams& p, int grid, bool pdl, cudaStream_t stre
 }  // namespace fp4
 
 cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, int fmt, int grid, bool pdl, cudaStream_t stream) {
-  return fmt == 0 ? fp4::launch<0, 64>(p, grid, pdl, stream) : fp4::launch<1, 64>(p, grid, pdl, stream);
+  return fp4::with_forms(p, fmt, [&](auto f, auto out, auto ragged) {
+    return fp4::launch<f.value, out.value, ragged.value>(p, grid, pdl, stream);
+  });
 }
 
 }  // namespace b4

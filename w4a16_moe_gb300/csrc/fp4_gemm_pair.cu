@@ -3,23 +3,22 @@
 // layouts and the treatment of groups are those of fp4_gemm.cu.
 //
 // What bounds it.  At the FP4 rate of the tensor core the operands' way from L2
-// into shared memory is a narrow place: an SM takes in about 60 bytes a cycle,
+// into shared memory is the narrow place: an SM takes in about 60 bytes a cycle,
 // and a unit of 128 weight rows x 192 activation rows on one SM needs 46 KB for
 // 384 cycles of products (measured at N = K = 4096, 4096 rows: 42 us with the
 // products, 33 us with the copies alone).  Two SMs that share a unit of 256
-// weight rows x 192 activation rows each hold their own 128 weight rows and half
-// of the activation rows: 34 KB.  The copies of scales into tensor memory run on
-// the same pipe as the products, 18 cycles each, twelve a stage of NVFP4 (six of
-// MXFP4): a stage takes 384 + 216 cycles.  With 256 activation rows a stage does
-// more for its scale copies (512 + 216) but leaves room for one accumulator only,
-// whose hand-over between units measured 1900 cycles.
+// weight rows x 256 activation rows each hold their own 128 weight rows and half
+// of the activation rows: 38 KB for 512 cycles.  The copies of scales into tensor
+// memory run on the same pipe as the products, 18 cycles each, twelve a stage of
+// NVFP4 and six of MXFP4.
 //
 // Each CTA copies its weight rows, its half of the activation rows, its weights'
 // scales and the scales of all activation rows into its own shared memory; every
 // copy signals the leader's barrier.  The leader's warp 1 issues the pair's
-// products and scale copies, and commits to the barriers of both.  Two
-// accumulators (128 lanes x 192 columns a CTA), so a unit's epilogue runs under
-// the next unit's products.  Roles of the warps as in fp4_gemm.cu.
+// products and scale copies, and commits to the barriers of both.  The epilogue
+// warps take a unit's accumulator (128 lanes x 256 columns a CTA) whole into
+// registers, hand it back, and only then scale, round and store, under the next
+// unit's products.  Roles of the warps as in fp4_gemm.cu.
 
 #include "fp4_mma.cuh"
 
@@ -40,20 +39,18 @@ struct PairCfg {
   static constexpr int kStage = kWStage + kAStage + 3 * kSfBytes;
   static constexpr int kStages = 5;
   static constexpr int kSfCols = 4 * kSfTiles * 3;                  // weights, two tiles of activation rows
-  static constexpr int kAccs = 2 * kPairRows + 2 * kSfCols <= 512 ? 2 : 1;
-  static constexpr int kSfFit = (512 - kAccs * kPairRows) / kSfCols;
-  static constexpr int kSfRing = kSfFit < kStages ? kSfFit : kStages;
+  static constexpr int kSfRing = (512 - kPairRows) / kSfCols < kStages ? (512 - kPairRows) / kSfCols : kStages;
   static constexpr size_t a = (size_t)kStages * kWStage;
   static constexpr size_t sf = a + (size_t)kStages * kAStage;
   static constexpr size_t epi = sf + (size_t)kStages * 3 * kSfBytes;
   static constexpr size_t bars = epi + kEpiBytes;
-  static constexpr int kNumBars = 2 * kStages + 4 + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 + 1;
   static constexpr size_t misc = bars + 8 * kNumBars;
   static constexpr size_t total = misc + 16 + 1024;                 // + alignment slack
-  static_assert(kSfRing >= 2, "tensor memory budget");
+  static_assert(kSfRing == kStages, "a stage's scale columns are free once its shared memory is");
 };
 
-template <int FMT>
+template <int FMT, int OUT, bool RAGGED>
 __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmParams p) {
   using C = PairCfg<FMT>;
   constexpr int NS = C::kStages;
@@ -65,8 +62,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::bars);  // the leader's: copies of both CTAs
   uint64_t* empty = full + NS;                                   // each CTA's own
   uint64_t* full_acc = empty + NS;                               // each CTA's own
-  uint64_t* empty_acc = full_acc + 2;                            // the leader's: epilogue warps of both
-  uint64_t* drain = empty_acc + 2;
+  uint64_t* empty_acc = full_acc + 1;                            // the leader's: epilogue warps of both
+  uint64_t* drain = empty_acc + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::misc + 4);
 
@@ -81,10 +78,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&full_acc[i], 1);
-      mbar_init(&empty_acc[i], 2 * kEpiWarps);
-    }
+    mbar_init(full_acc, 1);
+    mbar_init(empty_acc, 2 * kEpiWarps);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -94,13 +89,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   }
   if (!p.a_is_new) pdl_wait();  // standalone: every input may come from the kernel before
   const int wpairs = cdiv(p.n, 256);
-  if (p.offsets) build_groups<kPairRows>(p, groups);
+  if (RAGGED) build_groups<kPairRows>(p, groups);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers exist before either signals
   tc_fence_after();
   if (threadIdx.x == 0) pdl_launch_dependents();
   const uint32_t tmem = *s_tmem;
-  const int n_units = (p.offsets ? groups.tiles[p.groups] : p.groups * cdiv(p.m, kPairRows)) * wpairs;
+  const int n_units = (RAGGED ? groups.tiles[p.groups] : p.groups * cdiv(p.m, kPairRows)) * wpairs;
   const int k64 = cdiv(p.k, 64);                       // matrix instructions along K
   const int stages = cdiv(k64, 4);
   const int k_tiles = cdiv(p.k, 4 * fp4_group(FMT));   // scale tiles along K
@@ -112,13 +107,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     if (p.a_is_new) pdl_wait();
     uint32_t ss = 0;
     bool ok = true;
-    const uint32_t full0 = __shfl_sync(0xffffffffu, map_rank(full, 0), 0);
+    const uint32_t full0 = warp_uniform(map_rank(full, 0));
     for (int u = u0; u < n_units && ok; u += du) {
-      const Unit U = get_unit<kPairRows>(p, groups, wpairs, u);
-      const int rows = __shfl_sync(0xffffffffu, U.rows, 0), first = __shfl_sync(0xffffffffu, U.first, 0);
-      const int group = __shfl_sync(0xffffffffu, U.group, 0), atile = __shfl_sync(0xffffffffu, U.atile, 0);
-      const int wtile = 2 * __shfl_sync(0xffffffffu, U.wtile, 0) + (int)rank;
-      const int shift = __shfl_sync(0xffffffffu, U.shift, 0);
+      const Unit U = get_unit<kPairRows, RAGGED>(p, groups, wpairs, u);
+      const int rows = (int)warp_uniform(U.rows), first = (int)warp_uniform(U.first);
+      const int group = (int)warp_uniform(U.group), atile = (int)warp_uniform(U.atile);
+      const int wtile = 2 * (int)warp_uniform(U.wtile) + (int)rank;
+      const int shift = (int)warp_uniform(U.shift);
       const int half = round_up(rows, 32) / 2;  // activation rows a CTA holds
       const bool two = shift * 32 + rows > 128;
       const int boxes = (half + kBoxRows - 1) / kBoxRows;
@@ -128,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       const uint32_t bytes = 2 * (kWStage + boxes * kBoxRows * 128 + (two ? 3 : 2) * C::kSfBytes);
       for (int s = 0; s < stages; ++s, ++ss) {
         const uint32_t slot = ss % NS;
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ((ss / NS) & 1) ^ 1, ab, 111));
+        ok = __all_sync(0xffffffffu, wait(&empty[slot], ((ss / NS) & 1) ^ 1, ab, 111));
         if (!ok) break;
         const int kt0 = s * C::kSfTiles;
         uint8_t* sf = s_sf + slot * 3 * C::kSfBytes;
@@ -163,9 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       // The loop over a stage's slot is unrolled over the ring, so that slots
       // and scale columns are constants: with them in registers a stage took
       // 100 - 150 cycles more to issue than its products take to run.
-      static_assert(C::kSfRing == NS, "a stage's scale columns are free once its shared memory is");
       const uint32_t w_desc = desc_lo(smem_u32(smem)), a_desc = desc_lo(smem_u32(s_a)), s_desc = desc_lo(smem_u32(s_sf));
-      uint32_t acc_i = 0, phase = 0;
+      uint32_t phase = 0, acc_i = 0;
       int u = u0, s = 0;
       uint32_t idesc = 0;
       bool two = false;
@@ -175,14 +169,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
 #pragma unroll
         for (int slot = 0; slot < NS; ++slot) {
           if (s == 0) {
-            const int rows = __shfl_sync(0xffffffffu, get_unit<kPairRows>(p, groups, wpairs, u).rows, 0);
+            const int rows = (int)warp_uniform(get_unit<kPairRows, RAGGED>(p, groups, wpairs, u).rows);
             two = rows > 128;
             idesc = idesc_fp4(FMT, 256, (uint32_t)round_up(rows, 32));
-            ok = __all_sync(0xffffffffu, mbar_wait(empty_acc, (acc_i & 1) ^ 1, ab, 112));
+            ok = __all_sync(0xffffffffu, wait(empty_acc, (acc_i & 1) ^ 1, ab, 112));
             if (!ok) break;
+            ++acc_i;
           }
           if (!seen) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, ab, 114));
+            ok = __all_sync(0xffffffffu, wait(&full[slot], phase, ab, 114));
             if (!ok) break;
           }
           tc_fence_after();
@@ -220,7 +215,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
           ++s;
           if (last) {
             s = 0;
-            ++acc_i;
             u += du;
             ok = u < n_units;
             if (!ok) break;
@@ -237,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     }
   } else if (warp < 4) {
     // ------------------- rows of a ragged output past the last group: zero
-    if (p.offsets && !p.out_rows) {
+    if (RAGGED && !p.out_rows) {
       if (p.a_is_new) pdl_wait();
       clear_tail(p, groups.first[p.groups], threadIdx.x - 64);
     }
@@ -251,17 +245,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     const uint32_t done = map_rank(empty_acc, 0);
     uint32_t acc_i = 0;
     for (int u = u0; u < n_units; u += du) {
-      const Unit U = get_unit<kPairRows>(p, groups, wpairs, u);
+      const Unit U = get_unit<kPairRows, RAGGED>(p, groups, wpairs, u);
       const float gw = group_scale(p, U.group);
-      const int n0 = (2 * U.wtile + (int)rank) * 128 + 32 * q4;
-      const uint32_t abuf = acc_i % C::kAccs;
       RowInfo info[kChunks];
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) info[i] = row_info(p, U, 64 * i + 32 * turn, lane, gw);
-      const bool ok = mbar_wait(&full_acc[abuf], (acc_i / C::kAccs) & 1, ab, 115);
+      const int n0 = (2 * U.wtile + (int)rank) * 128 + 32 * q4;
+      const bool ok = wait(full_acc, acc_i & 1, ab, 115);
       if (!__all_sync(0xffffffffu, ok)) break;
+      ++acc_i;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + abuf * kPairRows + 32 * turn;
+      const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + 32 * turn;
       uint32_t lo[kChunks][16], hi[kChunks][16];
 #pragma unroll
       for (int i = 0; i < kChunks; ++i)
@@ -272,11 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(done + 8 * abuf);
+      if (lane == 0) mbar_arrive_cluster(done);
 #pragma unroll
       for (int i = 0; i < kChunks; ++i)
-        if (64 * i + 32 * turn < U.rows && n0 < p.n) store_chunk(p, lo[i], hi[i], info[i], n0, stage, lane);
-      ++acc_i;
+        if (64 * i + 32 * turn < U.rows && n0 < p.n) store_chunk<OUT>(p, lo[i], hi[i], info[i], n0, stage, lane);
     }
   }
 
@@ -286,9 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int FMT>
+template <int FMT, int OUT, bool RAGGED>
 cudaError_t launch_pair(const Fp4GemmParams& p, int pairs, bool pdl, cudaStream_t stream) {
-  auto kern = fp4_pair_kernel<FMT>;
+  auto kern = fp4_pair_kernel<FMT, OUT, RAGGED>;
   const size_t smem = PairCfg<FMT>::total;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -312,7 +305,9 @@ cudaError_t launch_pair(const Fp4GemmParams& p, int pairs, bool pdl, cudaStream_
 }  // namespace fp4
 
 cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& p, int fmt, int pairs, bool pdl, cudaStream_t stream) {
-  return fmt == 0 ? fp4::launch_pair<0>(p, pairs, pdl, stream) : fp4::launch_pair<1>(p, pairs, pdl, stream);
+  return fp4::with_forms(p, fmt, [&](auto f, auto out, auto ragged) {
+    return fp4::launch_pair<f.value, out.value, ragged.value>(p, pairs, pdl, stream);
+  });
 }
 
 }  // namespace b4

@@ -6,6 +6,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "fp4.cuh"
 #include "ptx.cuh"
 #include "tma.cuh"
@@ -71,6 +73,16 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
                  : "memory");
 }
 
+// mbar_wait with the waiting itself out of line: the kernels' loops stay small
+// (see store_chunk on the instruction cache).
+__device__ __noinline__ static bool wait_long(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* flag,
+                                              uint32_t where) {
+  return mbar_wait(bar, parity, Abort{status, flag}, where);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Abort& ab, uint32_t where) {
+  return mbar_test(bar, parity) || wait_long(bar, parity, ab.status, ab.flag, where);
+}
+
 // ------------------------------------------------------------------ units
 struct Unit {
   int group, wtile, first, rows;  // first: packed row; rows: live rows
@@ -123,12 +135,12 @@ __device__ __forceinline__ void build_groups(const Fp4GemmParams& p, Groups& g) 
 
 // Unit u: weight rows outermost within a group, so that neighbouring units
 // read the same weights.  wtiles: weight units of a group.
-template <int NT>
+template <int NT, bool RAGGED>
 __device__ __forceinline__ Unit get_unit(const Fp4GemmParams& p, const Groups& g, int wtiles, int u) {
   int lo = 0;
   int t;
   Unit U;
-  if (p.offsets) {
+  if constexpr (RAGGED) {
     int hi = p.groups - 1;  // last group whose tiles start at or before the unit's
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -144,7 +156,7 @@ __device__ __forceinline__ Unit get_unit(const Fp4GemmParams& p, const Groups& g
     U.atile = g.first[lo] / 128 + lo + t * NT / 128;
   } else {
     const int nt = cdiv(p.m, NT);
-    lo = u / (nt * wtiles);
+    lo = p.groups == 1 ? 0 : u / (nt * wtiles);
     const int v = u - lo * nt * wtiles;
     U.wtile = v / nt;
     t = v - U.wtile * nt;
@@ -271,11 +283,29 @@ __device__ __forceinline__ void store_direct(const Fp4GemmParams& p, const uint3
     }
 }
 
+// OUT: 0 bf16, 1 f16, both in 16-byte pieces; 2: any type, straight.  (A kernel
+// holds one form: with all three in it, the epilogue's code alone slowed the
+// issuing warps through the instruction cache, 29 -> 33 us at 4096^3.)
+template <int OUT>
 __device__ __forceinline__ void store_chunk(const Fp4GemmParams& p, const uint32_t (&lo)[16], const uint32_t (&hi)[16],
                                             const RowInfo& info, int n0, uint8_t* stage, int lane) {
-  if (p.vec && p.out_dtype == 0) store_staged<0>(p, lo, hi, info, n0, stage, lane);
-  else if (p.vec && p.out_dtype == 1) store_staged<1>(p, lo, hi, info, n0, stage, lane);
-  else store_direct(p, lo, hi, info, n0, lane);
+  if constexpr (OUT == 2) store_direct(p, lo, hi, info, n0, lane);
+  else store_staged<OUT>(p, lo, hi, info, n0, stage, lane);
+}
+
+// Calls f with a kernel's forms as compile-time values: format, output, ragged.
+template <typename F>
+cudaError_t with_forms(const Fp4GemmParams& p, int fmt, F f) {
+  auto by_out = [&](auto fm) {
+    auto by_groups = [&](auto out) {
+      return p.offsets ? f(fm, out, std::true_type{}) : f(fm, out, std::false_type{});
+    };
+    const int form = p.vec ? p.out_dtype : 2;
+    return form == 0   ? by_groups(std::integral_constant<int, 0>{})
+           : form == 1 ? by_groups(std::integral_constant<int, 1>{})
+                       : by_groups(std::integral_constant<int, 2>{});
+  };
+  return fmt == 0 ? by_out(std::integral_constant<int, 0>{}) : by_out(std::integral_constant<int, 1>{});
 }
 
 }  // namespace fp4

@@ -179,6 +179,13 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// A value that every lane holds, as one that the compiler knows to be the same
+// in all of them (a vote's result), so that what follows from it can stay in
+// uniform registers, where tcgen05 and TMA instructions take their operands.
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t v) {
+  return __ballot_sync(0xffffffffu, (v >> (threadIdx.x & 31)) & 1u);
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
