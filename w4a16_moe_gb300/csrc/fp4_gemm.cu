@@ -16,7 +16,8 @@
 // scales as whole 512-byte tiles by bulk copies next to them and from shared
 // into tensor memory by tcgen05.cp, which the instructions that read them
 // follow in order.  Roles of the twelve warps: 0 copies, 1 matrix instructions,
-// 2 and 3 rows of a ragged output past the last group (zeros), 4 to 11 epilogue.
+// 2 and 3 the epilogue's tables of row scales and places, and zeros in rows of a
+// ragged output past the last group, 4 to 11 epilogue.
 // Two accumulators, so a unit's epilogue runs under the next unit's products.
 // Every wait is bounded (ptx.cuh).
 
@@ -36,7 +37,7 @@ struct Cfg {
   static constexpr int kABlocks = NT > 64 ? 2 : 1;              // 128-row scale tiles a unit's rows touch
   static constexpr int kAStage = NT * 128;
   static constexpr int kStage = kWStage + kAStage + 2048 * (1 + kABlocks);
-  static constexpr int kStages = (216 * 1024 - kEpiBytes) / kStage;
+  static constexpr int kStages = (214 * 1024 - kEpiBytes - (int)sizeof(RowTable<NT>)) / kStage;
   static constexpr int kSfCols = 4 * kSfTiles * (1 + kABlocks);  // tensor-memory columns of a stage's scales
   // scale buffers in tensor memory: one per stage where they fit, then a stage's
   // scales are free to overwrite once its shared memory is
@@ -46,8 +47,9 @@ struct Cfg {
   static constexpr size_t a = (size_t)kStages * kWStage;
   static constexpr size_t sf = a + (size_t)kStages * kAStage;
   static constexpr size_t epi = sf + (size_t)kStages * 2048 * (1 + kABlocks);
-  static constexpr size_t bars = epi + kEpiBytes;
-  static constexpr int kNumBars = 2 * kStages + 4 + 1;
+  static constexpr size_t rows = epi + kEpiBytes;
+  static constexpr size_t bars = rows + sizeof(RowTable<NT>);
+  static constexpr int kNumBars = 2 * kStages + 4 + 1 + 4;
   static constexpr size_t misc = bars + 8 * kNumBars;
   static constexpr size_t total = misc + 16 + 1024;             // + alignment slack
   static_assert(kSfRing >= 2, "tensor memory budget");
@@ -69,6 +71,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
   uint64_t* full_acc = empty + NS;
   uint64_t* empty_acc = full_acc + 2;
   uint64_t* drain = empty_acc + 2;
+  uint64_t* full_rows = drain + 1;
+  uint64_t* empty_rows = full_rows + 2;
+  RowTable<NT>& tab = *reinterpret_cast<RowTable<NT>*>(smem + C::rows);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::misc + 4);
 
@@ -85,6 +90,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full_acc[i], 1);
       mbar_init(&empty_acc[i], kEpiWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full_rows[i], 2);
+      mbar_init(&empty_rows[i], kEpiWarps);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -224,39 +233,42 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     }
     __syncwarp();
   } else if (warp < 4) {
-    // ------------------- rows of a ragged output past the last group: zero
-    if (RAGGED && !p.out_rows) {
-      if (p.a_is_new) pdl_wait();
-      clear_tail(p, groups.first[p.groups], threadIdx.x - 64);
-    }
+    // ------- the epilogue's row tables; rows past the last group are zero
+    if (p.a_is_new) pdl_wait();
+    fill_rows<NT, RAGGED>(p, groups, tab, full_rows, empty_rows, wtiles, blockIdx.x, gridDim.x, n_units, ab);
+    if (RAGGED && !p.out_rows) clear_tail(p, groups.first[p.groups], threadIdx.x - 64);
   } else {
     // --------------------------------------------------------- epilogue
     if (p.a_is_new) pdl_wait();
+    static_assert(NT == 64, "a chunk for each warp");
     const int q4 = warp & 3;
     const int turn = (warp - 4) >> 2;
     uint8_t* stage = smem + C::epi + (warp - 4) * 32 * kEpiRow;
-    uint32_t acc_i = 0;
-    for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
-      const Unit U = get_unit<NT, RAGGED>(p, groups, wtiles, u);
-      const uint32_t abuf = acc_i & 1;
-      const float gw = group_scale(p, U.group);
-      RowInfo info = row_info(p, U, 32 * turn, lane, gw);
-      const bool ok = wait(&full_acc[abuf], (acc_i >> 1) & 1, ab, 105);
+    uint32_t i = 0;
+    for (int u = blockIdx.x; u < n_units; u += gridDim.x, ++i) {
+      const uint32_t b = i & 1;
+      bool ok = wait(&full_rows[b], (i >> 1) & 1, ab, 107);
+      ok = ok && wait(&full_acc[b], (i >> 1) & 1, ab, 105);
       if (!__all_sync(0xffffffffu, ok)) break;
+      const int rows = tab.rows[b];
+      const int n0 = tab.wtile[b] * 128 + 32 * q4;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + abuf * NT;
-      for (int c0 = 32 * turn; c0 < U.rows; c0 += 64) {
+      const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + b * NT + 32 * turn;
+      if (32 * turn < rows) {
         uint32_t lo[16], hi[16];
-        tmem_ld16x256b_x4(taddr + c0, lo);
-        tmem_ld16x256b_x4(taddr + (16u << 16) + c0, hi);
-        if (c0 != 32 * turn) info = row_info(p, U, c0, lane, gw);
+        tmem_ld16x256b_x4(taddr, lo);
+        tmem_ld16x256b_x4(taddr + (16u << 16), hi);
+        const int r = 32 * turn + lane;
+        const RowInfo info{tab.g[b][r], tab.to[b][r]};
         tmem_ld_wait();
-        store_chunk<OUT>(p, lo, hi, info, U.wtile * 128 + 32 * q4, stage, lane);
+        if (n0 < p.n) store_chunk<OUT>(p, lo, hi, info, n0, stage, lane);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty_acc[abuf]);
-      ++acc_i;
+      if (lane == 0) {
+        mbar_arrive(&empty_acc[b]);
+        mbar_arrive(&empty_rows[b]);
+      }
     }
   }
 

@@ -18,7 +18,8 @@
 // products and scale copies, and commits to the barriers of both.  The epilogue
 // warps take a unit's accumulator (128 lanes x 256 columns a CTA) whole into
 // registers, hand it back, and only then scale, round and store, under the next
-// unit's products.  Roles of the warps as in fp4_gemm.cu.
+// unit's products.  Roles of the warps as in fp4_gemm.cu (2 and 3 also look up the
+// rows' scales and places ahead of the epilogue).
 
 #include "fp4_mma.cuh"
 
@@ -43,8 +44,9 @@ struct PairCfg {
   static constexpr size_t a = (size_t)kStages * kWStage;
   static constexpr size_t sf = a + (size_t)kStages * kAStage;
   static constexpr size_t epi = sf + (size_t)kStages * 3 * kSfBytes;
-  static constexpr size_t bars = epi + kEpiBytes;
-  static constexpr int kNumBars = 2 * kStages + 2 + 1;
+  static constexpr size_t rows = epi + kEpiBytes;
+  static constexpr size_t bars = rows + sizeof(RowTable<kPairRows>);
+  static constexpr int kNumBars = 2 * kStages + 2 + 1 + 4;
   static constexpr size_t misc = bars + 8 * kNumBars;
   static constexpr size_t total = misc + 16 + 1024;                 // + alignment slack
   static_assert(kSfRing == kStages, "a stage's scale columns are free once its shared memory is");
@@ -64,6 +66,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   uint64_t* full_acc = empty + NS;                               // each CTA's own
   uint64_t* empty_acc = full_acc + 1;                            // the leader's: epilogue warps of both
   uint64_t* drain = empty_acc + 1;
+  uint64_t* full_rows = drain + 1;                               // each CTA's own, two deep
+  uint64_t* empty_rows = full_rows + 2;
+  RowTable<kPairRows>& tab = *reinterpret_cast<RowTable<kPairRows>*>(smem + C::rows);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::misc + 4);
 
@@ -81,6 +86,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     mbar_init(full_acc, 1);
     mbar_init(empty_acc, 2 * kEpiWarps);
     mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full_rows[i], 2);
+      mbar_init(&empty_rows[i], kEpiWarps);
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -230,46 +239,47 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       __syncwarp();
     }
   } else if (warp < 4) {
-    // ------------------- rows of a ragged output past the last group: zero
-    if (RAGGED && !p.out_rows) {
-      if (p.a_is_new) pdl_wait();
-      clear_tail(p, groups.first[p.groups], threadIdx.x - 64);
-    }
+    // ------- the epilogue's row tables; rows past the last group are zero
+    if (p.a_is_new) pdl_wait();
+    fill_rows<kPairRows, RAGGED>(p, groups, tab, full_rows, empty_rows, wpairs, u0, du, n_units, ab);
+    if (RAGGED && !p.out_rows) clear_tail(p, groups.first[p.groups], threadIdx.x - 64);
   } else {
     // --------------------------------------------------------- epilogue
     if (p.a_is_new) pdl_wait();
-    constexpr int kChunks = (kPairRows + 63) / 64;  // 32-row chunks a warp takes
+    constexpr int kChunks = kPairRows / 64;  // 32-row chunks a warp takes
     const int q4 = warp & 3;
     const int turn = (warp - 4) >> 2;
     uint8_t* stage = smem + C::epi + (warp - 4) * 32 * kEpiRow;
     const uint32_t done = map_rank(empty_acc, 0);
-    uint32_t acc_i = 0;
-    for (int u = u0; u < n_units; u += du) {
-      const Unit U = get_unit<kPairRows, RAGGED>(p, groups, wpairs, u);
-      const float gw = group_scale(p, U.group);
-      RowInfo info[kChunks];
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) info[i] = row_info(p, U, 64 * i + 32 * turn, lane, gw);
-      const int n0 = (2 * U.wtile + (int)rank) * 128 + 32 * q4;
-      const bool ok = wait(full_acc, acc_i & 1, ab, 115);
+    const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + 32 * turn;
+    uint32_t i = 0;
+    for (int u = u0; u < n_units; u += du, ++i) {
+      const uint32_t b = i & 1;
+      bool ok = wait(&full_rows[b], (i >> 1) & 1, ab, 107);
+      ok = ok && wait(full_acc, b, ab, 115);
       if (!__all_sync(0xffffffffu, ok)) break;
-      ++acc_i;
+      const int rows = tab.rows[b];
+      const int n0 = (2 * tab.wtile[b] + (int)rank) * 128 + 32 * q4;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + 32 * turn;
       uint32_t lo[kChunks][16], hi[kChunks][16];
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i)
-        if (64 * i + 32 * turn < U.rows) {
-          tmem_ld16x256b_x4(taddr + 64 * i, lo[i]);
-          tmem_ld16x256b_x4(taddr + (16u << 16) + 64 * i, hi[i]);
+      for (int c = 0; c < kChunks; ++c)
+        if (64 * c + 32 * turn < rows) {
+          tmem_ld16x256b_x4(taddr + 64 * c, lo[c]);
+          tmem_ld16x256b_x4(taddr + (16u << 16) + 64 * c, hi[c]);
         }
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(done);
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i)
-        if (64 * i + 32 * turn < U.rows && n0 < p.n) store_chunk<OUT>(p, lo[i], hi[i], info[i], n0, stage, lane);
+      for (int c = 0; c < kChunks; ++c)
+        if (64 * c + 32 * turn < rows && n0 < p.n) {
+          const int r = 64 * c + 32 * turn + lane;
+          store_chunk<OUT>(p, lo[c], hi[c], RowInfo{tab.g[b][r], tab.to[b][r]}, n0, stage, lane);
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty_rows[b]);
     }
   }
 

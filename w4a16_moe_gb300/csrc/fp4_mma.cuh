@@ -203,26 +203,53 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
-// Scale and output row (-1: none) of a chunk's 32 rows, one lane each.
+// What the epilogue needs to know of a unit, two units deep in shared memory:
+// warps 2 and 3 look it up ahead, since under the operands' traffic a load from
+// L2 takes some 3000 cycles, as long as half a unit's stores.
+template <int NT>
+struct RowTable {
+  float g[2][NT];   // scale of each activation row, the weights' included
+  int to[2][NT];    // its output row, or -1
+  int rows[2], wtile[2];
+};
 struct RowInfo {
   float g;
   int to;
 };
-__device__ __forceinline__ RowInfo row_info(const Fp4GemmParams& p, const Unit& U, int c0, int lane, float gw) {
-  RowInfo r{gw, -1};
-  if (c0 + lane < U.rows) {
-    const int at = U.first + c0 + lane;
-    if (p.a_gs && p.a_gs_per_row) r.g *= __ldg(p.a_gs + at);
-    r.to = at;
-    if (p.out_rows) {
-      r.to = __ldg(p.out_rows + at);
-      if (r.to >= p.m) r.to = -1;
+
+template <int NT, bool RAGGED>
+__device__ __forceinline__ void fill_rows(const Fp4GemmParams& p, const Groups& groups, RowTable<NT>& tab, uint64_t* full,
+                                          uint64_t* empty, int wunits, int u0, int du, int n_units, const Abort& ab) {
+  const int thread = threadIdx.x - 64, lane = threadIdx.x & 31;
+  uint32_t i = 0;
+  for (int u = u0; u < n_units; u += du, ++i) {
+    const uint32_t b = i & 1;
+    if (!__all_sync(0xffffffffu, wait(&empty[b], ((i >> 1) & 1) ^ 1, ab, 106))) break;
+    const Unit U = get_unit<NT, RAGGED>(p, groups, wunits, u);
+    const float gw = (p.w_gs ? __ldg(p.w_gs + U.group) : 1.f) *
+                     (p.a_gs && !p.a_gs_per_row ? __ldg(p.a_gs + U.group) : 1.f);
+    for (int r = thread; r < NT; r += 64) {
+      float g = gw;
+      int to = -1;
+      if (r < U.rows) {
+        const int at = U.first + r;
+        if (p.a_gs && p.a_gs_per_row) g *= __ldg(p.a_gs + at);
+        to = at;
+        if (p.out_rows) {
+          to = __ldg(p.out_rows + at);
+          if (to >= p.m) to = -1;
+        }
+      }
+      tab.g[b][r] = g;
+      tab.to[b][r] = to;
     }
+    if (thread == 0) {
+      tab.rows[b] = U.rows;
+      tab.wtile[b] = U.wtile;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[b]);
   }
-  return r;
-}
-__device__ __forceinline__ float group_scale(const Fp4GemmParams& p, int group) {
-  return (p.w_gs ? __ldg(p.w_gs + group) : 1.f) * (p.a_gs && !p.a_gs_per_row ? __ldg(p.a_gs + group) : 1.f);
 }
 
 // A chunk of 32 activation rows x 32 weight rows (from n0) out of fragments of
