@@ -351,6 +351,18 @@ DENSE = [
     (MX, 1, 37, 129, 96, F32),
     (MX, 1, 200, 64, 160, HF),
     (MX, 2, 200, 130, 288, BF),
+    # one unit shared by a cluster along K (its parts of 16 rows: one, three, four)
+    (MX, 1, 16, 200, 4096, HF),
+    (NV, 1, 40, 100, 4112, BF),
+    (NV, 1, 64, 70, 4096, F32),
+    (NV, 2, 5, 130, 2048, BF),
+    # pairs of SMs, units of 128 rows, then of 256
+    (NV, 1, 520, 2571, 272, F32),
+    (MX, 1, 520, 2576, 160, BF),
+    (NV, 3, 300, 1500, 112, BF),
+    (NV, 1, 1030, 2568, 1296, BF),
+    (MX, 1, 1030, 2568, 160, HF),
+    (MX, 2, 700, 2603, 96, BF),
 ]
 
 
@@ -408,6 +420,9 @@ RAGGED = [
     (NV, [2] * 64 + [0] * 960, 40, 64, 0),                # as many groups as there can be
     (MX, [5, 0, 300, 127, 129], 150, 96, 4),
     (MX, [1] * 30, 70, 160, 2),
+    (NV, [1, 0, 2, 5], 130, 2048, 2),                     # split along K
+    (NV, [100, 0, 128, 129, 65], 300, 528, 3),            # pairs, units of 128 rows
+    (MX, [400, 300, 0, 193], 270, 288, 7),                # pairs, units of 256 rows
 ]
 
 

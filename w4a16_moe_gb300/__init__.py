@@ -401,6 +401,7 @@ class Fp4Config:
                                   int(x_rows), *swiglu, int(x_stride), int(out_stride))
         self._ref = ctypes.byref(self._struct)
         self._sizes = {}
+        self._gather = (-1, None)
 
     def rows(self, ragged):
         return self.m if ragged else self.m * self.num_groups
@@ -441,18 +442,24 @@ def _fp4_x(cfg, x, rows, ragged):
         if n < cfg.rows(ragged):
             raise ValueError(f"x holds {n} rows, {cfg.rows(ragged)} needed")
     elif not 0 < cfg._struct.x_rows <= n:
-        c = _Fp4Config.from_buffer_copy(cfg._struct)
-        c.x_rows = n
-        return ctypes.byref(c)
+        bounded = cfg._gather
+        if bounded[0] != n:
+            c = _Fp4Config.from_buffer_copy(cfg._struct)
+            c.x_rows = n
+            bounded = cfg._gather = (n, ctypes.byref(c))
+        return bounded[1]
     return cfg._ref
+
+
+_U8, _I32, _F32, _Tensor = torch.uint8, torch.int32, torch.float32, torch.Tensor
 
 
 def _fp4_buffer(t, dtype, n, name):
     """Address of a contiguous tensor of at least n elements (None stays None)."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() >= n and t.is_contiguous():
-        return t.data_ptr()
     _need(t, dtype, name)
     raise ValueError(f"{name} needs {n} elements, got {t.numel()}")
 
@@ -497,10 +504,11 @@ def fp4_quantize(cfg: Fp4Config, x, codes, scales, gs=None, values=None, rows=No
     ragged = offsets is not None
     n, code_bytes, scale_bytes, gs_n = cfg._operand(ragged)
     st = _lib.b4_fp4_quantize(
-        _fp4_x(cfg, x, rows, ragged), x.data_ptr(), _fp4_buffer(rows, torch.int32, n, "rows"),
-        _fp4_buffer(offsets, torch.int32, cfg.num_groups + 1, "offsets"), _fp4_buffer(gs, torch.float32, gs_n, "gs"),
-        _fp4_buffer(codes, torch.uint8, code_bytes, "codes"), _fp4_buffer(scales, torch.uint8, scale_bytes, "scales"),
-        _fp4_buffer(values, cfg.x_dtype, n * cfg.k, "values"), _stream_of(stream, x))
+        _fp4_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _fp4_buffer(rows, _I32, n, "rows"),
+        _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None,
+        gs if gs is None else _fp4_buffer(gs, _F32, gs_n, "gs"), _fp4_buffer(codes, _U8, code_bytes, "codes"),
+        _fp4_buffer(scales, _U8, scale_bytes, "scales"),
+        values if values is None else _fp4_buffer(values, cfg.x_dtype, n * cfg.k, "values"), _stream_of(stream, x))
     if st:
         _check(st)
 
@@ -569,13 +577,16 @@ def fp4_linear(cfg: Fp4Config, x, w_codes, w_scales, w_gs, out, workspace, x_gs=
     """
     m = cfg.m
     w_bytes, ws_bytes = cfg._weight_sizes()
+    ragged = offsets is not None
     st = _lib.b4_fp4_linear(
-        _fp4_x(cfg, x, rows, offsets is not None), x.data_ptr(), _fp4_buffer(x_gs, torch.float32, cfg.num_groups, "x_gs"),
-        _fp4_buffer(rows, torch.int32, m, "rows"), _fp4_buffer(offsets, torch.int32, cfg.num_groups + 1, "offsets"),
-        _fp4_buffer(w_codes, torch.uint8, w_bytes, "w_codes"), _fp4_buffer(w_scales, torch.uint8, ws_bytes, "w_scales"),
-        _fp4_buffer(w_gs, torch.float32, cfg.num_groups, "w_gs"), _fp4_buffer(out_rows, torch.int32, m, "out_rows"),
-        _fp4_out(cfg, out, m), _fp4_buffer(workspace, torch.uint8, 0, "workspace"), workspace.numel(),
-        _stream_of(stream, x))
+        _fp4_x(cfg, x, rows, ragged), x.data_ptr(),
+        x_gs if x_gs is None else _fp4_buffer(x_gs, _F32, cfg.num_groups, "x_gs"),
+        rows if rows is None else _fp4_buffer(rows, _I32, m, "rows"),
+        _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None,
+        _fp4_buffer(w_codes, _U8, w_bytes, "w_codes"), _fp4_buffer(w_scales, _U8, ws_bytes, "w_scales"),
+        w_gs if w_gs is None else _fp4_buffer(w_gs, _F32, cfg.num_groups, "w_gs"),
+        out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, m, "out_rows"), _fp4_out(cfg, out, m),
+        _fp4_buffer(workspace, _U8, 0, "workspace"), workspace.numel(), _stream_of(stream, x))
     if st:
         _check(st)
 

@@ -33,8 +33,9 @@ __host__ __device__ constexpr int fp4_group(int fmt) { return fmt == 0 ? 16 : 32
 __host__ __device__ inline int64_t fp4_ld(int k) { return ((int64_t)k / 2 + 15) / 16 * 16; }
 __host__ __device__ inline int fp4_k_tiles(int k, int fmt) { return cdiv(k, 4 * fp4_group(fmt)); }
 
-// Rows of one activation box of a unit of up to nt rows.
-__host__ __device__ constexpr int fp4_box_rows(int) { return 32; }
+// Shared memory for the partial sums of a unit that a cluster splits along K: 8 KB
+// for every other CTA and 16 activation rows.
+constexpr int kSplitPartBytes = 96 * 1024;
 
 struct Fp4QuantParams {
   const void* x;
@@ -61,7 +62,7 @@ struct Fp4QuantParams {
 
 struct Fp4GemmParams {
   CUtensorMap tmap_w;        // weight codes [E N][K/2] bytes, box 128 x 128 rows
-  CUtensorMap tmap_a;        // activation codes [rows][K/2] bytes, box 128 x fp4_box_rows
+  CUtensorMap tmap_a;        // activation codes [rows][K/2] bytes, box 128 x 32 or 64 rows
   CUtensorMap tmap_ws, tmap_as;  // scale tiles of both (pair kernel)
   const uint8_t* w_scales;
   const uint8_t* a_scales;

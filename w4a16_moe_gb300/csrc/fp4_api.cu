@@ -20,8 +20,8 @@ cudaError_t launch_fp4_quantize(const Fp4QuantParams& p, int dtype, int num_sms,
 cudaError_t launch_fp4_tile_scales(const uint8_t* src, uint8_t* dst, int groups, int m, int blocks, int k_tiles,
                                    int num_sms, cudaStream_t stream);
 cudaError_t launch_fp4_combine(const Fp4CombineParams& p, cudaStream_t stream);
-cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, int fmt, int grid, bool pdl, cudaStream_t stream);
-cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& p, int fmt, int pairs, bool pdl, cudaStream_t stream);
+cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, int fmt, int grid, int splits, bool pdl, cudaStream_t stream);
+cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& p, int fmt, int nr, int pairs, bool pdl, cudaStream_t stream);
 }  // namespace b4
 
 using namespace b4;
@@ -131,11 +131,37 @@ Fp4QuantParams quant_params(const b4_fp4_config* c, const void* x, const int32_t
   return p;
 }
 
-// Activation rows of a unit: 64 (one SM a unit), or 192 (a pair of SMs) where
-// groups hold enough rows to fill more of the instruction's N.
-int unit_rows(const b4_fp4_config* c, bool ragged) {
-  const int per = ragged ? c->m / c->num_groups : c->m;
-  return per <= 64 ? 64 : 256;
+// Activation rows of a unit: 64 (fp4_gemm.cu, one SM a unit), 128 or 256
+// (fp4_gemm_pair.cu, a pair of SMs).  The smallest that makes one round of the
+// SMs, else the largest that groups fill.  Measured in us at 64 / 128 / 256: dense
+// N = K = 4096 m = 256 8.2 / 8.8 / 10.7, m = 512 13.3 / 9.2 / 11.1, m = 1024 23 / 13.6 / 11.9;
+// N = 2048 K = 1408 m = 512 5.2 / 6.7 / 8.0, m = 1024 7.4 / 7.0 / 8.2; 28 MXFP4 groups N = K =
+// 2880 of 64 rows each 28.4 / 27.7 / 29.2, 80 rows 41 / 28.3 / 30.3, 160 rows 56 / 40 / 34.
+int unit_rows(const b4_fp4_config* c, bool ragged, int sms) {
+  const int64_t groups = c->num_groups;
+  if (ragged) {  // the rows of a group are known on the device: their mean
+    const int64_t per = c->m / groups;
+    return per <= 64 ? 64 : per <= 128 ? 128 : 256;
+  }
+  if (c->m <= 64 || groups * cdiv(c->m, 64) * cdiv(c->n, 128) <= sms) return 64;
+  if (c->m <= 128 || groups * cdiv(c->m, 128) * cdiv(c->n, 256) <= sms / 2) return 128;
+  return 256;
+}
+
+// CTAs that share a unit along K where the units are fewer than the SMs.  A CTA
+// keeps at least three stages (of 256 K), more where its partial sums are larger
+// (16 rows a part): N = K = 4096 in us at 1 / 2 / 4 / 8 CTAs a unit, m = 1: 9.2 / 7.7 /
+// 7.0 / 7.1, m = 32: 9.3 / 8.4 / 8.0 / 8.0, m = 64: 9.7 / 9.4 / 10.6; K = 2048, N = 8192,
+// m = 64: 7.5 / 8.3.
+int k_splits(const b4_fp4_config* c, int64_t units, int sms) {
+  const int stages = cdiv(c->k, 256);
+  const int parts = cdiv(c->m < 64 ? c->m : 64, 16);
+  const int least = 2 * parts - 1 > 3 ? 2 * parts - 1 : 3;
+  int splits = 8;
+  while (splits > 1 && (splits * units > sms || stages < least * splits ||
+                        (splits - 1) * parts * 8 * 1024 > kSplitPartBytes))
+    splits /= 2;
+  return splits;
 }
 
 b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gs,
@@ -144,11 +170,11 @@ b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const u
                          cudaStream_t stream) {
   const bool ragged = offsets != nullptr;
   Fp4GemmParams p{};
-  const int nt = unit_rows(c, ragged);
+  const int nt = unit_rows(c, ragged, sms);
   const uint64_t ld = (uint64_t)fp4_ld(c->k);
   if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k / 2, ld, 128) ||
       !make_tmap_bytes_2d(&p.tmap_a, a_codes, (uint64_t)operand_rows(c, ragged), c->k / 2, ld,
-                          nt == 64 ? 32 : 64))
+                          nt == 64 ? 32 : nt / 4))
     FP4_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
   p.w_scales = w_scales;
   p.a_scales = a_scales;
@@ -168,19 +194,24 @@ b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const u
   p.vec = aligned(out, 16) && p.out_stride % per16 == 0 && c->n % per16 == 0;
   p.a_is_new = a_is_new;
   p.status = status;
-  // most units the call can have: each group ends at most one unit early
-  const int64_t tok = ragged ? c->m / nt + c->num_groups : (int64_t)cdiv(c->m, nt) * c->num_groups;
+  // most units the call can have: a group ends at most one unit early, and holds
+  // at least one row
+  int64_t tok = (int64_t)cdiv(c->m, nt) * c->num_groups;
+  if (ragged) tok = c->m / nt + c->num_groups < c->m ? c->m / nt + c->num_groups : c->m;
   const int64_t units = tok * cdiv(c->n, nt == 64 ? 128 : 256);
   if (units > (1 << 30)) FP4_INVALID("too many units of work: m, n and num_groups too large together");
-  if (nt == 64)
-    return cuda_status(launch_fp4_gemm(p, c->format, (int)(units < sms ? units : sms), a_is_new, stream), "fp4 product");
+  if (nt == 64) {
+    const int splits = k_splits(c, units, sms);
+    const int grid = (int)(splits > 1 || units < sms ? units : sms);
+    return cuda_status(launch_fp4_gemm(p, c->format, grid, splits, a_is_new, stream), "fp4 product");
+  }
   const uint64_t k_tiles = (uint64_t)fp4_k_tiles(c->k, c->format);
   const uint32_t box = (uint32_t)(c->format == B4_NVFP4_E4M3_K16 ? 4 : 2);
   if (!make_tmap_tiles(&p.tmap_ws, w_scales, (uint64_t)cdiv(c->n, 128) * c->num_groups * k_tiles, box) ||
       !make_tmap_tiles(&p.tmap_as, a_scales, (uint64_t)operand_tiles(c, ragged) * k_tiles, box))
     FP4_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected a scale map");
   const int pairs = (int)(units < sms / 2 ? units : sms / 2);
-  return cuda_status(launch_fp4_gemm_pair(p, c->format, pairs, a_is_new, stream), "fp4 product");
+  return cuda_status(launch_fp4_gemm_pair(p, c->format, nt, pairs, a_is_new, stream), "fp4 product");
 }
 
 // Workspace of b4_fp4_linear: the quantised activation operand (m rows, dense or

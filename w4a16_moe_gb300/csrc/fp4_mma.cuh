@@ -83,6 +83,19 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Abort
   return mbar_test(bar, parity) || wait_long(bar, parity, ab.status, ab.flag, where);
 }
 
+// As wait, for a barrier that other CTAs' asynchronous stores complete.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, const Abort& ab, uint32_t where) {
+  const bool ok = wait(bar, parity, ab, where);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return ok;
+}
+__device__ __forceinline__ void add4(uint32_t* v, const float4& x) {
+  v[0] = __float_as_uint(__uint_as_float(v[0]) + x.x);
+  v[1] = __float_as_uint(__uint_as_float(v[1]) + x.y);
+  v[2] = __float_as_uint(__uint_as_float(v[2]) + x.z);
+  v[3] = __float_as_uint(__uint_as_float(v[3]) + x.w);
+}
+
 // ------------------------------------------------------------------ units
 struct Unit {
   int group, wtile, first, rows;  // first: packed row; rows: live rows
@@ -134,37 +147,48 @@ __device__ __forceinline__ void build_groups(const Fp4GemmParams& p, Groups& g) 
 }
 
 // Unit u: weight rows outermost within a group, so that neighbouring units
-// read the same weights.  wtiles: weight units of a group.
+// read the same weights.  wtiles: weight units of a group.  The search is out of
+// line, one copy for all of a kernel's loops (unrolled over their rings): returns
+// group, weight unit, first packed row, and rows | token tile << 9.
 template <int NT, bool RAGGED>
-__device__ __forceinline__ Unit get_unit(const Fp4GemmParams& p, const Groups& g, int wtiles, int u) {
-  int lo = 0;
-  int t;
-  Unit U;
+__device__ __noinline__ static int4 find_unit(int groups, int m, const Groups* g, int wtiles, int u) {
+  int lo, t, nt, first, rows;
   if constexpr (RAGGED) {
-    int hi = p.groups - 1;  // last group whose tiles start at or before the unit's
+    lo = 0;
+    int hi = groups - 1;  // last group whose tiles start at or before the unit's
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((long long)g.tiles[mid] * wtiles <= u) lo = mid;
+      if ((long long)g->tiles[mid] * wtiles <= u) lo = mid;
       else hi = mid - 1;
     }
-    const int nt = g.tiles[lo + 1] - g.tiles[lo];
-    const int v = u - g.tiles[lo] * wtiles;
-    U.wtile = v / nt;
-    t = v - U.wtile * nt;
-    U.first = g.first[lo] + t * NT;
-    U.rows = min(NT, g.first[lo + 1] - U.first);
-    U.atile = g.first[lo] / 128 + lo + t * NT / 128;
+    nt = g->tiles[lo + 1] - g->tiles[lo];
+    u -= g->tiles[lo] * wtiles;
   } else {
-    const int nt = cdiv(p.m, NT);
-    lo = p.groups == 1 ? 0 : u / (nt * wtiles);
-    const int v = u - lo * nt * wtiles;
-    U.wtile = v / nt;
-    t = v - U.wtile * nt;
-    U.first = lo * p.m + t * NT;
-    U.rows = min(NT, p.m - t * NT);
-    U.atile = lo * cdiv(p.m, 128) + t * NT / 128;
+    nt = cdiv(m, NT);
+    lo = groups == 1 ? 0 : u / (nt * wtiles);
+    u -= lo * nt * wtiles;
   }
-  U.group = lo;
+  const int wtile = nt == 1 ? u : u / nt;
+  t = u - wtile * nt;
+  if constexpr (RAGGED) {
+    first = g->first[lo] + t * NT;
+    rows = min(NT, g->first[lo + 1] - first);
+  } else {
+    first = lo * m + t * NT;
+    rows = min(NT, m - t * NT);
+  }
+  return make_int4(lo, wtile, first, rows | t << 9);
+}
+template <int NT, bool RAGGED>
+__device__ __forceinline__ Unit get_unit(const Fp4GemmParams& p, const Groups& g, int wtiles, int u) {
+  const int4 v = find_unit<NT, RAGGED>(p.groups, p.m, &g, wtiles, u);
+  const int t = v.w >> 9;
+  Unit U;
+  U.group = v.x;
+  U.wtile = v.y;
+  U.first = v.z;
+  U.rows = v.w & 511;
+  U.atile = (RAGGED ? (v.z - t * NT) / 128 + v.x : v.x * cdiv(p.m, 128)) + t * NT / 128;
   U.shift = (t * NT & 127) >> 5;
   return U;
 }

@@ -13,13 +13,14 @@
 // A thread holds chunks of 16 consecutive elements: an NVFP4 block, half an
 // MXFP4 block (the pair joins by one shuffle).  Threads of a row stand side by
 // side, so a chunk is one 32-byte load of a contiguous stretch (two of fp32) and
-// its codes one 8-byte store; a thread loads all of its chunks (four of 16-bit
-// rows, two otherwise) before it uses any, and keeps them between the row's
-// maximum and its codes (longer rows are read again, from L1).  Every step is
-// IEEE fp32 in the order of the formula; h / d is the quotient corrected once by
-// its fused-multiply-add residual (Markstein's scheme: q = h y with y the
-// correctly rounded reciprocal, r = h - q d exactly, q + r y), two elements an
-// instruction, where a division costs a dozen.
+// its codes one 8-byte store; a thread loads all of its chunks (cached_chunks)
+// before it uses any, and keeps them between the row's maximum and its codes
+// (longer rows are read again, from L1).  Every step is IEEE fp32 in the order of
+// the formula, but for h / d, which is h y + h z in one fused multiply-add, y the
+// rounded reciprocal of d and z what it lacks (z = (1 - y d) y, the residual exact):
+// the quotient to 46 bits before its one rounding, so every tie of the codes is
+// met, in two operations an element, two elements an instruction, where a
+// division costs a dozen.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -194,30 +195,36 @@ __device__ __forceinline__ float row_gs(uint32_t a) {
   return __uint_as_float((uint32_t)(max(j, -126) + 127) << 23);
 }
 
-// Quotient a / b of a >= 0 by b within [2^-80, 2^100], y = 1 / b correctly rounded.
-__device__ __forceinline__ float corrected_quotient(float a, float b, float y) {
-  const float q = a * y;
-  return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+// A reciprocal to 46 bits: y the rounded one, z what it lacks.
+struct Recip {
+  float y, z;
+};
+__device__ __forceinline__ Recip recip(float d) {
+  const float y = __frcp_rn(d);
+  return Recip{y, __fmaf_rn(-y, d, 1.f) * y};
 }
+__device__ __forceinline__ float quotient(float a, const Recip& r) { return __fmaf_rn(a, r.y, a * r.z); }
 
 // 6 gs and its reciprocal, for the block scales of a row.
 struct RowScale {
-  float gs, six, inv;
-  bool safe;
+  float gs, six;
+  Recip inv;
+  bool safe;  // the reciprocal's terms stay normal
   __device__ __forceinline__ explicit RowScale(float g) : gs(g) {
     six = __fmul_rn(6.f, g);
-    safe = six >= 0x1p-80f && six <= 0x1p100f;
-    inv = safe ? __frcp_rn(six) : 0.f;
+    safe = six >= 0x1p-80f && six <= 0x1p80f;
+    inv = recip(safe ? six : 1.f);
   }
 };
 
 struct BlockScale {
   uint32_t code;  // the scale's byte
-  float d, inv;   // step of the codes and its reciprocal
-  int kind;       // 0: all codes zero, 1: corrected reciprocal, 2: true division
+  float d;        // step of the codes
+  Recip inv;      // its reciprocal
+  int kind;       // 0: all codes zero, 1: by the reciprocal, 2: true division
 };
 
-// True divisions, for scales outside the range where the residual is exact
+// True divisions, for scales outside the range where the reciprocal's terms are normal
 // (kept out of line: no ordinary block comes here).
 __device__ __noinline__ float true_quotient(float a, float b) { return __fdiv_rn(a, b); }
 
@@ -231,28 +238,29 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t a, const RowScale& r)
                                   : max((int)(a >> 23) - 2 + ((a & 0x7fffffu) > 0x400000u), 0);
     b.code = (uint32_t)e;
     b.d = e == 0 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)e << 23);  // 2^(e - 127)
-    b.inv = e >= 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - e) << 23);
+    b.inv = Recip{e >= 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - e) << 23), 0.f};
     b.kind = e == 255 ? 0 : 1;
     return b;
   }
-  float ratio = corrected_quotient(amax, r.six, r.inv);
-  if (!(r.safe && amax * r.inv < 0x1p20f)) ratio = true_quotient(amax, r.six);
+  float ratio = quotient(amax, r.inv);
+  if (!(r.safe && ratio < 0x1p20f)) ratio = true_quotient(amax, r.six);
   b.code = ratio != ratio ? 0x7fu : (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b.code, __NV_E4M3)));
   b.d = __fmul_rn(s, r.gs);
-  // the residual is exact while no product leaves the normal range
-  const bool safe = b.d >= 0x1p-100f && b.d <= 0x1p100f;
-  b.inv = __frcp_rn(safe ? b.d : 1.f);
-  b.kind = safe && amax * b.inv < 0x1p20f ? 1 : b.d > 0.f && a <= kInfBits ? 2 : 0;
+  const bool safe = b.d >= 0x1p-80f && b.d <= 0x1p80f;
+  b.inv = recip(safe ? b.d : 1.f);
+  b.kind = safe && amax * b.inv.y < 0x1p20f ? 1 : b.d > 0.f && a <= kInfBits ? 2 : 0;
   return b;
 }
 
-// E4M3 scales by code with their correctly rounded reciprocals (0 for the zero
-// scale): under a power-of-two global scale a block's step and its reciprocal
-// are these times 2^j and 2^-j, exactly.
-__device__ __forceinline__ float2 e4m3_and_reciprocal(uint32_t code) {
+// E4M3 scales by code with their reciprocals (0 for the zero scale, whose codes
+// are then zeros): under a power-of-two global scale a block's step and its
+// reciprocal are these times 2^j and 2^-j, exactly.
+__device__ __forceinline__ float4 e4m3_and_reciprocal(uint32_t code) {
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
-  return make_float2(s, s > 0.f ? __frcp_rn(s) : 0.f);
+  if (!(s > 0.f)) return make_float4(s, 0.f, 0.f, 0.f);
+  const Recip r = recip(s);
+  return make_float4(s, r.y, r.z, 0.f);
 }
 
 // Eight fp32 values as E2M1 codes, the first in the low nibble of byte 0.
@@ -269,19 +277,17 @@ __device__ __forceinline__ uint32_t e2m1x8(float2 a, float2 b, float2 c, float2 
   return r;
 }
 
-// E2M1 codes of a chunk, element 2j in the low nibble of byte j, for steps of
-// the corrected reciprocal.
+// E2M1 codes of a chunk, element 2j in the low nibble of byte j, by the step's
+// reciprocal (MXFP4: a power of two, its products exact).
 template <int FMT, typename C>
-__device__ __forceinline__ uint2 encode(const C& h, float d, float inv1) {
-  const uint64_t inv = pack2(inv1, inv1), nd = pack2(-d, -d);
+__device__ __forceinline__ uint2 encode(const C& h, const Recip& r) {
+  const uint64_t y = pack2(r.y, r.y), z = pack2(r.z, r.z);
   float2 q[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float2 x = h.pair(j);
     const uint64_t xx = pack2(x.x, x.y);
-    uint64_t r = mul2(xx, inv);  // MXFP4: exact, a power of two
-    if (FMT == 0) r = fma2(fma2(r, nd, xx), inv, r);
-    q[j] = unpack2(r);
+    q[j] = unpack2(FMT == 0 ? fma2(xx, y, mul2(xx, z)) : mul2(xx, y));
   }
   return make_uint2(e2m1x8(q[0], q[1], q[2], q[3]), e2m1x8(q[4], q[5], q[6], q[7]));
 }
@@ -324,28 +330,29 @@ __device__ __forceinline__ void store_values(T* dst, int level, const uint2& w, 
   store_words(dst, level, o);
 }
 
-// Chunks a thread keeps, and resident blocks asked of the compiler (4096 rows of
-// 4096 bf16: 12.9 us; 13.8 with two chunks, 14.9 with four at half the blocks).
+// Chunks a thread keeps, and resident blocks asked of the compiler: 4096 rows of
+// 4096 bf16 12.0 us (13.2 with two chunks and ten blocks), 2048 SwiGLU rows of 1408
+// 7.1 us (7.9 with two chunks and six blocks, 8.3 with one and six).
 template <typename T, bool ACT>
 __host__ __device__ constexpr int cached_chunks() {
   return ACT ? 1 : sizeof(T) == 2 ? 4 : 2;
 }
 template <typename T, bool ACT>
 __host__ __device__ constexpr int resident_blocks() {
-  return !ACT && sizeof(T) == 2 ? 8 : 6;
+  return ACT ? 8 : sizeof(T) == 2 ? 7 : 6;
 }
 
 }  // namespace
 
 // tpr_log2: threads per row.  Rows beyond the operand (pad_rows) only clear
 // their scales.
-template <typename T, int FMT, bool ACT, bool ROW>
+template <typename T, int FMT, bool ACT, bool ROW, bool VALUES>
 __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quantize_kernel(const __grid_constant__ Fp4QuantParams p,
                                                                  int tpr_log2) {
   constexpr int kCached = cached_chunks<T, ACT>();
   constexpr int kPerTile = FMT == 0 ? 4 : 8;  // chunks of a scale tile
   __shared__ uint32_t s_max[kQThreads / 32];
-  __shared__ float2 s_e4m3[ROW ? 128 : 1];
+  __shared__ float4 s_e4m3[ROW ? 128 : 1];
   const int tpr = 1 << tpr_log2;
   const int t = threadIdx.x & (tpr - 1);
   const int lane = threadIdx.x & 31;
@@ -434,56 +441,64 @@ __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quan
   const RowScale rs(gs);
   const float inv_gs = ROW ? __frcp_rn(rs.safe ? gs : 1.f) : 0.f;
 
-  uint8_t* codes = p.codes + row * p.ld;
-  T* values = p.values ? reinterpret_cast<T*>(p.values) + row * p.k : nullptr;
-  // scale of block b: row-major at [row][b], tiled in byte b % 4 of the row's word of tile b / 4
-  uint8_t* scales = p.rowmajor_scales ? p.scales + row * (p.k / (FMT == 0 ? 16 : 32))
-                                      : p.scales + tile * p.k_tiles * kSfTile + (lr & 31) * 16 + ((lr >> 5) & 3) * 4;
-  const bool scaled = p.rowmajor_scales ? live : live || pad;
-  const int scale_chunks = p.rowmajor_scales ? chunks : p.k_tiles * kPerTile;
+  // this thread's first chunk in each output, and the way to its next one; the
+  // scale of block b is at [row][b] or, tiled, in byte b % 4 of the row's word of
+  // tile b / 4 (an MXFP4 block's even chunk stores it)
+  uint8_t* codes = p.codes + row * p.ld + 8 * t;
+  T* values = VALUES ? reinterpret_cast<T*>(p.values) + row * p.k + 16 * t : nullptr;
+  const int blk = FMT == 0 ? t : t >> 1, blk_step = FMT == 0 ? tpr : tpr >> 1;
+  uint8_t* scales;
+  int scale_step, scale_chunks;  // chunks that have a scale to store
+  if (p.rowmajor_scales) {
+    scales = p.scales + row * (p.k / (FMT == 0 ? 16 : 32)) + blk;
+    scale_step = blk_step;
+    scale_chunks = chunks;
+  } else {
+    scales = p.scales + (tile * p.k_tiles + (blk >> 2)) * kSfTile + (lr & 31) * 16 + ((lr >> 5) & 3) * 4 + (blk & 3);
+    scale_step = (blk_step >> 2) * kSfTile;
+    scale_chunks = live || pad ? p.k_tiles * kPerTile : 0;
+  }
+  if (FMT != 0 && (t & 1)) scale_chunks = 0;
 
-  auto emit = [&](int c, const Chunk<T, ACT>& v, uint32_t a) {
+  auto emit = [&](int it, const Chunk<T, ACT>& v, uint32_t a) {
+    const int c = it * tpr + t;
     uint32_t code;
     uint2 w;
     float d;
     if (ROW && rs.safe) {
       // every block's largest magnitude is within 6 448 gs
-      code = (uint32_t)__nv_cvt_float_to_fp8(corrected_quotient(__uint_as_float(a), rs.six, rs.inv), __NV_SATFINITE,
-                                             __NV_E4M3);
-      const float2 s = s_e4m3[code];
+      code = (uint32_t)__nv_cvt_float_to_fp8(quotient(__uint_as_float(a), rs.inv), __NV_SATFINITE, __NV_E4M3);
+      const float4 s = s_e4m3[code];
       d = s.x * gs;
-      w = encode<FMT>(v, d, s.y * inv_gs);
+      w = encode<FMT>(v, Recip{s.y * inv_gs, s.z * inv_gs});
       if (code == 0) w = make_uint2(0, 0);
     } else {
       if (FMT != 0) a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
       const BlockScale b = block_scale<FMT>(a, rs);
       code = b.code;
       d = b.d;
-      w = encode<FMT>(v, d, b.inv);
+      w = encode<FMT>(v, b.inv);
       if (FMT == 0 && b.kind == 2) w = encode_by_division(v, d);
       if (b.kind == 0) w = make_uint2(0, 0);
     }
-    const int64_t at = 16 * (int64_t)c;
     if (c < chunks) {
-      *reinterpret_cast<uint2*>(codes + at / 2) = w;
-      if (values) store_values(values + at, p.values_vec, w, d, code == (FMT == 0 ? 0x7fu : 255u));
+      *reinterpret_cast<uint2*>(codes + (int64_t)it * (8 * tpr)) = w;
+      if constexpr (VALUES)
+        store_values(values + (int64_t)it * (16 * tpr), p.values_vec, w, d, code == (FMT == 0 ? 0x7fu : 255u));
     } else {
       code = 0;
     }
-    if (scaled && c < scale_chunks && (FMT == 0 || !(c & 1))) {
-      const int b = FMT == 0 ? c : c >> 1;
-      scales[p.rowmajor_scales ? b : (b >> 2) * kSfTile + (b & 3)] = (uint8_t)code;
-    }
+    if (c < scale_chunks) scales[(int64_t)it * scale_step] = (uint8_t)code;
   };
 #pragma unroll
   for (int it = 0; it < kCached; ++it)
-    if (it < n_it) emit(it * tpr + t, h[it], amax[it]);
+    if (it < n_it) emit(it, h[it], amax[it]);
   for (int it = kCached; it < n_it; ++it) {
     const int c = it * tpr + t;
     Chunk<T, ACT> v;
     if (c < filled) v.get(p, x, c);
     else v.zero();
-    emit(c, v, v.amax());
+    emit(it, v, v.amax());
   }
 }
 
@@ -625,12 +640,11 @@ cudaError_t quantize_t(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStrea
     e = launch_pdl(fp4_gs_kernel, dim3(cdiv(p.groups, 256)), dim3(256), 0, false, stream, p.gs, p.groups);
     if (e != cudaSuccess) return e;
   }
+  auto go = [&](auto kern) { return launch_pdl(kern, dim3((unsigned)grid), dim3(kQThreads), 0, pdl, stream, p, lg); };
   if constexpr (FMT == 0)
     if (p.gs_mode == kGsRow)
-      return launch_pdl(fp4_quantize_kernel<T, FMT, ACT, true>, dim3((unsigned)grid), dim3(kQThreads), 0, pdl, stream, p,
-                        lg);
-  return launch_pdl(fp4_quantize_kernel<T, FMT, ACT, false>, dim3((unsigned)grid), dim3(kQThreads), 0, pdl, stream, p,
-                    lg);
+      return p.values ? go(fp4_quantize_kernel<T, FMT, ACT, true, true>) : go(fp4_quantize_kernel<T, FMT, ACT, true, false>);
+  return p.values ? go(fp4_quantize_kernel<T, FMT, ACT, false, true>) : go(fp4_quantize_kernel<T, FMT, ACT, false, false>);
 }
 
 template <typename T>
