@@ -509,6 +509,69 @@ def test_linear(b4, fmt, dtype, m, n, k, act):
     assert torch.equal(out, again)
 
 
+FEW = [
+    # fmt, x dtype, out dtype, m, n, k, act, gs mode, x shift, row padding
+    (NV, BF, BF, 1, 130, 4096, None, "row", 0, 0), (NV, F32, F32, 2, 1, 16, None, "row", 0, 0),
+    (NV, HF, HF, 3, 257, 1040, None, "row", 3, 9), (NV, BF, F32, 4, 128, 2320, None, "row", 1, 2),
+    (NV, F32, BF, 5, 90, 528, None, "row", 1, 5), (NV, BF, BF, 4, 200, 208, None, "given", 0, 8),
+    (MX, BF, HF, 2, 150, 2880, None, "none", 0, 0), (MX, F32, F32, 3, 40, 32, None, "none", 1, 0),
+    (MX, HF, BF, 4, 129, 288, None, "none", 5, 1), (NV, BF, BF, 3, 140, 1424, "silu", "row", 0, 0),
+    (NV, HF, F32, 4, 60, 80, "swiglu_oai", "row", 2, 4), (MX, BF, BF, 2, 30, 96, "silu", "none", 1, 1),
+    (NV, F32, F32, 2, 70, 272, "relu2", "given", 0, 0),
+]
+
+
+@pytest.mark.parametrize("fmt,dtype,odtype,m,n,k,act,mode,shift,pad", FEW)
+def test_linear_of_few_rows(b4, fmt, dtype, odtype, m, n, k, act, mode, shift, pad):
+    """Few rows are quantised by the product's own kernel: the same bits as the two calls, an infinite and a NaN
+    row among them, from strided and unaligned rows, and nothing written past the output's rows."""
+    width = 2 * k if act in ("silu", "swiglu_oai") else k
+    stride = width + pad
+    base = _randn((m * stride + shift,), 43, dtype).cuda()
+    x = base[shift:].view(m, stride)[:, :width]
+    if m > 2:
+        x[1, width // 2] = float("inf")
+        x[2, 0] = float("nan")
+    cfg = b4.Fp4Config(m=m, n=n, k=k, format=b4.FORMATS[fmt], x_dtype=dtype, out_dtype=odtype, x_stride=stride,
+                       out_stride=n + pad, activation=b4.ACTIVATIONS.get(act), gs_mode=getattr(b4, "GS_" + mode.upper()))
+    gs = torch.full((1,), 2.0**-8, device="cuda") if mode == "given" else None
+    _, wd = _weights(fmt, 1, n, k, 44)
+    parts = b4.fp4_empty(cfg, "cuda")
+    if mode == "given":
+        parts[2].copy_(gs)
+    b4.fp4_quantize(cfg, x, *parts)
+    want, got = (torch.full((m + 1, n + pad), 7.0, dtype=odtype, device="cuda") for _ in range(2))
+    b4.fp4_matmul(cfg, *parts, *wd, want[:m, :n])
+    ws = torch.empty(b4.fp4_linear_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    b4.fp4_linear(cfg, x, *wd, got[:m, :n], ws, **({} if gs is None else {"x_gs": gs}))
+    b4.check_status(ws)
+    torch.testing.assert_close(got, want, rtol=0, atol=0, equal_nan=True)
+    assert torch.isfinite(got[0]).all() and torch.all(got[m] == 7.0) and torch.all(got[:, n:] == 7.0)
+
+
+@pytest.mark.parametrize("fmt,k", [(NV, 80), (NV, 2064), (MX, 2048)])
+@pytest.mark.parametrize("counts", [[1] * 8, [8], [0, 3, 0, 0, 4], [0, 0], [2, 1, 5]])
+def test_grouped_linear_of_few_rows(b4, fmt, k, counts):
+    """As above for a few gathered rows by group, in place and scattered: groups empty, of one row and of all."""
+    n, e, tokens, div = 140, len(counts), 5, 2
+    m = 8
+    off = dev(np.concatenate(([0], np.cumsum(counts))).astype(np.int32))
+    rows = dev(np.array([3, 0, 9, -1, 4, 11, 1, 8], dtype=np.int32))  # -1 and 11 / 2 are no token: zero rows
+    to = dev(np.array([5, 2, -1, 0, 8, 7, 1, 3], dtype=np.int32))     # -1 and 8 are dropped
+    x = _randn((tokens, k), 45, BF).cuda()
+    cfg = b4.Fp4Config(m=m, n=n, k=k, num_groups=e, format=b4.FORMATS[fmt], row_div=div)
+    _, wd = _weights(fmt, e, n, k, 46)
+    parts = b4.fp4_empty(cfg, "cuda", ragged=True)
+    b4.fp4_quantize(cfg, x, *parts, rows=rows, offsets=off)
+    ws = torch.empty(b4.fp4_linear_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    for out_rows in (None, to):
+        want, got = (torch.full((m, n), 7.0, dtype=BF, device="cuda") for _ in range(2))
+        b4.fp4_matmul(cfg, *parts, *wd, want, offsets=off, out_rows=out_rows)
+        b4.fp4_linear(cfg, x, *wd, got, ws, rows=rows, offsets=off, out_rows=out_rows)
+        b4.check_status(ws)
+        assert torch.equal(got, want) and torch.isfinite(got).all()
+
+
 def test_grouped_linear_from_packed_routes(b4):
     """Routes packed by b4_route_pack (drops included), rows gathered, outputs by expert."""
     wl = W.WORKLOADS["mxfp4"].scaled(hidden=160, inter=96, experts=7)

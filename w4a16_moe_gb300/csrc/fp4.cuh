@@ -37,6 +37,12 @@ __host__ __device__ inline int fp4_k_tiles(int k, int fmt) { return cdiv(k, 4 * 
 // for every other CTA and 16 activation rows.
 constexpr int kSplitPartBytes = 96 * 1024;
 
+// Direct products: rows of a call that the kernel quantises for itself (a ragged call's
+// groups share them), rows of its operand in shared memory (the instruction's least N),
+// and stages of 256 K of them that a CTA keeps.
+constexpr int kDirectRows = 8, kDirectDenseRows = 4, kDirectTile = 16;
+__host__ __device__ constexpr int fp4_direct_stages(bool split) { return split ? 6 : 16; }
+
 struct Fp4QuantParams {
   const void* x;
   int64_t x_stride;          // elements between rows
@@ -76,6 +82,8 @@ struct Fp4GemmParams {
   int64_t out_stride;        // elements
   int out_dtype;             // 0 bf16, 1 f16, 2 f32
   int vec;                   // rows of out are 16-byte aligned and n fills them
+  Fp4QuantParams q;          // direct: the rows the kernel quantises for itself
+  int x_dtype, clear_status;
   int a_is_new;              // the activation operand comes from the kernel before (programmatic launch)
   uint32_t* status;          // or null
 };

@@ -21,6 +21,7 @@ cudaError_t launch_fp4_tile_scales(const uint8_t* src, uint8_t* dst, int groups,
                                    int num_sms, cudaStream_t stream);
 cudaError_t launch_fp4_combine(const Fp4CombineParams& p, cudaStream_t stream);
 cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, int fmt, int grid, int splits, bool pdl, cudaStream_t stream);
+cudaError_t launch_fp4_gemm_direct(const Fp4GemmParams& p, int fmt, int grid, int splits, bool pdl, cudaStream_t stream);
 cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& p, int fmt, int nr, int pairs, bool pdl, cudaStream_t stream);
 }  // namespace b4
 
@@ -164,23 +165,20 @@ int k_splits(const b4_fp4_config* c, int64_t units, int sms) {
   return splits;
 }
 
-b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gs,
-                         const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gs, const int32_t* offsets,
-                         const int32_t* out_rows, void* out, uint32_t* status, bool a_is_new, int sms,
-                         cudaStream_t stream) {
-  const bool ragged = offsets != nullptr;
+// Most units a call can have: a group ends at most one unit early, and holds at
+// least one row.
+int64_t most_units(const b4_fp4_config* c, bool ragged, int nt) {
+  int64_t tok = (int64_t)cdiv(c->m, nt) * c->num_groups;
+  if (ragged) tok = c->m / nt + c->num_groups < c->m ? c->m / nt + c->num_groups : c->m;
+  return tok * cdiv(c->n, nt == 64 ? 128 : 256);
+}
+
+// The fields of a product that do not depend on where its activations come from.
+Fp4GemmParams product_params(const b4_fp4_config* c, const uint8_t* w_scales, const float* w_gs, const int32_t* offsets,
+                             const int32_t* out_rows, void* out, uint32_t* status) {
   Fp4GemmParams p{};
-  const int nt = unit_rows(c, ragged, sms);
-  const uint64_t ld = (uint64_t)fp4_ld(c->k);
-  if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k / 2, ld, 128) ||
-      !make_tmap_bytes_2d(&p.tmap_a, a_codes, (uint64_t)operand_rows(c, ragged), c->k / 2, ld,
-                          nt == 64 ? 32 : nt / 4))
-    FP4_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
   p.w_scales = w_scales;
-  p.a_scales = a_scales;
   p.w_gs = w_gs;
-  p.a_gs = a_gs;
-  p.a_gs_per_row = c->gs_mode == B4_FP4_GS_ROW;
   p.groups = c->num_groups;
   p.m = c->m;
   p.n = c->n;
@@ -192,13 +190,54 @@ b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const u
   p.out_dtype = c->out_dtype;
   const int per16 = 16 / dtype_bytes(c->out_dtype);
   p.vec = aligned(out, 16) && p.out_stride % per16 == 0 && c->n % per16 == 0;
-  p.a_is_new = a_is_new;
   p.status = status;
-  // most units the call can have: a group ends at most one unit early, and holds
-  // at least one row
-  int64_t tok = (int64_t)cdiv(c->m, nt) * c->num_groups;
-  if (ragged) tok = c->m / nt + c->num_groups < c->m ? c->m / nt + c->num_groups : c->m;
-  const int64_t units = tok * cdiv(c->n, nt == 64 ? 128 : 256);
+  return p;
+}
+
+// K splits of a direct product (0: the call takes the two launches): few rows, every
+// unit has a CTA or a cluster of its own, and a CTA's part of the quantised rows fits
+// in shared memory.  One launch saves 2 us of the caller's time; on the GPU alone
+// (N = K = 4096) it takes 6.6 / 6.9 / 7.3 / 8.6 us for 1 / 2 / 4 / 8 rows of a unit where
+// two launches take 7.0.  A ragged call of 8 rows has them in a unit only if all chose
+// the same expert; 8 rows in 8 groups take 10.4 (two launches 10.7, 128 experts, N 1408, K 2048).
+int direct_splits(const b4_fp4_config* c, bool ragged, int sms) {
+  if (c->m > (ragged ? kDirectRows : kDirectDenseRows)) return 0;
+  const int64_t units = most_units(c, ragged, 64);
+  if (units > sms) return 0;
+  const int splits = k_splits(c, units, sms);
+  return cdiv(cdiv(c->k, 256), splits) <= fp4_direct_stages(splits > 1) ? splits : 0;
+}
+
+b4_status launch_direct(const b4_fp4_config* c, const Fp4QuantParams& q, const uint8_t* w_codes, const uint8_t* w_scales,
+                        const float* w_gs, const int32_t* out_rows, void* out, uint32_t* clear, uint32_t* status,
+                        int splits, cudaStream_t stream) {
+  Fp4GemmParams p = product_params(c, w_scales, w_gs, q.offsets, out_rows, out, status);
+  if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k / 2, (uint64_t)fp4_ld(c->k), 128))
+    FP4_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
+  p.q = q;
+  p.x_dtype = c->x_dtype;
+  p.clear_status = clear != nullptr;
+  return cuda_status(launch_fp4_gemm_direct(p, c->format, (int)most_units(c, q.offsets, 64), splits, true, stream),
+                     "fp4 product");
+}
+
+b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gs,
+                         const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gs, const int32_t* offsets,
+                         const int32_t* out_rows, void* out, uint32_t* status, bool a_is_new, int sms,
+                         cudaStream_t stream) {
+  const bool ragged = offsets != nullptr;
+  Fp4GemmParams p = product_params(c, w_scales, w_gs, offsets, out_rows, out, status);
+  const int nt = unit_rows(c, ragged, sms);
+  const uint64_t ld = (uint64_t)fp4_ld(c->k);
+  if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k / 2, ld, 128) ||
+      !make_tmap_bytes_2d(&p.tmap_a, a_codes, (uint64_t)operand_rows(c, ragged), c->k / 2, ld,
+                          nt == 64 ? 32 : nt / 4))
+    FP4_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
+  p.a_scales = a_scales;
+  p.a_gs = a_gs;
+  p.a_gs_per_row = c->gs_mode == B4_FP4_GS_ROW;
+  p.a_is_new = a_is_new;
+  const int64_t units = most_units(c, ragged, nt);
   if (units > (1 << 30)) FP4_INVALID("too many units of work: m, n and num_groups too large together");
   if (nt == 64) {
     const int splits = k_splits(c, units, sms);
@@ -236,8 +275,8 @@ LinearWs linear_ws(const b4_fp4_config* c) {
   return L;
 }
 
-// Quantise into `ws` and multiply: two launches, the second a programmatic
-// dependent of the first.
+// Quantise and multiply: one launch for a few rows, else one into `ws` and one that
+// is a programmatic dependent of it.
 b4_status quantize_and_multiply(const b4_fp4_config* c, const void* x, const float* x_gs, const int32_t* rows,
                                 const int32_t* offsets, const uint8_t* w_codes, const uint8_t* w_scales,
                                 const float* w_gs, const int32_t* out_rows, void* out, uint8_t* ws, uint32_t* clear,
@@ -247,6 +286,8 @@ b4_status quantize_and_multiply(const b4_fp4_config* c, const void* x, const flo
   uint8_t* scales = ws + L.scales;
   float* gs = c->gs_mode == B4_FP4_GS_ROW ? reinterpret_cast<float*>(ws + L.gs) : const_cast<float*>(x_gs);
   Fp4QuantParams q = quant_params(c, x, rows, offsets, gs, codes, scales);
+  if (const int splits = direct_splits(c, offsets, sms))
+    return launch_direct(c, q, w_codes, w_scales, w_gs, out_rows, out, clear, status, splits, stream);
   q.status = clear;
   cudaError_t e = launch_fp4_quantize(q, c->x_dtype, sms, true, stream);
   if (e != cudaSuccess) return cuda_status(e, "fp4 quantise");
