@@ -145,16 +145,13 @@ __device__ __forceinline__ void quantize_unit(const Fp4GemmParams& p, const Unit
     else h.zero();
     uint32_t a = h.amax();
     if (FMT != 0) a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    const BlockScale b = block_scale<FMT>(a, rs);
-    uint2 w = encode<FMT>(h, b.inv);
-    if (FMT == 0 && b.kind == 2) w = encode_by_division(h, b.d);
-    if (b.kind == 0 || c >= chunks) w = make_uint2(0, 0);
-    const uint32_t code = c < chunks ? b.code : 0;
+    Quantized o = quantize_block<FMT>(h, a, rs);
+    if (c >= chunks) o.w = make_uint2(0, 0), o.code = 0;
     const int st = (c >> 4) - s_beg, in = c & 15;
     if (live && c < 16 * s_end) {
-      *reinterpret_cast<uint2*>(row_a + st * (kDirectTile * 128) + (((in >> 1) ^ (r & 7)) << 4) + (in & 1) * 8) = w;
-      if (FMT == 0) s_sf[st * kSfBytes + (in >> 2) * kSfTile + r * 16 + (in & 3)] = (uint8_t)code;
-      else if (!(in & 1)) s_sf[st * kSfBytes + (in >> 3) * kSfTile + r * 16 + ((in >> 1) & 3)] = (uint8_t)code;
+      *reinterpret_cast<uint2*>(row_a + st * (kDirectTile * 128) + (((in >> 1) ^ (r & 7)) << 4) + (in & 1) * 8) = o.w;
+      if (FMT == 0) s_sf[st * kSfBytes + (in >> 2) * kSfTile + r * 16 + (in & 3)] = (uint8_t)o.code;
+      else if (!(in & 1)) s_sf[st * kSfBytes + (in >> 3) * kSfTile + r * 16 + ((in >> 1) & 3)] = (uint8_t)o.code;
     }
   }
 }

@@ -41,6 +41,38 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Of these a NaN operand gives NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // N words (8 or 16) from or to consecutive global memory.  level 2: 32-byte
 // aligned, 1: 16-byte.
 template <int N>
@@ -111,26 +143,28 @@ template <>
 __device__ __forceinline__ float2 Raw<float>::pair(int i) const {
   return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
 }
-__device__ __forceinline__ uint32_t amax16x2(const uint32_t (&w)[8]) {
-  uint32_t m = w[0] & 0x7fff7fffu;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
-  return max(m >> 16, m & 0xffffu);
-}
+// (the maximum of magnitudes with the operands' signs multiplied: the sign is dropped at the end)
 template <>
 __device__ __forceinline__ uint32_t Raw<__nv_bfloat16>::amax() const {
-  return amax16x2(w) << 16;
+  uint32_t m = w[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+  return max(m << 16 & 0x7fff0000u, m & 0x7fff0000u);
 }
 template <>
 __device__ __forceinline__ uint32_t Raw<__half>::amax() const {
-  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)amax16x2(w))));
+  uint32_t m = w[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) asm("max.NaN.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+  m = max(m >> 16 & 0x7fffu, m & 0x7fffu);
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
 }
 template <>
 __device__ __forceinline__ uint32_t Raw<float>::amax() const {
-  uint32_t a = 0;
+  float a = __uint_as_float(w[0] & 0x7fffffffu);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) a = max(a, w[i] & 0x7fffffffu);
-  return a;
+  for (int i = 1; i < 15; i += 2) a = max3_abs_nan(a, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+  return __float_as_uint(max3_abs_nan(a, __uint_as_float(w[15]), 0.f));
 }
 
 // Chunk c of a row: as it is, or through the activation in fp32.
@@ -144,19 +178,30 @@ struct Chunk<T, true> : Raw<float> {
     Raw<T> g, u;
     g.load(row + 16 * c, p.vec);
     if (p.act == 0) {
+      // g sigmoid(alpha g) (u + beta) of the clamped g and u, two columns an instruction; the
+      // exponential and the reciprocal are the machine's approximations (2^-22 each), and
+      // the sigmoid is 0 where 1 + e^(-alpha g) passes 2^126
       u.load(row + p.k + 16 * c, p.vec);
+      const float limit = p.glu.limit, scale = -1.44269504f * p.glu.alpha;
+      const uint64_t scale2 = pack2(scale, scale), beta2 = pack2(p.glu.beta, p.glu.beta), one2 = pack2(1.f, 1.f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 a = g.pair(i), b = u.pair(i);
-        this->w[2 * i] = __float_as_uint(gated_act(a.x, b.x, p.glu));
-        this->w[2 * i + 1] = __float_as_uint(gated_act(a.y, b.y, p.glu));
+        const uint64_t gc = pack2(min_nan(a.x, limit), min_nan(a.y, limit));
+        const uint64_t uc = pack2(max_nan(min_nan(b.x, limit), -limit), max_nan(min_nan(b.y, limit), -limit));
+        const float2 t = unpack2(mul2(gc, scale2));
+        const float2 d = unpack2(add2(pack2(exp2_approx(t.x), exp2_approx(t.y)), one2));
+        const float2 h = unpack2(mul2(mul2(gc, pack2(rcp_approx(d.x), rcp_approx(d.y))), add2(uc, beta2)));
+        this->w[2 * i] = __float_as_uint(h.x);
+        this->w[2 * i + 1] = __float_as_uint(h.y);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {  // NaN stays NaN
+      for (int i = 0; i < 8; ++i) {
         const float2 a = g.pair(i);
-        this->w[2 * i] = __float_as_uint(a.x < 0.f ? 0.f : a.x * a.x);
-        this->w[2 * i + 1] = __float_as_uint(a.y < 0.f ? 0.f : a.y * a.y);
+        const float x = max_nan(a.x, 0.f), y = max_nan(a.y, 0.f);
+        this->w[2 * i] = __float_as_uint(x * x);
+        this->w[2 * i + 1] = __float_as_uint(y * y);
       }
     }
   }
@@ -173,12 +218,13 @@ __device__ __forceinline__ float row_gs(uint32_t a) {
   return __uint_as_float((uint32_t)(max(j, -126) + 127) << 23);
 }
 
-// A reciprocal to 46 bits: y the rounded one, z what it lacks.
+// A reciprocal of a number from 2^-92 to 2^92, to 46 bits: y the machine's approximation
+// (2^-23), z what it lacks, from the exact residual.
 struct Recip {
   float y, z;
 };
 __device__ __forceinline__ Recip recip(float d) {
-  const float y = __frcp_rn(d);
+  const float y = rcp_approx(d);
   return Recip{y, __fmaf_rn(-y, d, 1.f) * y};
 }
 __device__ __forceinline__ float quotient(float a, const Recip& r) { return __fmaf_rn(a, r.y, a * r.z); }
@@ -195,51 +241,9 @@ struct RowScale {
   }
 };
 
-struct BlockScale {
-  uint32_t code;  // the scale's byte
-  float d;        // step of the codes
-  Recip inv;      // its reciprocal
-  int kind;       // 0: all codes zero, 1: by the reciprocal, 2: true division
-};
-
-// True divisions, for scales outside the range where the reciprocal's terms are normal
-// (kept out of line: no ordinary block comes here).
-static __device__ __noinline__ float true_quotient(float a, float b) { return __fdiv_rn(a, b); }
-
-template <int FMT>
-__device__ __forceinline__ BlockScale block_scale(uint32_t a, const RowScale& r) {
-  BlockScale b;
-  const float amax = __uint_as_float(a);
-  if constexpr (FMT != 0) {
-    const int e = a > kInfBits ? 255
-                  : a == kInfBits ? 254
-                                  : max((int)(a >> 23) - 2 + ((a & 0x7fffffu) > 0x400000u), 0);
-    b.code = (uint32_t)e;
-    b.d = e == 0 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)e << 23);  // 2^(e - 127)
-    b.inv = Recip{e >= 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - e) << 23), 0.f};
-    b.kind = e == 255 ? 0 : 1;
-    return b;
-  }
-  float ratio = quotient(amax, r.inv);
-  if (!(r.safe && ratio < 0x1p20f)) ratio = true_quotient(amax, r.six);
-  b.code = ratio != ratio ? 0x7fu : (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
-  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b.code, __NV_E4M3)));
-  b.d = __fmul_rn(s, r.gs);
-  const bool safe = b.d >= 0x1p-80f && b.d <= 0x1p80f;
-  b.inv = recip(safe ? b.d : 1.f);
-  b.kind = safe && amax * b.inv.y < 0x1p20f ? 1 : b.d > 0.f && a <= kInfBits ? 2 : 0;
-  return b;
-}
-
-// E4M3 scales by code with their reciprocals (0 for the zero scale, whose codes
-// are then zeros): under a power-of-two global scale a block's step and its
-// reciprocal are these times 2^j and 2^-j, exactly.
-__device__ __forceinline__ float4 e4m3_and_reciprocal(uint32_t code) {
-  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
-  if (!(s > 0.f)) return make_float4(s, 0.f, 0.f, 0.f);
-  const Recip r = recip(s);
-  return make_float4(s, r.y, r.z, 0.f);
-}
+// The number an E4M3 code without its sign stands for (not NaN): its bits are the top of an
+// fp32's, but for the exponent's bias.
+__device__ __forceinline__ float e4m3_value(uint32_t code) { return __uint_as_float(code << 20) * 0x1p120f; }
 
 // Eight fp32 values as E2M1 codes, the first in the low nibble of byte 0.
 __device__ __forceinline__ uint32_t e2m1x8(float2 a, float2 b, float2 c, float2 d) {
@@ -269,6 +273,9 @@ __device__ __forceinline__ uint2 encode(const C& h, const Recip& r) {
   }
   return make_uint2(e2m1x8(q[0], q[1], q[2], q[3]), e2m1x8(q[4], q[5], q[6], q[7]));
 }
+// True divisions, for steps outside the range where the reciprocal's terms are normal
+// (kept out of line: no ordinary block comes here).
+static __device__ __noinline__ float true_quotient(float a, float b) { return __fdiv_rn(a, b); }
 template <typename C>
 __device__ __forceinline__ uint2 encode_by_division(const C& h, float d) {
   float2 q[8];
@@ -278,6 +285,44 @@ __device__ __forceinline__ uint2 encode_by_division(const C& h, float d) {
     q[j] = make_float2(true_quotient(x.x, d), true_quotient(x.y, d));
   }
   return make_uint2(e2m1x8(q[0], q[1], q[2], q[3]), e2m1x8(q[4], q[5], q[6], q[7]));
+}
+
+// A quantised chunk: its codes, the byte of its scale, the step of its codes.
+struct Quantized {
+  uint2 w;
+  uint32_t code;
+  float d;
+};
+
+// Chunk h with the bits a of its block's largest magnitude, in a row of scales r.
+template <int FMT, typename C>
+__device__ __forceinline__ Quantized quantize_block(const C& h, uint32_t a, const RowScale& r) {
+  Quantized q;
+  if constexpr (FMT != 0) {
+    const int e = a > kInfBits ? 255
+                  : a == kInfBits ? 254
+                                  : max((int)(a >> 23) - 2 + ((a & 0x7fffffu) > 0x400000u), 0);
+    q.code = (uint32_t)e;
+    q.d = e == 0 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)e << 23);  // 2^(e - 127)
+    const float inv = e >= 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - e) << 23);
+    q.w = encode<FMT>(h, Recip{inv, 0.f});
+    if (e == 255) q.w = make_uint2(0, 0);
+    return q;
+  }
+  const float amax = __uint_as_float(a);
+  float ratio = quotient(amax, r.inv);
+  if (r.safe && ratio < 0x1p20f) {  // every block, unless a scale was given that is far off
+    q.code = (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
+    q.d = e4m3_value(q.code) * r.gs;
+    q.w = encode<FMT>(h, recip(q.d));
+    if (q.code == 0) q.w = make_uint2(0, 0);
+  } else {
+    ratio = true_quotient(amax, r.six);
+    q.code = ratio != ratio ? 0x7fu : (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
+    q.d = q.code == 0x7fu ? __uint_as_float(0x7fffffffu) : __fmul_rn(e4m3_value(q.code), r.gs);
+    q.w = q.d > 0.f && a <= kInfBits ? encode_by_division(h, q.d) : make_uint2(0, 0);
+  }
+  return q;
 }
 
 }  // namespace fp4q

@@ -16,11 +16,17 @@
 // its codes one 8-byte store; a thread loads all of its chunks (cached_chunks)
 // before it uses any, and keeps them between the row's maximum and its codes
 // (longer rows are read again, from L1).  Every step is IEEE fp32 in the order of
-// the formula, but for h / d, which is h y + h z in one fused multiply-add, y the
-// rounded reciprocal of d and z what it lacks (z = (1 - y d) y, the residual exact):
+// the formula, but for h / d, which is h y + h z in one fused multiply-add, y an
+// approximate reciprocal of d and z what it lacks (z = (1 - y d) y, the residual exact):
 // the quotient to 46 bits before its one rounding, so every tie of the codes is
 // met, in two operations an element, two elements an instruction, where a
 // division costs a dozen.
+//
+// Bound by DRAM where rows are many, but for the gated prologue: 16384 rows of 4096
+// bf16, per matrix (given) 29.1 us, 5.9 TB/s, by row 31.7 us, as MXFP4 26.9 us, 6.3 TB/s;
+// by the ramp of one wave below (4096 rows 10.8 us, 512 rows 2.9 us, one row 2.2 us).
+// SwiGLU reads two elements and spends two transcendental operations for each: 12288
+// rows of 1408 27.1 us.
 
 #include "fp4_quant.cuh"
 
@@ -60,16 +66,17 @@ __device__ __forceinline__ void store_values(T* dst, int level, const uint2& w, 
   store_words(dst, level, o);
 }
 
-// Chunks a thread keeps, and resident blocks asked of the compiler: 4096 rows of
-// 4096 bf16 12.0 us (13.2 with two chunks and ten blocks), 2048 SwiGLU rows of 1408
-// 7.1 us (7.9 with two chunks and six blocks, 8.3 with one and six).
+// Chunks a thread keeps, and resident blocks asked of the compiler: 4096 rows of 4096
+// bf16 10.8 us (11.1 with seven blocks, 13.4 with two chunks and ten); 16384 such rows of
+// fp32 56.6 us (58.4 with eight blocks, 68 with five); 2048 SwiGLU rows of 1408 5.3 us (5.8
+// with two chunks and seven blocks, though 12288 take 24.7 for 27.1).
 template <typename T, bool ACT>
 __host__ __device__ constexpr int cached_chunks() {
   return ACT ? 1 : sizeof(T) == 2 ? 4 : 2;
 }
 template <typename T, bool ACT>
 __host__ __device__ constexpr int resident_blocks() {
-  return ACT ? 8 : sizeof(T) == 2 ? 7 : 6;
+  return sizeof(T) == 2 || ACT ? 8 : 7;
 }
 
 }  // namespace
@@ -82,19 +89,15 @@ __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quan
   constexpr int kCached = cached_chunks<T, ACT>();
   constexpr int kPerTile = FMT == 0 ? 4 : 8;  // chunks of a scale tile
   __shared__ uint32_t s_max[kQThreads / 32];
-  __shared__ float4 s_e4m3[ROW ? 128 : 1];
   const int tpr = 1 << tpr_log2;
   const int t = threadIdx.x & (tpr - 1);
   const int lane = threadIdx.x & 31;
-  if constexpr (ROW) {
-    if (threadIdx.x < 128) s_e4m3[threadIdx.x] = e4m3_and_reciprocal(threadIdx.x);
-  }
   pdl_wait();
   pdl_launch_dependents();
   if (p.status && blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
 
   // this thread's row: packed index (codes, gs, values), scale tile and row in it
-  const int64_t vrow = (int64_t)blockIdx.x * (kQThreads >> tpr_log2) + (threadIdx.x >> tpr_log2);
+  const int64_t vrow = (int64_t)blockIdx.x * (blockDim.x >> tpr_log2) + (threadIdx.x >> tpr_log2);
   const int tiles_per = cdiv(p.m, 128);
   bool live = false, pad = false;
   int64_t row = 0, tile = 0;
@@ -157,9 +160,9 @@ __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quan
       }
     }
     for (int o = min(tpr, 32) / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if (lane == 0) s_max[threadIdx.x >> 5] = a;
-    __syncthreads();  // also the scale table's
     if (tpr > 32) {
+      if (lane == 0) s_max[threadIdx.x >> 5] = a;
+      __syncthreads();
       const int w0 = (threadIdx.x >> tpr_log2) << (tpr_log2 - 5);
       for (int w = 0; w < (tpr >> 5); ++w) a = max(a, s_max[w0 + w]);
     }
@@ -169,7 +172,6 @@ __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quan
     gs = __ldg(p.gs + group);
   }
   const RowScale rs(gs);
-  const float inv_gs = ROW ? __frcp_rn(rs.safe ? gs : 1.f) : 0.f;
 
   // this thread's first chunk in each output, and the way to its next one; the
   // scale of block b is at [row][b] or, tiled, in byte b % 4 of the row's word of
@@ -192,33 +194,16 @@ __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quan
 
   auto emit = [&](int it, const Chunk<T, ACT>& v, uint32_t a) {
     const int c = it * tpr + t;
-    uint32_t code;
-    uint2 w;
-    float d;
-    if (ROW && rs.safe) {
-      // every block's largest magnitude is within 6 448 gs
-      code = (uint32_t)__nv_cvt_float_to_fp8(quotient(__uint_as_float(a), rs.inv), __NV_SATFINITE, __NV_E4M3);
-      const float4 s = s_e4m3[code];
-      d = s.x * gs;
-      w = encode<FMT>(v, Recip{s.y * inv_gs, s.z * inv_gs});
-      if (code == 0) w = make_uint2(0, 0);
-    } else {
-      if (FMT != 0) a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      const BlockScale b = block_scale<FMT>(a, rs);
-      code = b.code;
-      d = b.d;
-      w = encode<FMT>(v, b.inv);
-      if (FMT == 0 && b.kind == 2) w = encode_by_division(v, d);
-      if (b.kind == 0) w = make_uint2(0, 0);
-    }
+    if (FMT != 0) a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    Quantized q = quantize_block<FMT>(v, a, rs);
     if (c < chunks) {
-      *reinterpret_cast<uint2*>(codes + (int64_t)it * (8 * tpr)) = w;
+      *reinterpret_cast<uint2*>(codes + (int64_t)it * (8 * tpr)) = q.w;
       if constexpr (VALUES)
-        store_values(values + (int64_t)it * (16 * tpr), p.values_vec, w, d, code == (FMT == 0 ? 0x7fu : 255u));
+        store_values(values + (int64_t)it * (16 * tpr), p.values_vec, q.w, q.d, q.code == (FMT == 0 ? 0x7fu : 255u));
     } else {
-      code = 0;
+      q.code = 0;
     }
-    if (c < scale_chunks) scales[(int64_t)it * scale_step] = (uint8_t)code;
+    if (c < scale_chunks) scales[(int64_t)it * scale_step] = (uint8_t)q.code;
   };
 #pragma unroll
   for (int it = 0; it < kCached; ++it)
@@ -357,7 +342,10 @@ cudaError_t quantize_t(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStrea
   const int share = live * slots <= (int64_t)num_sms * 2048 ? 1 : cached_chunks<T, ACT>();
   int lg = p.offsets ? 5 : 3;
   while ((1 << lg) < kQThreads && (1 << lg) * share < slots) ++lg;
-  const int64_t grid = (rows + (kQThreads >> lg) - 1) / (kQThreads >> lg);
+  // a block of its own for a row of two warps: 16384 rows of 4096 31.7 us, two in a block 32.8
+  // (rows of one warp the other way round: 12288 of 2048 11.7 us, in blocks of two 12.0)
+  const int threads = share > 1 && lg == 6 ? 64 : kQThreads;
+  const int64_t grid = (rows + (threads >> lg) - 1) / (threads >> lg);
   if (p.gs_mode == kGsTensor) {
     cudaError_t e = cudaMemsetAsync(p.gs, 0, sizeof(float) * p.groups, stream);
     if (e != cudaSuccess) return e;
@@ -370,7 +358,7 @@ cudaError_t quantize_t(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStrea
     e = launch_pdl(fp4_gs_kernel, dim3(cdiv(p.groups, 256)), dim3(256), 0, false, stream, p.gs, p.groups);
     if (e != cudaSuccess) return e;
   }
-  auto go = [&](auto kern) { return launch_pdl(kern, dim3((unsigned)grid), dim3(kQThreads), 0, pdl, stream, p, lg); };
+  auto go = [&](auto kern) { return launch_pdl(kern, dim3((unsigned)grid), dim3(threads), 0, pdl, stream, p, lg); };
   if constexpr (FMT == 0)
     if (p.gs_mode == kGsRow)
       return p.values ? go(fp4_quantize_kernel<T, FMT, ACT, true, true>) : go(fp4_quantize_kernel<T, FMT, ACT, true, false>);
