@@ -28,6 +28,8 @@
 // SwiGLU reads two elements and spends two transcendental operations for each: 12288
 // rows of 1408 27.1 us.
 
+#include <algorithm>
+
 #include "fp4_quant.cuh"
 
 namespace b4 {
@@ -97,7 +99,8 @@ __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quan
   if (p.status && blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
 
   // this thread's row: packed index (codes, gs, values), scale tile and row in it
-  const int64_t vrow = (int64_t)blockIdx.x * (blockDim.x >> tpr_log2) + (threadIdx.x >> tpr_log2);
+  const uint32_t block = p.gs_mode == kGsTensor ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  const int64_t vrow = (int64_t)block * (blockDim.x >> tpr_log2) + (threadIdx.x >> tpr_log2);
   const int tiles_per = cdiv(p.m, 128);
   bool live = false, pad = false;
   int64_t row = 0, tile = 0;
@@ -219,19 +222,33 @@ __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quan
 
 // ------------------------------------------- one global scale per matrix
 // Largest magnitude of each matrix of a stack, as fp32 bits (order of the
-// atomics does not matter to a maximum), then amax / (6 448) in place.
+// atomics does not matter to a maximum), then amax / (6 448) in place.  Blocks
+// take the matrices in order and the quantiser takes them from the end, so that what
+// the cache still holds is read from there: 16 fp32 matrices of 2816 x 2048 with their
+// values 180 us for 182 (both passes move 6.4 TB/s).
+constexpr int kAmaxChunks = 8;  // of a thread
 template <typename T, bool ACT>
 __global__ void __launch_bounds__(kQThreads) fp4_amax_kernel(const __grid_constant__ Fp4QuantParams p) {
   __shared__ uint32_t s_max[kQThreads / 32];
   const int group = blockIdx.y;
-  const int per_row = p.k / 16;
+  const uint32_t per_row = p.k / 16;
   const int64_t n = (int64_t)p.m * per_row;
+  const T* x = reinterpret_cast<const T*>(p.x) + (int64_t)group * p.m * p.x_stride;
   uint32_t a = 0;
-  for (int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kQThreads) {
-    const int64_t r = i / per_row;
-    Chunk<T, ACT> h;
-    h.get(p, reinterpret_cast<const T*>(p.x) + ((int64_t)group * p.m + r) * p.x_stride, (int)(i - r * per_row));
-    a = max(a, h.amax());
+  for (int64_t b = (int64_t)blockIdx.x * (kQThreads * kAmaxChunks); b < n; b += (int64_t)gridDim.x * (kQThreads * kAmaxChunks)) {
+    // the block's first chunk by a division, the others from there
+    const int64_t r0 = b / per_row;
+    const uint32_t c0 = (uint32_t)(b - r0 * per_row);
+#pragma unroll
+    for (int it = 0; it < kAmaxChunks; ++it) {
+      const uint32_t j = c0 + it * kQThreads + threadIdx.x;
+      const uint32_t r = j / per_row;
+      if (b + it * kQThreads + threadIdx.x < n) {
+        Chunk<T, ACT> h;
+        h.get(p, x + (r0 + r) * p.x_stride, (int)(j - r * per_row));
+        a = max(a, h.amax());
+      }
+    }
   }
   for (int o = 16; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = a;
@@ -243,6 +260,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_amax_kernel(const __grid_consta
 }
 
 __global__ void fp4_gs_kernel(float* gs, int groups) {
+  pdl_wait();
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= groups) return;
   const float a = gs[i];
@@ -349,14 +367,12 @@ cudaError_t quantize_t(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStrea
   if (p.gs_mode == kGsTensor) {
     cudaError_t e = cudaMemsetAsync(p.gs, 0, sizeof(float) * p.groups, stream);
     if (e != cudaSuccess) return e;
-    const int64_t work = ((int64_t)p.m * (p.k / 16) + 4 * kQThreads - 1) / (4 * kQThreads);
-    int gx = (8 * num_sms + p.groups - 1) / p.groups;
-    if (gx > work) gx = (int)work;
-    if (gx < 1) gx = 1;
-    e = launch_pdl(fp4_amax_kernel<T, ACT>, dim3(gx, p.groups), dim3(kQThreads), 0, false, stream, p);
+    const int64_t work = ((int64_t)p.m * (p.k / 16) + kAmaxChunks * kQThreads - 1) / (kAmaxChunks * kQThreads);
+    e = launch_pdl(fp4_amax_kernel<T, ACT>, dim3((unsigned)std::min<int64_t>(work, 1 << 30), p.groups), dim3(kQThreads), 0, false, stream, p);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(fp4_gs_kernel, dim3(cdiv(p.groups, 256)), dim3(256), 0, false, stream, p.gs, p.groups);
+    e = launch_pdl(fp4_gs_kernel, dim3(cdiv(p.groups, 256)), dim3(256), 0, true, stream, p.gs, p.groups);
     if (e != cudaSuccess) return e;
+    pdl = true;
   }
   auto go = [&](auto kern) { return launch_pdl(kern, dim3((unsigned)grid), dim3(threads), 0, pdl, stream, p, lg); };
   if constexpr (FMT == 0)
