@@ -84,6 +84,7 @@ struct Fp4GemmParams {
   int vec;                   // rows of out are 16-byte aligned and n fills them
   Fp4QuantParams q;          // direct: the rows the kernel quantises for itself
   int x_dtype, clear_status;
+  int halves_from;           // dense units of 256 rows from here on are taken as two halves
   int a_is_new;              // the activation operand comes from the kernel before (programmatic launch)
   uint32_t* status;          // or null
 };

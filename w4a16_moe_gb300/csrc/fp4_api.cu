@@ -250,6 +250,11 @@ b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const u
       !make_tmap_tiles(&p.tmap_as, a_scales, (uint64_t)operand_tiles(c, ragged) * k_tiles, box))
     FP4_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected a scale map");
   const int pairs = (int)(units < sms / 2 ? units : sms / 2);
+  // the last round's units in halves, where a round holds them: N = K = 4096, 4096 rows 28.6 us
+  // for 30.5, 5120 rows 34.2 for 36.1; N = 2048, K = 1408, 2560 rows 9.8 for 10.9
+  const int64_t left = units % pairs;
+  const bool even = (c->m + 127) / 128 % 2 == 0;  // every unit has a second half
+  p.halves_from = (int)(2 * left <= pairs && even ? units - left : units);
   return cuda_status(launch_fp4_gemm_pair(p, c->format, nt, pairs, a_is_new, stream), "fp4 product");
 }
 

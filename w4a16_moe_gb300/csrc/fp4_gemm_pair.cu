@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   tc_fence_after();
   if (threadIdx.x == 0) pdl_launch_dependents();
   const uint32_t tmem = *s_tmem;
-  const int n_units = (RAGGED ? groups.tiles[p.groups] : p.groups * cdiv(p.m, NR)) * wpairs;
+  int n_units = (RAGGED ? groups.tiles[p.groups] : p.groups * cdiv(p.m, NR)) * wpairs;
+  if (!RAGGED && NR == 256) n_units += max(n_units - p.halves_from, 0);
   const int k64 = cdiv(p.k, 64);                       // matrix instructions along K
   const int stages = cdiv(k64, 4);
   const int k_tiles = cdiv(p.k, 4 * fp4_group(FMT));   // scale tiles along K

@@ -149,10 +149,15 @@ __device__ __forceinline__ void build_groups(const Fp4GemmParams& p, Groups& g) 
 // Unit u: weight rows outermost within a group, so that neighbouring units
 // read the same weights.  wtiles: weight units of a group.  The search is out of
 // line, one copy for all of a kernel's loops (unrolled over their rings): returns
-// group, weight unit, first packed row, and rows | token tile << 9.
+// group, weight unit << 1 | half, first packed row, and rows | token tile << 9.
+// Dense units of 256 rows from halves_from on are two units of 128 each.
 template <int NT, bool RAGGED>
-__device__ __noinline__ static int4 find_unit(int groups, int m, const Groups* g, int wtiles, int u) {
-  int lo, t, nt, first, rows;
+__device__ __noinline__ static int4 find_unit(int groups, int m, const Groups* g, int wtiles, int u, int halves_from) {
+  int lo, t, nt, first, rows, half = -1;
+  if (!RAGGED && NT == 256 && u >= halves_from) {
+    half = (u - halves_from) & 1;
+    u = halves_from + ((u - halves_from) >> 1);
+  }
   if constexpr (RAGGED) {
     lo = 0;
     int hi = groups - 1;  // last group whose tiles start at or before the unit's
@@ -176,19 +181,23 @@ __device__ __noinline__ static int4 find_unit(int groups, int m, const Groups* g
   } else {
     first = lo * m + t * NT;
     rows = min(NT, m - t * NT);
+    if (half >= 0) {
+      first += 128 * half;
+      rows = min(128, rows - 128 * half);
+    }
   }
-  return make_int4(lo, wtile, first, rows | t << 9);
+  return make_int4(lo, 2 * wtile + max(half, 0), first, rows | t << 9);
 }
 template <int NT, bool RAGGED>
 __device__ __forceinline__ Unit get_unit(const Fp4GemmParams& p, const Groups& g, int wtiles, int u) {
-  const int4 v = find_unit<NT, RAGGED>(p.groups, p.m, &g, wtiles, u);
+  const int4 v = find_unit<NT, RAGGED>(p.groups, p.m, &g, wtiles, u, p.halves_from);
   const int t = v.w >> 9;
   Unit U;
   U.group = v.x;
-  U.wtile = v.y;
+  U.wtile = v.y >> 1;
   U.first = v.z;
   U.rows = v.w & 511;
-  U.atile = (RAGGED ? (v.z - t * NT) / 128 + v.x : v.x * cdiv(p.m, 128)) + t * NT / 128;
+  U.atile = (RAGGED ? (v.z - t * NT) / 128 + v.x : v.x * cdiv(p.m, 128)) + t * NT / 128 + (v.y & 1);
   U.shift = (t * NT & 127) >> 5;
   return U;
 }
