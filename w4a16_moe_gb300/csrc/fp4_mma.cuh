@@ -151,6 +151,12 @@ __device__ __forceinline__ void build_groups(const Fp4GemmParams& p, Groups& g) 
 // line, one copy for all of a kernel's loops (unrolled over their rings): returns
 // group, weight unit << 1 | half, first packed row, and rows | token tile << 9.
 // Dense units of 256 rows from halves_from on are two units of 128 each.
+// Ragged units of 256 rows are taken from each third of them in turn: units of large groups
+// are bound by the way into shared memory, those of small groups by the stream of weights from
+// DRAM, and the two mix better than they follow one another (8 groups of 1100 rows and 56 of
+// 60, N = 2816, K = 2048: 57.4 us where the large ones are neighbours, in order 60.8; in a random
+// order 58.0 and 57.7).
+constexpr int kMix = 3;
 template <int NT, bool RAGGED>
 __device__ __noinline__ static int4 find_unit(int groups, int m, const Groups* g, int wtiles, int u, int halves_from) {
   int lo, t, nt, first, rows, half = -1;
@@ -159,6 +165,10 @@ __device__ __noinline__ static int4 find_unit(int groups, int m, const Groups* g
     u = halves_from + ((u - halves_from) >> 1);
   }
   if constexpr (RAGGED) {
+    if (NT == 256) {
+      const int run = (g->tiles[groups] * wtiles) / kMix;
+      if (u < run * kMix) u = u % kMix * run + u / kMix;
+    }
     lo = 0;
     int hi = groups - 1;  // last group whose tiles start at or before the unit's
     while (lo < hi) {
