@@ -215,6 +215,37 @@ def test_special_values(b4):
             assert np.all(np.abs(v[4] - 2.0**-130) <= 2.0**-130)
 
 
+@pytest.mark.parametrize("act", [None, "silu", "relu2"])
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+def test_nan_and_infinity_of_every_type(b4, dtype, act):
+    """By row: rows with a NaN or an infinity, of either sign and in any place of a chunk, give NaN, and only they;
+    the other rows' bits do not depend on them."""
+    m, k = 36, 80
+    x = _randn((m, 2 * k if act == "silu" else k), 5, dtype)
+    clean = x.clone()
+    bad = []
+    for i, v in enumerate((float("nan"), float("inf"), -float("inf"))):
+        for j, col in enumerate((0, 1, 15, 16, 47, 78, 79)):
+            r = 1 + 8 * i + j
+            x[r, col] = v
+            if not (act == "relu2" and v < 0):  # ReLU of -inf is 0
+                bad.append(r)
+    good = [r for r in range(m) if r not in bad]
+    cfg = b4.Fp4Config(m=m, k=k, x_dtype=dtype, activation=b4.ACTIVATIONS.get(act))
+    outs = []
+    for rows in (x, clean):
+        codes, scales, gs = b4.fp4_empty(cfg, "cuda")
+        values = torch.empty(m, k, dtype=dtype, device="cuda")
+        b4.fp4_quantize(cfg, rows.cuda(), codes, scales, gs, values=values)
+        outs.append((codes[..., : k // 2], gs.reshape(-1), values))  # (bytes past K / 2 are padding)
+    assert torch.isnan(outs[0][1][bad]).all() and torch.isnan(outs[0][2][bad]).all()
+    same = [r for r in good if torch.equal(x[r], clean[r])]
+    assert len(same) >= m - 21
+    for a, b in zip(*outs):
+        assert torch.equal(a[..., same, :] if a.dim() > 1 else a[same], b[..., same, :] if b.dim() > 1 else b[same])
+    assert torch.isfinite(outs[0][2][good]).all()
+
+
 def test_given_scale_that_is_far_off(b4):
     """Saturation at 6 * 448 gs, all-zero blocks below it, and scales outside the reciprocal's safe range."""
     x = _randn((4, 64), 4, F32)
