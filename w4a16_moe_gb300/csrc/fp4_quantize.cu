@@ -26,7 +26,7 @@
 // bf16, per matrix (given) 29.1 us, 5.9 TB/s, by row 31.7 us, as MXFP4 26.9 us, 6.3 TB/s;
 // by the ramp of one wave below (4096 rows 10.8 us, 512 rows 2.9 us, one row 2.2 us).
 // SwiGLU reads two elements and spends two transcendental operations for each: 12288
-// rows of 1408 27.1 us.
+// rows of 1408 23.7 us, 3.3 TB/s.
 
 #include <algorithm>
 
@@ -70,8 +70,8 @@ __device__ __forceinline__ void store_values(T* dst, int level, const uint2& w, 
 
 // Chunks a thread keeps, and resident blocks asked of the compiler: 4096 rows of 4096
 // bf16 10.8 us (11.1 with seven blocks, 13.4 with two chunks and ten); 16384 such rows of
-// fp32 56.6 us (58.4 with eight blocks, 68 with five); 2048 SwiGLU rows of 1408 5.3 us (5.8
-// with two chunks and seven blocks, though 12288 take 24.7 for 27.1).
+// fp32 56.6 us (58.4 with eight blocks, 68 with five); 2048 SwiGLU rows of 1408 5.0 us (5.3
+// with two chunks and seven blocks, 5.5 with ten blocks).
 template <typename T, bool ACT>
 __host__ __device__ constexpr int cached_chunks() {
   return ACT ? 1 : sizeof(T) == 2 ? 4 : 2;
@@ -83,16 +83,17 @@ __host__ __device__ constexpr int resident_blocks() {
 
 }  // namespace
 
-// tpr_log2: threads per row.  Rows beyond the operand (pad_rows) only clear
+// shape: threads per row, as their logarithm, or behind an activation their number: a power
+// of two up to 32, or the whole block.  Rows beyond the operand (pad_rows) only clear
 // their scales.
 template <typename T, int FMT, bool ACT, bool ROW, bool VALUES>
 __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quantize_kernel(const __grid_constant__ Fp4QuantParams p,
-                                                                 int tpr_log2) {
+                                                                 int shape) {
   constexpr int kCached = cached_chunks<T, ACT>();
   constexpr int kPerTile = FMT == 0 ? 4 : 8;  // chunks of a scale tile
   __shared__ uint32_t s_max[kQThreads / 32];
-  const int tpr = 1 << tpr_log2;
-  const int t = threadIdx.x & (tpr - 1);
+  const int tpr = ACT ? shape : 1 << shape;
+  const int t = ACT && tpr > 32 ? threadIdx.x : threadIdx.x & (tpr - 1);
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
@@ -100,7 +101,8 @@ __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quan
 
   // this thread's row: packed index (codes, gs, values), scale tile and row in it
   const uint32_t block = p.gs_mode == kGsTensor ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-  const int64_t vrow = (int64_t)block * (blockDim.x >> tpr_log2) + (threadIdx.x >> tpr_log2);
+  const int64_t vrow = ACT ? tpr > 32 ? block : ((int64_t)block * blockDim.x + threadIdx.x) >> (31 - __clz(tpr))
+                           : (int64_t)block * (blockDim.x >> shape) + (threadIdx.x >> shape);
   const int tiles_per = cdiv(p.m, 128);
   bool live = false, pad = false;
   int64_t row = 0, tile = 0;
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kQThreads, resident_blocks<T, ACT>()) fp4_quan
     if (tpr > 32) {
       if (lane == 0) s_max[threadIdx.x >> 5] = a;
       __syncthreads();
-      const int w0 = (threadIdx.x >> tpr_log2) << (tpr_log2 - 5);
+      const int w0 = ACT ? 0 : (threadIdx.x >> shape) << (shape - 5);
       for (int w = 0; w < (tpr >> 5); ++w) a = max(a, s_max[w0 + w]);
     }
     gs = row_gs(a);
@@ -362,8 +364,17 @@ cudaError_t quantize_t(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStrea
   while ((1 << lg) < kQThreads && (1 << lg) * share < slots) ++lg;
   // a block of its own for a row of two warps: 16384 rows of 4096 31.7 us, two in a block 32.8
   // (rows of one warp the other way round: 12288 of 2048 11.7 us, in blocks of two 12.0)
-  const int threads = share > 1 && lg == 6 ? 64 : kQThreads;
-  const int64_t grid = (rows + (threads >> lg) - 1) / (threads >> lg);
+  int shape = lg, rows_per = 1, threads = share > 1 && lg == 6 ? 64 : kQThreads;
+  if (ACT) {
+    // and for every row of several warps behind an activation, of no more warps than it
+    // fills: 12288 SwiGLU rows of 1408 23.7 us, on 128 threads each 27.1
+    shape = lg > 5 && slots < kQThreads ? round_up(slots, 32) : 1 << lg;
+    threads = lg > 5 ? shape : kQThreads;
+    rows_per = threads / shape;
+  } else {
+    rows_per = threads >> lg;
+  }
+  const int64_t grid = (rows + rows_per - 1) / rows_per;
   if (p.gs_mode == kGsTensor) {
     cudaError_t e = cudaMemsetAsync(p.gs, 0, sizeof(float) * p.groups, stream);
     if (e != cudaSuccess) return e;
@@ -374,7 +385,7 @@ cudaError_t quantize_t(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStrea
     if (e != cudaSuccess) return e;
     pdl = true;
   }
-  auto go = [&](auto kern) { return launch_pdl(kern, dim3((unsigned)grid), dim3(threads), 0, pdl, stream, p, lg); };
+  auto go = [&](auto kern) { return launch_pdl(kern, dim3((unsigned)grid), dim3(threads), 0, pdl, stream, p, shape); };
   if constexpr (FMT == 0)
     if (p.gs_mode == kGsRow)
       return p.values ? go(fp4_quantize_kernel<T, FMT, ACT, true, true>) : go(fp4_quantize_kernel<T, FMT, ACT, true, false>);
