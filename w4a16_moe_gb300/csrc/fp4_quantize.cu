@@ -353,13 +353,14 @@ cudaError_t launch_pdl(K kern, dim3 grid, dim3 block, size_t smem, bool pdl, cud
 template <typename T, int FMT, bool ACT>
 cudaError_t quantize_t(const Fp4QuantParams& p, int num_sms, bool pdl, cudaStream_t stream) {
   // Threads per row: as many as it takes for a thread to hold its share, and
-  // while all rows together do not fill the GPU once, down to one chunk each;
-  // at least a warp for ragged rows (the whole warp finds their group) and
-  // eight for a scale word.
+  // while all rows together are a few chunks for every SM's threads, down to one
+  // chunk each; at least a warp for ragged rows (the whole warp finds their group)
+  // and eight for a scale word.  Shares of four from 512 chunks an SM on (2048 bf16 rows of
+  // 2048 3.5 us, single chunks 5.4; 768 of 4096 3.3, 4.0; 384 of 4096 3.0, 2.8).
   const int slots = p.k_tiles * (FMT == 0 ? 4 : 8);
   const int64_t rows = p.offsets ? p.m : (int64_t)p.groups * (p.pad_rows ? cdiv(p.m, 128) * 128 : p.m);
   const int64_t live = p.offsets ? p.m : (int64_t)p.groups * p.m;
-  const int share = live * slots <= (int64_t)num_sms * 2048 ? 1 : cached_chunks<T, ACT>();
+  const int share = live * slots <= (int64_t)num_sms * 512 ? 1 : cached_chunks<T, ACT>();
   int lg = p.offsets ? 5 : 3;
   while ((1 << lg) < kQThreads && (1 << lg) * share < slots) ++lg;
   // a block of its own for a row of two warps: 16384 rows of 4096 31.7 us, two in a block 32.8
