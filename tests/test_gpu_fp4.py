@@ -448,7 +448,7 @@ def test_nan_scale_reaches_its_row_only(b4):
 
 RAGGED = [
     (NV, [3], 96, 80, 5),
-    (NV, [0, 1, 64, 65, 0, 130, 7, 0], 200, 272, 9),      # small units: 64-row tiles at 0 and 64 of a scale tile
+    (NV, [0, 1, 64, 65, 0, 130, 7, 0], 200, 272, 9),      # pairs, one unit of two rows past 128
     (NV, [0, 400, 193, 1, 192, 0], 130, 64, 3),           # wide units
     (NV, [0, 0, 0], 40, 64, 6),                           # nothing live
     (NV, [2] * 64 + [0] * 960, 40, 64, 0),                # as many groups as there can be
@@ -457,6 +457,9 @@ RAGGED = [
     (NV, [1, 0, 2, 5], 130, 2048, 2),                     # split along K
     (NV, [100, 0, 128, 129, 65], 300, 528, 3),            # pairs, units of 128 rows
     (MX, [400, 300, 0, 193], 270, 288, 7),                # pairs, units of 256 rows
+    (NV, [0, 1, 65, 0, 130, 7] + [0] * 10, 200, 272, 9),  # a small mean: units of 64 rows at 0 and 64 of a scale tile
+    (MX, [70, 5] + [0] * 8, 150, 96, 3),
+    (NV, [300, 0, 129, 256, 70, 1, 385], 700, 80, 4),     # units of 256 rows from three places at once
 ]
 
 

@@ -136,13 +136,17 @@ Fp4QuantParams quant_params(const b4_fp4_config* c, const void* x, const int32_t
 // (fp4_gemm_pair.cu, a pair of SMs).  The smallest that makes one round of the
 // SMs, else the largest that groups fill.  Measured in us at 64 / 128 / 256: dense
 // N = K = 4096 m = 256 8.2 / 8.8 / 10.7, m = 512 13.3 / 9.2 / 11.1, m = 1024 23 / 13.6 / 11.9;
-// N = 2048 K = 1408 m = 512 5.2 / 6.7 / 8.0, m = 1024 7.4 / 7.0 / 8.2; 28 MXFP4 groups N = K =
-// 2880 of 64 rows each 28.4 / 27.7 / 29.2, 80 rows 41 / 28.3 / 30.3, 160 rows 56 / 40 / 34.
+// N = 2048 K = 1408 m = 512 5.2 / 6.7 / 8.0, m = 1024 7.4 / 7.0 / 8.2.  Ragged groups take the
+// unit by their mean, which popular experts exceed (64 groups N = 2816 K = 2048, popularities
+// spread by e^N(0, 1/2), or e^N(0, 1) up to a mean of 24): mean 8 36.4 / 36.1, 24 39.8 / 38.5, 40 41.4 /
+// 40.1 / 42.0, 64 50.1 / 41.1 / 44.1, 96 65 / 45.7 / 44.8, 112 71 / 47.5 / 45.5, 144 87 / 52.2 / 48.3; without
+// the spread 64 49.8 / 42.0 / 43.1, 96 65 / 43.6 / 45.0, 112 68 / 44.4 / 45.8; 28 MXFP4 groups N = K =
+// 2880 mean 16 23.4 / 26.0, 32 26.3 / 27.4, 64 33.7 / 28.1 / 30.5, 112 44 / 31.3 / 31.6, 128 48 / 34.8 / 33.1.
 int unit_rows(const b4_fp4_config* c, bool ragged, int sms) {
   const int64_t groups = c->num_groups;
   if (ragged) {  // the rows of a group are known on the device: their mean
     const int64_t per = c->m / groups;
-    return per <= 64 ? 64 : per <= 128 ? 128 : 256;
+    return per <= 16 ? 64 : per <= 104 ? 128 : 256;
   }
   if (c->m <= 64 || groups * cdiv(c->m, 64) * cdiv(c->n, 128) <= sms) return 64;
   if (c->m <= 128 || groups * cdiv(c->m, 128) * cdiv(c->n, 256) <= sms / 2) return 128;
