@@ -463,8 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
                   }
               }
               const int n0 = tab.wtile[0] * 128 + 32 * q4;
-              const int at = 32 * turn + lane;
-              const RowInfo info{tab.g[0][at], tab.to[0][at]};
+              const RowInfo info{tab.g[0] + 32 * turn, tab.to[0] + 32 * turn};
               if (n0 < p.n) store_chunk<OUT>(p, lo, hi, info, n0, stage, lane);
             }
           }
@@ -485,8 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
           uint32_t lo[16], hi[16];
           tmem_ld16x256b_x4(taddr, lo);
           tmem_ld16x256b_x4(taddr + (16u << 16), hi);
-          const int r = 32 * turn + lane;
-          const RowInfo info{tab.g[b][r], tab.to[b][r]};
+          const RowInfo info{tab.g[b] + 32 * turn, tab.to[b] + 32 * turn};
           tmem_ld_wait();
           if (n0 < p.n) store_chunk<OUT>(p, lo, hi, info, n0, stage, lane);
         }

@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
         if (64 * c + 32 * turn < rows && n0 < p.n) {
-          const int r = 64 * c + 32 * turn + lane;
-          store_chunk<OUT>(p, lo[c], hi[c], RowInfo{tab.g[b][r], tab.to[b][r]}, n0, stage, lane);
+          const int r = 64 * c + 32 * turn;
+          store_chunk<OUT>(p, lo[c], hi[c], RowInfo{tab.g[b] + r, tab.to[b] + r}, n0, stage, lane);
         }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty_rows[b]);

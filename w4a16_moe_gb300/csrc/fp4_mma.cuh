@@ -235,8 +235,18 @@ __device__ __forceinline__ void store_out(const Fp4GemmParams& p, int64_t at, fl
   else reinterpret_cast<float*>(p.out)[at] = v;
 }
 
+// Two accumulators times their rows' scales, in one instruction.
+__device__ __forceinline__ float2 times2(uint32_t a, uint32_t b, float2 g) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(a), "r"(b), "f"(g.x), "f"(g.y));
+  return r;
+}
+
 template <int DT>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack16(float2 v2) {
+  const float lo = v2.x, hi = v2.y;
   if constexpr (DT == 0) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -255,9 +265,9 @@ struct RowTable {
   int to[2][NT];    // its output row, or -1
   int rows[2], wtile[2];
 };
-struct RowInfo {
-  float g;
-  int to;
+struct RowInfo {  // of 32 rows of the table
+  const float* g;
+  const int* to;
 };
 
 template <int NT, bool RAGGED>
@@ -306,11 +316,11 @@ __device__ __forceinline__ void store_staged(const Fp4GemmParams& p, const uint3
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = 8 * i + 2 * (lane & 3);
-    const float g0 = __shfl_sync(0xffffffffu, info.g, t), g1 = __shfl_sync(0xffffffffu, info.g, t + 1);
+    const float2 g = *reinterpret_cast<const float2*>(info.g + t);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      h[i][j] = pack16<DT>(__uint_as_float(lo[4 * i + 2 * j]) * g0, __uint_as_float(lo[4 * i + 2 * j + 1]) * g1);
-      h[i][2 + j] = pack16<DT>(__uint_as_float(hi[4 * i + 2 * j]) * g0, __uint_as_float(hi[4 * i + 2 * j + 1]) * g1);
+      h[i][j] = pack16<DT>(times2(lo[4 * i + 2 * j], lo[4 * i + 2 * j + 1], g));
+      h[i][2 + j] = pack16<DT>(times2(hi[4 * i + 2 * j], hi[4 * i + 2 * j + 1], g));
     }
   }
   const uint32_t st_addr = smem_u32(stage) + (lane & 7) * kEpiRow + (lane >> 3) * 16;
@@ -325,7 +335,7 @@ __device__ __forceinline__ void store_staged(const Fp4GemmParams& p, const uint3
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     w[i] = *reinterpret_cast<const uint4*>(src + 8 * i * kEpiRow);
-    o[i] = __shfl_sync(0xffffffffu, info.to, 8 * i + (lane >> 2));
+    o[i] = info.to[8 * i + (lane >> 2)];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -342,8 +352,8 @@ __device__ __forceinline__ void store_direct(const Fp4GemmParams& p, const uint3
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = 8 * i + 2 * (lane & 3) + j;
-      const float g = __shfl_sync(0xffffffffu, info.g, t);
-      const int o = __shfl_sync(0xffffffffu, info.to, t);
+      const float g = info.g[t];
+      const int o = info.to[t];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const int n = n0 + 8 * h + (lane >> 2);
