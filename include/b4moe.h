@@ -470,7 +470,8 @@ b4_status b4_fp4_linear(const b4_fp4_config* cfg, const void* x, const float* x_
  * first, w2 [E_l][H][ld(I)], tiled scales, gs13 / gs2 [E_l] (NVFP4).  NVFP4
  * activations take per-row global scales.  The intermediate roundings to bf16 (FC1's
  * output, each route's FC2 output) are far below the 4-bit activations' own.
- * 6 launches; 4 for at most 8 routes. */
+ * 6 launches; one less for each product that quantises its few rows itself
+ * (b4_fp4_linear). */
 size_t b4_fused_moe_a4_workspace_bytes(const b4_moe_config* cfg, int32_t activation);
 b4_status b4_fused_moe_a4(const b4_moe_config* cfg, const uint16_t* x, const uint8_t* w13, const uint8_t* s13,
                           const float* gs13, const uint8_t* w2, const uint8_t* s2, const float* gs2,
