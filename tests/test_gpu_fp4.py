@@ -394,6 +394,9 @@ DENSE = [
     (NV, 1, 1030, 2568, 1296, BF),
     (MX, 1, 1030, 2568, 160, HF),
     (MX, 2, 700, 2603, 96, BF),
+    # pairs, more than two rounds of units of 128 rows and of 256
+    (NV, 1, 100, 40000, 80, BF),
+    (MX, 1, 1030, 8000, 96, HF),
     # the last units of 256 rows in halves, one of them ragged
     (NV, 1, 1970, 2500, 80, BF),
     (MX, 2, 1000, 2500, 96, F32),

@@ -22,7 +22,8 @@ cudaError_t launch_fp4_tile_scales(const uint8_t* src, uint8_t* dst, int groups,
 cudaError_t launch_fp4_combine(const Fp4CombineParams& p, cudaStream_t stream);
 cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, int fmt, int grid, int splits, bool pdl, cudaStream_t stream);
 cudaError_t launch_fp4_gemm_direct(const Fp4GemmParams& p, int fmt, int grid, int splits, bool pdl, cudaStream_t stream);
-cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& p, int fmt, int nr, int pairs, bool pdl, cudaStream_t stream);
+cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& p, int fmt, int nr, int pairs, int rounds, bool pdl,
+                                 cudaStream_t stream);
 }  // namespace b4
 
 using namespace b4;
@@ -259,7 +260,8 @@ b4_status launch_product(const b4_fp4_config* c, const uint8_t* a_codes, const u
   const int64_t left = units % pairs;
   const bool even = (c->m + 127) / 128 % 2 == 0;  // every unit has a second half
   p.halves_from = (int)(2 * left <= pairs && even ? units - left : units);
-  return cuda_status(launch_fp4_gemm_pair(p, c->format, nt, pairs, a_is_new, stream), "fp4 product");
+  return cuda_status(
+      launch_fp4_gemm_pair(p, c->format, nt, pairs, cdiv((int)units, pairs), a_is_new, stream), "fp4 product");
 }
 
 // Workspace of b4_fp4_linear: the quantised activation operand (m rows, dense or

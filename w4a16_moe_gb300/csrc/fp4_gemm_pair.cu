@@ -56,10 +56,12 @@ struct PairCfg {
   static_assert(kAccs * NR + kStages * kSfCols <= 512, "a stage's scale columns are free once its shared memory is");
 };
 
-template <int FMT, int OUT, bool RAGGED, int NR>
+// LONG: the issuing loop is unrolled over the ring.
+template <int FMT, int OUT, bool RAGGED, int NR, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_constant__ Fp4GemmParams p) {
   using C = PairCfg<FMT, NR>;
   constexpr int NS = C::kStages;
+  constexpr int kUnroll = LONG ? NS : 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;  // aligned as declared: the swizzled stages need 1024 bytes
   Groups& groups = *reinterpret_cast<Groups*>(smem + C::misc + 16);  // ragged only
@@ -166,9 +168,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   } else if (warp == 1) {
     // ---------------------------------------------- matrix instructions
     if (rank == 0) {
-      // The loop over a stage's slot is unrolled over the ring, so that slots
-      // and scale columns are constants: with them in registers a stage took
-      // 100 - 150 cycles more to issue than its products take to run.
+      // Where a pair takes many units the loop over a stage's slot is unrolled over the
+      // ring, so that slots and scale columns are constants: with them in registers a
+      // stage takes longer to issue than its products take to run (8192 x 8192 x 4096 82.0
+      // us, rolled 84.0).  In one round or two the smaller code, fetched cold, gains more
+      // (N = K = 4096, 1024 rows 11.3 us, unrolled 11.7; N = 2048, K = 1408, 1024 rows 6.5, 6.8).
       const uint32_t w_desc = desc_lo(smem_u32(smem)), a_desc = desc_lo(smem_u32(s_a)), s_desc = desc_lo(smem_u32(s_sf));
       uint32_t phase = 0, acc_i = 0, d = 0, abuf = 0;
       int u = u0, s = 0;
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
       bool ok = u < n_units;
       bool seen = false;  // the stage's copies were seen complete during the stage before
       while (ok) {
-#pragma unroll
+#pragma unroll kUnroll
         for (int slot = 0; slot < NS; ++slot) {
           if (s == 0) {
             const int rows = (int)warp_uniform(get_unit<NR, RAGGED>(p, groups, wpairs, u).rows);
@@ -295,9 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-template <int FMT, int OUT, bool RAGGED, int NR>
+template <int FMT, int OUT, bool RAGGED, int NR, bool LONG>
 cudaError_t launch_pair(const Fp4GemmParams& p, int pairs, bool pdl, cudaStream_t stream) {
-  auto kern = fp4_pair_kernel<FMT, OUT, RAGGED, NR>;
+  auto kern = fp4_pair_kernel<FMT, OUT, RAGGED, NR, LONG>;
   const size_t smem = PairCfg<FMT, NR>::total(RAGGED);
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -320,11 +324,19 @@ cudaError_t launch_pair(const Fp4GemmParams& p, int pairs, bool pdl, cudaStream_
 
 }  // namespace fp4
 
-// nr: activation rows of a unit, 128 or 256; the activation map's box holds a quarter of them.
-cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& p, int fmt, int nr, int pairs, bool pdl, cudaStream_t stream) {
+// nr: activation rows of a unit, 128 or 256; the activation map's box holds a quarter of
+// them.  rounds: units a pair takes at most.
+cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& p, int fmt, int nr, int pairs, int rounds, bool pdl,
+                                 cudaStream_t stream) {
   return fp4::with_forms(p, fmt, [&](auto f, auto out, auto ragged) {
-    return nr == 128 ? fp4::launch_pair<f.value, out.value, ragged.value, 128>(p, pairs, pdl, stream)
-                     : fp4::launch_pair<f.value, out.value, ragged.value, 256>(p, pairs, pdl, stream);
+    constexpr int F = f.value, O = out.value;
+    constexpr bool G = ragged.value;
+    const bool many = G || rounds > 2;
+    if (nr == 128)
+      return many ? fp4::launch_pair<F, O, G, 128, true>(p, pairs, pdl, stream)
+                  : fp4::launch_pair<F, O, G, 128, G>(p, pairs, pdl, stream);
+    return many ? fp4::launch_pair<F, O, G, 256, true>(p, pairs, pdl, stream)
+                : fp4::launch_pair<F, O, G, 256, G>(p, pairs, pdl, stream);
   });
 }
 
