@@ -134,10 +134,11 @@ Fp4QuantParams quant_params(const b4_fp4_config* c, const void* x, const int32_t
 }
 
 // Activation rows of a unit: 64 (fp4_gemm.cuh, one SM a unit), 128 or 256
-// (fp4_gemm_pair.cu, a pair of SMs).  The smallest that makes one round of the
-// SMs, else the largest that groups fill.  Measured in us at 64 / 128 / 256: dense
-// N = K = 4096 m = 256 8.2 / 8.8 / 10.7, m = 512 13.3 / 9.2 / 11.1, m = 1024 23 / 13.6 / 11.9;
-// N = 2048 K = 1408 m = 512 5.2 / 6.7 / 8.0, m = 1024 7.4 / 7.0 / 8.2.  Ragged groups take the
+// (fp4_gemm_pair.cu, a pair of SMs).  Dense: 64 where that makes one round of the SMs,
+// else by the rounds of the pairs, one with 128 rows taken as 0.7 of one with 256.
+// Measured in us at 64 / 128 / 256: N = K = 4096 m = 256 8.1 / 8.7 / 10.5, m = 512 13.3 / 9.0 / 10.7,
+// m = 1024 23 / 13.3 / 11.3; N = 2048 K = 1408 m = 512 5.1 / 6.3 / 7.8, m = 1024 7.4 / 6.5 / 7.9;
+// N = 11264 K = 4096 m = 384 - / 14.2 / 18.0, m = 512 - / 17.7 / 17.1.  Ragged groups take the
 // unit by their mean, which popular experts exceed (64 groups N = 2816 K = 2048, popularities
 // spread by e^N(0, 1/2), or e^N(0, 1) up to a mean of 24): mean 8 36.4 / 36.1, 24 39.8 / 38.5, 40 41.4 /
 // 40.1 / 42.0, 64 50.1 / 41.1 / 44.1, 96 65 / 45.7 / 44.8, 112 71 / 47.5 / 45.5, 144 87 / 52.2 / 48.3; without
@@ -150,8 +151,8 @@ int unit_rows(const b4_fp4_config* c, bool ragged, int sms) {
     return per <= 16 ? 64 : per <= 104 ? 128 : 256;
   }
   if (c->m <= 64 || groups * cdiv(c->m, 64) * cdiv(c->n, 128) <= sms) return 64;
-  if (c->m <= 128 || groups * cdiv(c->m, 128) * cdiv(c->n, 256) <= sms / 2) return 128;
-  return 256;
+  auto rounds = [&](int nt) { return (groups * cdiv(c->m, nt) * cdiv(c->n, 256) + sms / 2 - 1) / (sms / 2); };
+  return 7 * rounds(128) < 10 * rounds(256) ? 128 : 256;
 }
 
 // CTAs that share a unit along K where the units are fewer than the SMs.  A CTA
