@@ -434,8 +434,9 @@ b4_status b4_fp4_tile_scales(const b4_fp4_config* cfg, const uint8_t* src, uint8
 /* out[t][n] = gs_a gs_w[e] sum_k (scale e2m1)_a[t][k] (scale e2m1)_w[e][n][k] for the
  * rows t of group e, accumulated in fp32 by the tensor cores and rounded once.
  *
- * a_codes, a_scales  quantised activations (tiled scales); a_gs by gs_mode: per row
- *               (ROW), per group (GIVEN, TENSOR), NULL (MXFP4).
+ * a_codes, a_scales  quantised activations, tiled scales (a scale_layout of ROWS is
+ *               refused); a_gs by gs_mode: per row (ROW), per group (GIVEN, TENSOR),
+ *               NULL (MXFP4).
  * w_codes       [num_groups][n][ld]; w_scales tiles of the stack of n-row matrices;
  *               w_gs [num_groups] (NVFP4).
  * offsets       NULL: a stack of m rows per group.
@@ -445,7 +446,7 @@ b4_status b4_fp4_tile_scales(const b4_fp4_config* cfg, const uint8_t* src, uint8
  *               outside [0, m) are dropped): packed routes go back to route order.
  * device_status NULL, or 2 uint32 that the caller has zeroed: B4_ERR_TIMEOUT and the
  *               wait site if a bounded wait ran out, untouched otherwise.
- * 1 launch.  Does not read x, x_rows, x_stride, row_div, activation, scale_layout. */
+ * 1 launch.  Does not read x_dtype, x_rows, x_stride, row_div, activation. */
 b4_status b4_fp4_matmul(const b4_fp4_config* cfg, const uint8_t* a_codes, const uint8_t* a_scales, const float* a_gs,
                         const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gs, const int32_t* offsets,
                         const int32_t* out_rows, void* out, uint32_t* device_status, b4_stream_t stream);

@@ -1,0 +1,51 @@
+"""Refusals of the FP4 operators that keep a launch inside its buffers or from a wrong reading of them (CPU: every one
+of them comes before any device is looked up)."""
+
+import ctypes
+
+import pytest
+import torch
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def b4():
+    import __graft_entry__
+
+    __graft_entry__._build_module().build()
+    import w4a16_moe_gb300 as mod
+
+    return mod
+
+
+@pytest.fixture()
+def addr():
+    buf = ctypes.create_string_buffer(1 << 12)
+    return (ctypes.addressof(buf) + 255) // 256 * 256, buf
+
+
+def _weights(n, k, groups=1):
+    """Zero weights as a product takes them: codes, tiled scales, global scales."""
+    ld = -(-(k // 2) // 16) * 16
+    return (torch.zeros(groups, n, ld, dtype=torch.uint8),
+            torch.zeros(groups, -(-n // 128), -(-k // 64), 32, 4, 4, dtype=torch.uint8), torch.ones(groups))
+
+
+@pytest.mark.parametrize("m", [0, 4])
+def test_product_refuses_row_major_scales(b4, addr, m):
+    """The product reads whole tiles: scales in the checkpoint's layout are too short for it."""
+    a = addr[0]
+    cfg = b4.Fp4Config(m=m, k=64, n=8, scale_layout=b4.SCALES_ROWS)
+    st = b4.raw_lib().b4_fp4_matmul(cfg._ref, a, a, a, a, a, a, None, None, a, None, None)
+    assert st == b4.B4_ERR_INVALID_ARGUMENT and "tiled scales" in b4.last_error()
+    if m == 0:
+        return
+    codes, scales, gs = b4.fp4_empty(cfg, "cpu")
+    assert scales.numel() == 16  # of the 512 bytes of a tile
+    with pytest.raises((b4.B4Error, ValueError), match="tiled scales"):
+        b4.fp4_matmul(cfg, codes, scales, gs, *_weights(8, 64), torch.zeros(4, 8, dtype=BF), stream=_NoStream)
+
+
+class _NoStream:
+    cuda_stream = None

@@ -431,6 +431,7 @@ b4_status b4_fp4_matmul(const b4_fp4_config* cfg, const uint8_t* a_codes, const 
   if (st != B4_OK) return st;
   if ((st = check_n(cfg)) != B4_OK) return st;
   if ((st = check_rows(cfg, offsets)) != B4_OK) return st;
+  if (cfg->scale_layout != B4_FP4_SCALES_TILED) FP4_INVALID("b4_fp4_matmul takes tiled scales");
   if (cfg->m == 0) return B4_OK;
   if (!a_codes || !a_scales || !out) FP4_INVALID("null pointer argument");
   if ((cfg->gs_mode == B4_FP4_GS_NONE) != (a_gs == nullptr))
