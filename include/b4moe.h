@@ -428,7 +428,8 @@ size_t b4_fp4_scale_bytes(const b4_fp4_config* cfg, int32_t ragged);
 b4_status b4_fp4_quantize(const b4_fp4_config* cfg, const void* x, const int32_t* rows, const int32_t* offsets,
                           float* gs, uint8_t* codes, uint8_t* scales, void* values, b4_stream_t stream);
 
-/* Row-major scales of a checkpoint, [num_groups][m][k / g], into tiles. */
+/* Row-major scales of a checkpoint, [num_groups][m][k / g], into tiles: dst holds
+ * b4_fp4_scale_bytes(cfg, 0) bytes (a scale_layout of ROWS is refused). */
 b4_status b4_fp4_tile_scales(const b4_fp4_config* cfg, const uint8_t* src, uint8_t* dst, b4_stream_t stream);
 
 /* out[t][n] = gs_a gs_w[e] sum_k (scale e2m1)_a[t][k] (scale e2m1)_w[e][n][k] for the

@@ -49,3 +49,12 @@ def test_product_refuses_row_major_scales(b4, addr, m):
 
 class _NoStream:
     cuda_stream = None
+
+
+def test_tiling_refuses_a_row_major_config(b4, addr):
+    """b4_fp4_scale_bytes of such a config is the source's size, less than the tiles that would be written."""
+    a = addr[0]
+    cfg = b4.Fp4Config(m=1, k=64, scale_layout=b4.SCALES_ROWS)
+    assert b4.fp4_scale_bytes(cfg) == 4
+    st = b4.raw_lib().b4_fp4_tile_scales(cfg._ref, a, a, None)
+    assert st == b4.B4_ERR_INVALID_ARGUMENT and "tiled scales" in b4.last_error()

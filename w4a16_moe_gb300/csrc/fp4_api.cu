@@ -413,6 +413,7 @@ b4_status b4_fp4_quantize(const b4_fp4_config* cfg, const void* x, const int32_t
 b4_status b4_fp4_tile_scales(const b4_fp4_config* cfg, const uint8_t* src, uint8_t* dst, b4_stream_t stream) {
   b4_status st = check(cfg);
   if (st != B4_OK) return st;
+  if (cfg->scale_layout != B4_FP4_SCALES_TILED) FP4_INVALID("b4_fp4_tile_scales writes tiled scales");
   if (cfg->m == 0) return B4_OK;
   if (!src || !dst) FP4_INVALID("null pointer argument");
   if (!aligned(dst, 16)) FP4_INVALID("dst must be 16-byte aligned");
