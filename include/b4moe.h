@@ -443,8 +443,9 @@ b4_status b4_fp4_tile_scales(const b4_fp4_config* cfg, const uint8_t* src, uint8
  * offsets       NULL: a stack of m rows per group.
  * out           [rows][out_stride].  Ragged without out_rows: written in full, rows
  *               past offsets[num_groups] as zeros.
- * out_rows      NULL, or the output row of each operand row ([m] int32; entries
- *               outside [0, m) are dropped): packed routes go back to route order.
+ * out_rows      NULL, or the output row of each operand row ([rows] int32, rows = m of
+ *               a ragged operand and num_groups * m of a stack; entries outside
+ *               [0, rows) are dropped): packed routes go back to route order.
  * device_status NULL, or 2 uint32 that the caller has zeroed: B4_ERR_TIMEOUT and the
  *               wait site if a bounded wait ran out, untouched otherwise.
  * 1 launch.  Does not read x_dtype, x_rows, x_stride, row_div, activation. */

@@ -704,3 +704,22 @@ def test_layer_with_4bit_activations(b4, name, wl, m):
         out = torch.full((m, wl.hidden), float("nan"), dtype=BF, device="cuda")
         b4.fused_moe_a4(*args[:8], none, args[9], act, out, ws)
         assert not out.any()
+
+
+@pytest.mark.parametrize("fmt,groups,m,n,k", [(NV, 3, 70, 130, 112), (NV, 2, 5, 130, 2048), (NV, 3, 300, 1500, 112),
+                                              (MX, 2, 700, 2603, 96)])
+def test_scatter_of_a_stack(b4, fmt, groups, m, n, k):
+    """out_rows of a stack has an entry for each of its groups * m rows and may name any of them."""
+    rows = groups * m
+    cfg = b4.Fp4Config(m=m, n=n, k=k, num_groups=groups, format=b4.FORMATS[fmt])
+    _, _, ad = _operand(b4, cfg, fmt, _np(_randn((rows, k), 81, BF)))
+    _, wd = _weights(fmt, groups, n, k, 82)
+    plain, got = (torch.full((rows, n), 7.0, dtype=BF, device="cuda") for _ in range(2))
+    b4.fp4_matmul(cfg, *ad, *wd, plain)
+    to = np.random.default_rng(83).permutation(rows).astype(np.int32)
+    to[1], to[m] = -1, rows  # dropped
+    b4.fp4_matmul(cfg, *ad, *wd, got, out_rows=dev(to))
+    want = torch.full_like(plain, 7.0)
+    kept = (to >= 0) & (to < rows)
+    want[torch.from_numpy(to[kept]).long().cuda()] = plain[torch.from_numpy(np.flatnonzero(kept)).cuda()]
+    assert (to[kept] >= m).any() and torch.equal(got, want)

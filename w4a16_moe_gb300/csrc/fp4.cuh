@@ -78,6 +78,7 @@ struct Fp4GemmParams {
   int groups, m, n, k;       // m: rows per group (stack) or row capacity (ragged)
   const int32_t* offsets;    // ragged, or null
   const int32_t* out_rows;   // output row of each activation row, or null
+  int out_rows_end;          // rows of the operand: entries of out_rows outside [0, this) are dropped
   void* out;
   int64_t out_stride;        // elements
   int out_dtype;             // 0 bf16, 1 f16, 2 f32

@@ -191,6 +191,7 @@ Fp4GemmParams product_params(const b4_fp4_config* c, const uint8_t* w_scales, co
   p.k = c->k;
   p.offsets = offsets;
   p.out_rows = out_rows;
+  p.out_rows_end = (int)operand_rows(c, offsets);
   p.out = out;
   p.out_stride = c->out_stride ? c->out_stride : c->n;
   p.out_dtype = c->out_dtype;

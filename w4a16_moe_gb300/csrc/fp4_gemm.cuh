@@ -135,7 +135,7 @@ __device__ __forceinline__ void quantize_unit(const Fp4GemmParams& p, const Unit
     int to = at;
     if (p.out_rows) {
       to = __ldg(p.out_rows + at);
-      if (to >= p.m) to = -1;
+      if (to >= p.out_rows_end) to = -1;
     }
     tab.g[0][r] = gw * gs;
     tab.to[0][r] = to;

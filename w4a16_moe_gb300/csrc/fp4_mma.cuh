@@ -290,7 +290,7 @@ __device__ __forceinline__ void fill_rows(const Fp4GemmParams& p, const Groups& 
         to = at;
         if (p.out_rows) {
           to = __ldg(p.out_rows + at);
-          if (to >= p.m) to = -1;
+          if (to >= p.out_rows_end) to = -1;
         }
       }
       tab.g[b][r] = g;
