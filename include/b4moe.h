@@ -424,7 +424,8 @@ size_t b4_fp4_scale_bytes(const b4_fp4_config* cfg, int32_t ragged);
  * Tiled scales of a stack are written in full, the missing rows of its last row
  * tiles as zeros; those of a ragged operand only where rows are live, and its rows
  * past offsets[num_groups] are not written at all.
- * TENSOR takes neither rows nor offsets.  1 launch (TENSOR: a memset and 3). */
+ * TENSOR takes neither rows nor offsets.  1 launch (TENSOR: a memset and 3); m = 0
+ * launches nothing and writes nothing. */
 b4_status b4_fp4_quantize(const b4_fp4_config* cfg, const void* x, const int32_t* rows, const int32_t* offsets,
                           float* gs, uint8_t* codes, uint8_t* scales, void* values, b4_stream_t stream);
 

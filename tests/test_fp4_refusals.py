@@ -58,3 +58,18 @@ def test_tiling_refuses_a_row_major_config(b4, addr):
     assert b4.fp4_scale_bytes(cfg) == 4
     st = b4.raw_lib().b4_fp4_tile_scales(cfg._ref, a, a, None)
     assert st == b4.B4_ERR_INVALID_ARGUMENT and "tiled scales" in b4.last_error()
+
+
+@pytest.mark.parametrize("fmt,mode", [(0, "ROW"), (0, "TENSOR"), (1, "NONE")])
+def test_empty_calls_are_accepted(b4, fmt, mode):
+    """No rows: every buffer of rows is empty, its address null, and nothing is launched."""
+    cfg = b4.Fp4Config(m=0, k=64, n=8, format=fmt, gs_mode=getattr(b4, "GS_" + mode))
+    x, parts = torch.zeros(0, 64, dtype=BF), b4.fp4_empty(cfg, "cpu")
+    b4.fp4_quantize(cfg, x, *parts, values=torch.zeros_like(x), stream=_NoStream)
+    w = _weights(8, 64)
+    w = w[:2] + (w[2] if fmt == 0 else None,)
+    out = torch.zeros(0, 8, dtype=BF)
+    b4.fp4_matmul(cfg, *parts, *w, out, stream=_NoStream)
+    if mode != "TENSOR":
+        ws = torch.zeros(b4.fp4_linear_workspace_bytes(cfg), dtype=torch.uint8)
+        b4.fp4_linear(cfg, x, *w, out, ws, stream=_NoStream)

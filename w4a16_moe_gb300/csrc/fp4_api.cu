@@ -393,9 +393,9 @@ b4_status b4_fp4_quantize(const b4_fp4_config* cfg, const void* x, const int32_t
   if ((st = check_rows(cfg, offsets)) != B4_OK) return st;
   if (cfg->gs_mode == B4_FP4_GS_TENSOR && (rows || offsets))
     FP4_INVALID("one global scale per matrix (B4_FP4_GS_TENSOR) takes neither rows nor offsets");
+  if (cfg->m == 0) return B4_OK;
   if ((cfg->gs_mode == B4_FP4_GS_NONE) != (gs == nullptr))
     FP4_INVALID("gs must be given for NVFP4 and NULL for MXFP4");
-  if (cfg->m == 0) return B4_OK;
   if (!x || !codes || !scales) FP4_INVALID("null pointer argument");
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(values, 16))
     FP4_INVALID("codes, scales and values must be 16-byte aligned");
