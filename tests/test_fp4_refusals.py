@@ -73,3 +73,17 @@ def test_empty_calls_are_accepted(b4, fmt, mode):
     if mode != "TENSOR":
         ws = torch.zeros(b4.fp4_linear_workspace_bytes(cfg), dtype=torch.uint8)
         b4.fp4_linear(cfg, x, *w, out, ws, stream=_NoStream)
+
+
+@pytest.mark.parametrize("x", [torch.zeros(63, dtype=BF), torch.zeros(1, 62, dtype=BF), torch.zeros(0, 64, dtype=BF)])
+def test_gather_needs_a_row_to_gather_from(b4, x):
+    """An x shorter than one row bounds gathered rows by 0, which the library takes for no bound."""
+    cfg = b4.Fp4Config(m=4, k=64, n=8)
+    rows = torch.tensor([0, -1, 5, 100], dtype=torch.int32)
+    with pytest.raises(ValueError, match="not one row"):
+        b4.fp4_quantize(cfg, x, *b4.fp4_empty(cfg, "cpu"), rows=rows, stream=_NoStream)
+    ws = torch.zeros(b4.fp4_linear_workspace_bytes(cfg), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="not one row"):
+        b4.fp4_linear(cfg, x, *_weights(8, 64), torch.zeros(4, 8, dtype=BF), ws, rows=rows, stream=_NoStream)
+    none = b4.Fp4Config(m=0, k=64, n=8)
+    b4.fp4_quantize(none, x, *b4.fp4_empty(none, "cpu"), rows=rows[:0], stream=_NoStream)  # nothing to gather

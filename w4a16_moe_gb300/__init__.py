@@ -441,6 +441,8 @@ def _fp4_x(cfg, x, rows, ragged):
     if rows is None:
         if n < cfg.rows(ragged):
             raise ValueError(f"x holds {n} rows, {cfg.rows(ragged)} needed")
+    elif n == 0 and cfg.m:  # (a bound of 0 rows would be none)
+        raise ValueError(f"x holds not one row of {cfg.width} elements to gather from")
     elif not 0 < cfg._struct.x_rows <= n:
         bounded = cfg._gather
         if bounded[0] != n:
