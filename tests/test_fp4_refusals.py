@@ -87,3 +87,48 @@ def test_gather_needs_a_row_to_gather_from(b4, x):
         b4.fp4_linear(cfg, x, *_weights(8, 64), torch.zeros(4, 8, dtype=BF), ws, rows=rows, stream=_NoStream)
     none = b4.Fp4Config(m=0, k=64, n=8)
     b4.fp4_quantize(none, x, *b4.fp4_empty(none, "cpu"), rows=rows[:0], stream=_NoStream)  # nothing to gather
+
+
+def _layer(b4, hidden=352, inter=160, act=0, m=3, top_k=2, experts=5, fmt=0):
+    """Config and valid arguments of the layer with 4-bit activations."""
+    cfg = b4.MoEConfig(m, top_k, experts, experts, hidden, inter, format=fmt)
+    n1 = inter if act == b4.RELU2 else 2 * inter
+    kt = (lambda k: -(-k // 64)) if fmt == 0 else (lambda k: -(-k // 128))
+    ld = lambda k: -(-(k // 2) // 16) * 16  # noqa: E731
+    args = dict(
+        x=torch.zeros(m, hidden, dtype=BF), w13=torch.zeros(experts, n1, ld(hidden), dtype=torch.uint8),
+        s13=torch.zeros(experts, -(-n1 // 128), kt(hidden), 32, 4, 4, dtype=torch.uint8),
+        gs13=torch.ones(experts) if fmt == 0 else None,
+        w2=torch.zeros(experts, hidden, ld(inter), dtype=torch.uint8),
+        s2=torch.zeros(experts, -(-hidden // 128), kt(inter), 32, 4, 4, dtype=torch.uint8),
+        gs2=torch.ones(experts) if fmt == 0 else None, topk_ids=torch.zeros(m, top_k, dtype=torch.int32),
+        topk_weights=torch.ones(m, top_k), activation=act, out=torch.zeros(m, hidden, dtype=BF),
+        workspace=torch.zeros(0, dtype=torch.uint8))  # too small: a call that passes the binding ends there
+    return cfg, args
+
+
+@pytest.mark.parametrize("act,fmt", [(0, 0), (1, 0), (2, 1)])
+def test_layer_refuses_short_buffers(b4, act, fmt):
+    """Every buffer of the layer is as large as the kernels read it; one element less is named and refused."""
+    cfg, args = _layer(b4, act=act, fmt=fmt)
+    with pytest.raises(b4.B4Error) as ei:
+        b4.fused_moe_a4(cfg, **args, stream=_NoStream)
+    assert ei.value.status == b4.B4_ERR_INVALID_ARGUMENT  # (no workspace at all)
+    for name, t in args.items():
+        if isinstance(t, torch.Tensor) and name != "workspace":
+            with pytest.raises(ValueError, match=rf"^{name} needs {t.numel()} elements, got {t.numel() - 1}$"):
+                b4.fused_moe_a4(cfg, **{**args, name: t.reshape(-1)[:-1]}, stream=_NoStream)
+            with pytest.raises(TypeError, match=f"^{name} must be"):
+                b4.fused_moe_a4(cfg, **{**args, name: t.to(torch.int16)}, stream=_NoStream)
+    with pytest.raises(TypeError, match="^w13 must be"):
+        b4.fused_moe_a4(cfg, **{**args, "w13": None}, stream=_NoStream)
+
+
+@pytest.mark.parametrize("hidden,inter,name", [(336, 160, "w13"), (352, 176, "w2")])
+def test_layer_refuses_a_checkpoints_unpadded_codes(b4, hidden, inter, name):
+    """K % 32 == 16: the kernels' rows of codes are 8 bytes further apart than the checkpoint's."""
+    cfg, args = _layer(b4, hidden, inter)
+    unpadded = args[name][..., :-8].contiguous()
+    assert unpadded.shape[-1] == (hidden if name == "w13" else inter) // 2
+    with pytest.raises(ValueError, match=f"^{name} needs"):
+        b4.fused_moe_a4(cfg, **{**args, name: unpadded}, stream=_NoStream)

@@ -419,8 +419,7 @@ class Fp4Config:
         """(code bytes, scale bytes) of the weights."""
         s = self._sizes.get("w")
         if s is None:
-            tiles = self.num_groups * -(-self.n // 128) * -(-self.k // (64 if self.format == NVFP4 else 128))
-            s = self._sizes["w"] = (self.num_groups * self.n * self.ld, 512 * tiles)
+            s = self._sizes["w"] = _stack_bytes(self.num_groups, self.n, self.k, self.format)
         return s
 
 
@@ -601,24 +600,36 @@ def fused_moe_a4_workspace_bytes(cfg: MoEConfig, activation: int) -> int:
     return int(n)
 
 
+def _layer_buffer(t, dtype, n, name):
+    """As _fp4_buffer, for an argument that has to be there."""
+    if t is None:
+        _need(t, dtype, name)
+    return _fp4_buffer(t, dtype, n, name)
+
+
+def _stack_bytes(e, n, k, format):
+    """(code bytes, scale bytes) of a stack of e quantised [n, k] matrices."""
+    return e * n * ((k // 2 + 15) // 16 * 16), 512 * e * -(-n // 128) * -(-k // (64 if format == NVFP4 else 128))
+
+
 def fused_moe_a4(cfg: MoEConfig, x, w13, s13, gs13, w2, s2, gs2, topk_ids, topk_weights, activation, out, workspace,
                  stream=None):
     """The fused layer with 4-bit activations (``b4_fused_moe_a4``): weights as quantised operands
-    (``fp4_quantize``, or checkpoint codes with ``fp4_tile_scales``); ``out`` [m, H] bf16 is written in full."""
-    _need(x, torch.bfloat16, "x")
-    _need(out, torch.bfloat16, "out")
-    _need(topk_ids, torch.int32, "topk_ids")
-    _need(topk_weights, torch.float32, "topk_weights")
+    (``fp4_quantize``, or checkpoint codes with ``fp4_tile_scales``: rows of codes are K/2 bytes rounded up to 16
+    apart, so a checkpoint's codes are used as they are where hidden and inter are multiples of 32); ``out`` [m, H]
+    bf16 is written in full."""
+    e, m, h, i = cfg.num_local_experts, cfg.m, cfg.hidden, cfg.inter
+    w13_bytes, s13_bytes = _stack_bytes(e, i if activation == RELU2 else 2 * i, h, cfg.format)
+    w2_bytes, s2_bytes = _stack_bytes(e, h, i, cfg.format)
     _need(workspace, torch.uint8, "workspace")
-    for t, n in ((w13, "w13"), (s13, "s13"), (w2, "w2"), (s2, "s2")):
-        _need(t, torch.uint8, n)
-    for t, n in ((gs13, "gs13"), (gs2, "gs2")):
-        if t is not None:
-            _need(t, torch.float32, n)
     c = cfg._c()
-    _check(_lib.b4_fused_moe_a4(ctypes.byref(c), _ptr(x), _ptr(w13), _ptr(s13), _ptr(gs13), _ptr(w2), _ptr(s2),
-                                _ptr(gs2), _ptr(topk_ids), _ptr(topk_weights), int(activation), _ptr(out),
-                                _ptr(workspace), workspace.numel(), _stream(stream)))
+    _check(_lib.b4_fused_moe_a4(
+        ctypes.byref(c), _layer_buffer(x, torch.bfloat16, m * h, "x"), _layer_buffer(w13, _U8, w13_bytes, "w13"),
+        _layer_buffer(s13, _U8, s13_bytes, "s13"), _fp4_buffer(gs13, _F32, e, "gs13"),
+        _layer_buffer(w2, _U8, w2_bytes, "w2"), _layer_buffer(s2, _U8, s2_bytes, "s2"), _fp4_buffer(gs2, _F32, e, "gs2"),
+        _layer_buffer(topk_ids, _I32, m * cfg.top_k, "topk_ids"),
+        _layer_buffer(topk_weights, _F32, m * cfg.top_k, "topk_weights"), int(activation),
+        _layer_buffer(out, torch.bfloat16, m * h, "out"), _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 def fused_moe_raw(cfg: MoEConfig, ptrs: dict, activation: int, workspace_ptr: int, workspace_bytes_: int,
