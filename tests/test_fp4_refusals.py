@@ -132,3 +132,33 @@ def test_layer_refuses_a_checkpoints_unpadded_codes(b4, hidden, inter, name):
     assert unpadded.shape[-1] == (hidden if name == "w13" else inter) // 2
     with pytest.raises(ValueError, match=f"^{name} needs"):
         b4.fused_moe_a4(cfg, **{**args, name: unpadded}, stream=_NoStream)
+
+
+@pytest.mark.parametrize("fmt,n,k", [(0, 128, 64), (0, 256, 192), (1, 128, 256)])
+def test_scales_that_were_not_tiled_are_refused(b4, fmt, n, k):
+    """Where a matrix fills its tiles, row-major scales have the tiles' size: they are told by their shape."""
+    cfg = b4.Fp4Config(m=128, n=n, k=k, num_groups=2, format=fmt)
+    parts = b4.fp4_empty(cfg, "cpu")
+    codes, gs = torch.zeros(2, n, k // 2, dtype=torch.uint8), torch.ones(2) if fmt == 0 else None
+    rows = torch.zeros(2, n, cfg.blocks, dtype=torch.uint8)
+    tiles = torch.zeros(2, n // 128, k // (64 if fmt == 0 else 128), 32, 4, 4, dtype=torch.uint8)
+    assert rows.numel() == tiles.numel()
+    out = torch.zeros(256, n, dtype=BF)
+    with pytest.raises(ValueError, match="^w_scales has the row-major shape"):
+        b4.fp4_matmul(cfg, *parts, codes, rows, gs, out, stream=_NoStream)
+    with pytest.raises(ValueError, match="^a_scales has the row-major shape"):
+        b4.fp4_matmul(cfg, parts[0], parts[1].view(2, 128, cfg.blocks), parts[2], codes, tiles, gs, out, stream=_NoStream)
+    lin = b4.Fp4Config(m=4, n=n, k=k, format=fmt)
+    ws = torch.zeros(b4.fp4_linear_workspace_bytes(lin), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="^w_scales has the row-major shape"):
+        b4.fp4_linear(lin, torch.zeros(4, k, dtype=BF), codes[:1], rows[:1], None if gs is None else gs[:1],
+                      torch.zeros(4, n, dtype=BF), ws, stream=_NoStream)
+    cfg, args = _layer(b4, hidden=256, inter=128, fmt=fmt)
+    for name, n, k in (("s13", 256, 256), ("s2", 256, 128)):
+        bad = torch.zeros(5, n, k // (16 if fmt == 0 else 32), dtype=torch.uint8)
+        assert bad.numel() == args[name].numel()
+        with pytest.raises(ValueError, match=f"^{name} has the row-major shape"):
+            b4.fused_moe_a4(cfg, **{**args, name: bad}, stream=_NoStream)
+        flat = {**args, name: args[name].view(-1)}  # tiles in another shape are tiles
+        with pytest.raises(b4.B4Error):
+            b4.fused_moe_a4(cfg, **flat, stream=_NoStream)

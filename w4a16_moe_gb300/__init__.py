@@ -396,6 +396,7 @@ class Fp4Config:
         self.x_stride = int(x_stride) or self.width
         self.out_stride = int(out_stride) or self.n
         self.ld = (self.k // 2 + 15) // 16 * 16
+        self.blocks = self.k // (16 if format == NVFP4 else 32)
         self._struct = _Fp4Config(self.m, self.n, self.k, self.num_groups, format, DTYPES[x_dtype], DTYPES[out_dtype],
                                   -1 if activation is None else activation, gs_mode, scale_layout, int(row_div),
                                   int(x_rows), *swiglu, int(x_stride), int(out_stride))
@@ -463,6 +464,16 @@ def _fp4_buffer(t, dtype, n, name):
         return None
     _need(t, dtype, name)
     raise ValueError(f"{name} needs {n} elements, got {t.numel()}")
+
+
+def _fp4_tiles(t, nbytes, name, e, n, blocks):
+    """Address of the tiled scales of e matrices of n rows of ``blocks`` scales.  The row-major scales of a checkpoint
+    have the same size where the matrices fill their tiles, so they are told by their shape (rows of 512 are left
+    alone: that may be a view of the tiles)."""
+    p = _fp4_buffer(t, _U8, nbytes, name)
+    if t is not None and t.dim() == 3 and t.shape == (e, n, blocks) and blocks != 512:
+        raise ValueError(f"{name} has the row-major shape of a checkpoint's scales; tiled scales are needed (fp4_tile_scales)")
+    return p
 
 
 def fp4_codes_bytes(cfg: Fp4Config, ragged=False) -> int:
@@ -552,8 +563,9 @@ def fp4_matmul(cfg: Fp4Config, a_codes, a_scales, a_gs, w_codes, w_scales, w_gs,
     w_bytes, ws_bytes = cfg._weight_sizes()
     st = _lib.b4_fp4_matmul(
         cfg._ref, _fp4_buffer(a_codes, torch.uint8, code_bytes, "a_codes"),
-        _fp4_buffer(a_scales, torch.uint8, scale_bytes, "a_scales"), _fp4_buffer(a_gs, torch.float32, gs_n, "a_gs"),
-        _fp4_buffer(w_codes, torch.uint8, w_bytes, "w_codes"), _fp4_buffer(w_scales, torch.uint8, ws_bytes, "w_scales"),
+        _fp4_tiles(a_scales, scale_bytes, "a_scales", cfg.num_groups, cfg.m, cfg.blocks), _fp4_buffer(a_gs, torch.float32, gs_n, "a_gs"),
+        _fp4_buffer(w_codes, torch.uint8, w_bytes, "w_codes"),
+        _fp4_tiles(w_scales, ws_bytes, "w_scales", cfg.num_groups, cfg.n, cfg.blocks),
         _fp4_buffer(w_gs, torch.float32, cfg.num_groups, "w_gs"),
         _fp4_buffer(offsets, torch.int32, cfg.num_groups + 1, "offsets"),
         _fp4_buffer(out_rows, torch.int32, n, "out_rows"), _fp4_out(cfg, out, n),
@@ -584,7 +596,8 @@ def fp4_linear(cfg: Fp4Config, x, w_codes, w_scales, w_gs, out, workspace, x_gs=
         x_gs if x_gs is None else _fp4_buffer(x_gs, _F32, cfg.num_groups, "x_gs"),
         rows if rows is None else _fp4_buffer(rows, _I32, m, "rows"),
         _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None,
-        _fp4_buffer(w_codes, _U8, w_bytes, "w_codes"), _fp4_buffer(w_scales, _U8, ws_bytes, "w_scales"),
+        _fp4_buffer(w_codes, _U8, w_bytes, "w_codes"),
+        _fp4_tiles(w_scales, ws_bytes, "w_scales", cfg.num_groups, cfg.n, cfg.blocks),
         w_gs if w_gs is None else _fp4_buffer(w_gs, _F32, cfg.num_groups, "w_gs"),
         out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, m, "out_rows"), _fp4_out(cfg, out, m),
         _fp4_buffer(workspace, _U8, 0, "workspace"), workspace.numel(), _stream_of(stream, x))
@@ -607,6 +620,12 @@ def _layer_buffer(t, dtype, n, name):
     return _fp4_buffer(t, dtype, n, name)
 
 
+def _layer_tiles(t, nbytes, name, e, n, blocks):
+    if t is None:
+        _need(t, _U8, name)
+    return _fp4_tiles(t, nbytes, name, e, n, blocks)
+
+
 def _stack_bytes(e, n, k, format):
     """(code bytes, scale bytes) of a stack of e quantised [n, k] matrices."""
     return e * n * ((k // 2 + 15) // 16 * 16), 512 * e * -(-n // 128) * -(-k // (64 if format == NVFP4 else 128))
@@ -619,14 +638,16 @@ def fused_moe_a4(cfg: MoEConfig, x, w13, s13, gs13, w2, s2, gs2, topk_ids, topk_
     apart, so a checkpoint's codes are used as they are where hidden and inter are multiples of 32); ``out`` [m, H]
     bf16 is written in full."""
     e, m, h, i = cfg.num_local_experts, cfg.m, cfg.hidden, cfg.inter
-    w13_bytes, s13_bytes = _stack_bytes(e, i if activation == RELU2 else 2 * i, h, cfg.format)
+    n1, g = i if activation == RELU2 else 2 * i, 16 if cfg.format == NVFP4 else 32
+    w13_bytes, s13_bytes = _stack_bytes(e, n1, h, cfg.format)
     w2_bytes, s2_bytes = _stack_bytes(e, h, i, cfg.format)
     _need(workspace, torch.uint8, "workspace")
     c = cfg._c()
     _check(_lib.b4_fused_moe_a4(
         ctypes.byref(c), _layer_buffer(x, torch.bfloat16, m * h, "x"), _layer_buffer(w13, _U8, w13_bytes, "w13"),
-        _layer_buffer(s13, _U8, s13_bytes, "s13"), _fp4_buffer(gs13, _F32, e, "gs13"),
-        _layer_buffer(w2, _U8, w2_bytes, "w2"), _layer_buffer(s2, _U8, s2_bytes, "s2"), _fp4_buffer(gs2, _F32, e, "gs2"),
+        _layer_tiles(s13, s13_bytes, "s13", e, n1, h // g), _fp4_buffer(gs13, _F32, e, "gs13"),
+        _layer_buffer(w2, _U8, w2_bytes, "w2"), _layer_tiles(s2, s2_bytes, "s2", e, h, i // g),
+        _fp4_buffer(gs2, _F32, e, "gs2"),
         _layer_buffer(topk_ids, _I32, m * cfg.top_k, "topk_ids"),
         _layer_buffer(topk_weights, _F32, m * cfg.top_k, "topk_weights"), int(activation),
         _layer_buffer(out, torch.bfloat16, m * h, "out"), _ptr(workspace), workspace.numel(), _stream(stream)))
