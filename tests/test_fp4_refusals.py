@@ -162,3 +162,55 @@ def test_scales_that_were_not_tiled_are_refused(b4, fmt, n, k):
         flat = {**args, name: args[name].view(-1)}  # tiles in another shape are tiles
         with pytest.raises(b4.B4Error):
             b4.fused_moe_a4(cfg, **flat, stream=_NoStream)
+
+
+def _passes_the_binding(call):
+    """A call on CPU tensors that the binding lets through ends at the library's device check."""
+    import w4a16_moe_gb300 as b4
+
+    with pytest.raises(b4.B4Error) as ei:
+        call()
+    return ei.value.status in (b4.B4_ERR_UNSUPPORTED_DEVICE, b4.B4_ERR_CUDA)
+
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the calls it lets through would reach the GPU")
+
+
+@no_gpu
+def test_an_x_of_longer_rows_is_refused(b4):
+    """A contiguous x whose rows are longer than the config's would be read as more and shorter rows."""
+    cfg = b4.Fp4Config(m=4, k=64, n=8)
+    ws = torch.zeros(b4.fp4_linear_workspace_bytes(cfg) + 256, dtype=torch.uint8)
+    ws = ws[-ws.data_ptr() % 256:]
+    idx = torch.zeros(4, dtype=torch.int32)
+
+    def quant(x, c=cfg, **kw):
+        return b4.fp4_quantize(c, x, *b4.fp4_empty(c, "cpu"), stream=_NoStream, **kw)
+
+    def linear(x, **kw):
+        return b4.fp4_linear(cfg, x, *_weights(8, 64), torch.zeros(4, 8, dtype=BF), ws, stream=_NoStream, **kw)
+
+    for x in (torch.zeros(4, 128, dtype=BF), torch.zeros(2, 4, 80, dtype=BF)):
+        for call in (quant, linear):
+            with pytest.raises(ValueError, match="^x has rows of"):
+                call(x)
+            with pytest.raises(ValueError, match="^x has rows of"):
+                call(x, rows=idx)
+    # the config's elements in any contiguous shape, more rows than needed, the stride said, one flat row
+    for x in (torch.zeros(4, 64), torch.zeros(9, 64), torch.zeros(2, 128), torch.zeros(4, 4, 16), torch.zeros(256),
+              torch.zeros(1, 512), torch.zeros(2, 3, 64)):
+        assert _passes_the_binding(lambda: quant(x.to(BF))) and _passes_the_binding(lambda: linear(x.to(BF)))
+    assert _passes_the_binding(lambda: quant(torch.zeros(4, 128, dtype=BF), b4.Fp4Config(m=4, k=64, x_stride=128)))
+    assert _passes_the_binding(lambda: quant(torch.zeros(4, 128, dtype=BF)[:, :64], b4.Fp4Config(m=4, k=64, x_stride=128)))
+    assert _passes_the_binding(lambda: quant(torch.zeros(2, 4, 64, dtype=BF), b4.Fp4Config(m=4, k=64, num_groups=2)))
+    assert _passes_the_binding(lambda: quant(torch.zeros(7, 64, dtype=BF), rows=idx))
+
+
+def test_the_layers_rows_are_the_configs(b4):
+    cfg, args = _layer(b4)
+    for name in ("x", "out"):
+        with pytest.raises(ValueError, match=f"^{name} has rows of 400 elements, the config rows of 352$"):
+            b4.fused_moe_a4(cfg, **{**args, name: torch.zeros(3, 400, dtype=BF)}, stream=_NoStream)
+        for t in (torch.zeros(7, 352, dtype=BF), torch.zeros(1056, dtype=BF), torch.zeros(2, 528, dtype=BF)):
+            with pytest.raises(b4.B4Error):  # passes: a larger buffer, the layer's elements in another shape
+                b4.fused_moe_a4(cfg, **{**args, name: t}, stream=_NoStream)

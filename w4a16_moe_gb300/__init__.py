@@ -424,6 +424,13 @@ class Fp4Config:
         return s
 
 
+def _wider(t, pitch, elements):
+    """Whether the rows of a contiguous tensor are longer than the config's, so that read in one go its rows would
+    not be the config's; a tensor of exactly ``elements`` (None: never) or of one row is taken as its elements."""
+    shape = t.shape
+    return len(shape) > 1 and shape[-1] > pitch and shape[-1] != t.numel() != elements
+
+
 def _fp4_x(cfg, x, rows, ragged):
     """x as the config describes it: a 2-D view of rows, or any contiguous shape with that many elements.
     Returns the call's config: with gathered rows, bounded by the rows x holds."""
@@ -432,6 +439,8 @@ def _fp4_x(cfg, x, rows, ragged):
     if x.is_contiguous():
         have = x.numel()
         n = 0 if have < cfg.width else (have - cfg.width) // cfg.x_stride + 1
+        if _wider(x, cfg.x_stride, None if rows is not None else cfg.rows(ragged) * cfg.x_stride):
+            raise ValueError(f"x has rows of {x.shape[-1]} elements, the config rows of {cfg.x_stride} (x_stride)")
     else:
         if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) != cfg.x_stride:
             raise ValueError("x must be contiguous, or two-dimensional with rows x_stride elements apart")
@@ -472,7 +481,8 @@ def _fp4_tiles(t, nbytes, name, e, n, blocks):
     alone: that may be a view of the tiles)."""
     p = _fp4_buffer(t, _U8, nbytes, name)
     if t is not None and t.dim() == 3 and t.shape == (e, n, blocks) and blocks != 512:
-        raise ValueError(f"{name} has the row-major shape of a checkpoint's scales; tiled scales are needed (fp4_tile_scales)")
+        raise ValueError(f"{name} has the row-major shape of a checkpoint's scales; "
+                         "tiled scales are needed (fp4_tile_scales)")
     return p
 
 
@@ -642,6 +652,9 @@ def fused_moe_a4(cfg: MoEConfig, x, w13, s13, gs13, w2, s2, gs2, topk_ids, topk_
     w13_bytes, s13_bytes = _stack_bytes(e, n1, h, cfg.format)
     w2_bytes, s2_bytes = _stack_bytes(e, h, i, cfg.format)
     _need(workspace, torch.uint8, "workspace")
+    for t, name in ((x, "x"), (out, "out")):
+        if t is not None and _wider(t, h, m * h):
+            raise ValueError(f"{name} has rows of {t.shape[-1]} elements, the config rows of {h}")
     c = cfg._c()
     _check(_lib.b4_fused_moe_a4(
         ctypes.byref(c), _layer_buffer(x, torch.bfloat16, m * h, "x"), _layer_buffer(w13, _U8, w13_bytes, "w13"),
