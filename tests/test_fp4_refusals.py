@@ -214,3 +214,19 @@ def test_the_layers_rows_are_the_configs(b4):
         for t in (torch.zeros(7, 352, dtype=BF), torch.zeros(1056, dtype=BF), torch.zeros(2, 528, dtype=BF)):
             with pytest.raises(b4.B4Error):  # passes: a larger buffer, the layer's elements in another shape
                 b4.fused_moe_a4(cfg, **{**args, name: t}, stream=_NoStream)
+
+
+@no_gpu
+def test_an_out_of_longer_rows_is_refused(b4):
+    """As for x: a stack's output [groups, m, width] with a width that is not the config's."""
+    cfg = b4.Fp4Config(m=4, k=64, n=8, num_groups=2)
+
+    def product(out, c=cfg):
+        return b4.fp4_matmul(c, *b4.fp4_empty(c, "cpu"), *_weights(8, 64, 2), out, stream=_NoStream)
+
+    with pytest.raises(ValueError, match="^out has rows of 16 elements"):
+        product(torch.zeros(2, 4, 16, dtype=BF))
+    for shape in ((2, 4, 8), (3, 4, 8), (64,), (2, 2, 16), (2, 4, 2, 4), (8, 8)):
+        assert _passes_the_binding(lambda: product(torch.zeros(*shape, dtype=BF)))
+    wide = b4.Fp4Config(m=4, k=64, n=8, num_groups=2, out_stride=16)
+    assert _passes_the_binding(lambda: product(torch.zeros(2, 4, 16, dtype=BF), wide))

@@ -560,6 +560,8 @@ def _fp4_out(cfg, out, rows):
     else:
         if not out.is_contiguous():
             raise ValueError("out must be contiguous, or two-dimensional with rows out_stride elements apart")
+        if _wider(out, cfg.out_stride, rows * cfg.out_stride):
+            raise ValueError(f"out has rows of {shape[-1]} elements, the config rows of {cfg.out_stride} (out_stride)")
         ok = rows == 0 or out.numel() >= (rows - 1) * cfg.out_stride + cfg.n
     if not ok:
         raise ValueError(f"out needs {rows} rows of {cfg.n} elements")
