@@ -230,3 +230,49 @@ def test_an_out_of_longer_rows_is_refused(b4):
         assert _passes_the_binding(lambda: product(torch.zeros(*shape, dtype=BF)))
     wide = b4.Fp4Config(m=4, k=64, n=8, num_groups=2, out_stride=16)
     assert _passes_the_binding(lambda: product(torch.zeros(2, 4, 16, dtype=BF), wide))
+
+
+@no_gpu
+def test_each_refusal_is_its_own(b4):
+    """Each malformed argument is refused for what it is, where the same call with it mended passes the binding."""
+    cfg = b4.Fp4Config(m=4, k=64, n=8)
+    parts = b4.fp4_empty(cfg, "cpu")
+    quant = dict(x=torch.zeros(4, 64, dtype=BF), codes=parts[0], scales=parts[1], gs=parts[2],
+                 values=torch.zeros(4, 64, dtype=BF), rows=torch.zeros(4, dtype=torch.int32))
+    w = _weights(8, 64)
+    product = dict(a_codes=parts[0], a_scales=parts[1], a_gs=parts[2], w_codes=w[0], w_scales=w[1], w_gs=w[2],
+                   out=torch.zeros(4, 8, dtype=BF), out_rows=torch.zeros(4, dtype=torch.int32))
+
+    def call(f, base, **kw):
+        return f(cfg, **{**base, **kw}, stream=_NoStream)
+
+    assert _passes_the_binding(lambda: call(b4.fp4_quantize, quant))
+    assert _passes_the_binding(lambda: call(b4.fp4_quantize, quant, rows=None))
+    assert _passes_the_binding(lambda: call(b4.fp4_matmul, product))
+    x, out = quant["x"], product["out"]
+    for kw, error, text in (
+            (dict(x=x.float()), TypeError, "x must be torch.bfloat16"), (dict(x=x[:3], rows=None), ValueError, "x holds 3 rows, 4 needed"),
+            (dict(x=x.t()), ValueError, "x must be contiguous, or two-dimensional"),
+            (dict(x=torch.zeros(4, 80, dtype=BF)[:, :64]), ValueError, "x must be contiguous, or two-dimensional"),
+            (dict(codes=parts[0][:, :2].contiguous()), ValueError, "codes needs 128 elements, got 64"),
+            (dict(codes=parts[0].to(torch.int8)), TypeError, "codes must be torch.uint8"),
+            (dict(scales=parts[1].view(-1)[:511]), ValueError, "scales needs 512 elements, got 511"),
+            (dict(gs=parts[2].view(-1)[:3]), ValueError, "gs needs 4 elements, got 3"),
+            (dict(values=quant["values"][:3]), ValueError, "values needs 256 elements, got 192"),
+            (dict(rows=torch.zeros(4, dtype=torch.int64)), TypeError, "rows must be torch.int32"),
+            (dict(rows=torch.zeros(3, dtype=torch.int32)), ValueError, "rows needs 4 elements, got 3"),
+            (dict(offsets=torch.zeros(1, dtype=torch.int32)), ValueError, "offsets needs 2 elements, got 1")):
+        with pytest.raises(error, match=text):
+            call(b4.fp4_quantize, quant, **kw)
+    for kw, error, text in (
+            (dict(w_codes=w[0][:, :7].contiguous()), ValueError, "w_codes needs 256 elements, got 224"),
+            (dict(w_scales=w[1].view(-1)[:256]), ValueError, "w_scales needs 512 elements, got 256"),
+            (dict(w_gs=w[2][:0]), ValueError, "w_gs needs 1 elements, got 0"),
+            (dict(out=out[:3]), ValueError, "out needs 4 rows of 8 elements"),
+            (dict(out=out.t().contiguous().t()), ValueError, "out rows must be contiguous"),
+            (dict(out=torch.zeros(4, 7, dtype=BF)), ValueError, "out rows must be contiguous and out_stride"),
+            (dict(out=out.float()), TypeError, "out must be torch.bfloat16"),
+            (dict(out_rows=torch.zeros(3, dtype=torch.int32)), ValueError, "out_rows needs 4 elements, got 3"),
+            (dict(device_status=torch.zeros(1, dtype=torch.int32)), ValueError, "device_status needs 2 elements, got 1")):
+        with pytest.raises(error, match=text):
+            call(b4.fp4_matmul, product, **kw)
