@@ -130,3 +130,10 @@ def test_reference_arm_prints_nothing_on_other_ranks():
     r = subprocess.run([sys.executable, os.path.join(ROOT, "bench.py"), "--impl", "reference", "--steps", "1",
                         "--warmup", "3"], capture_output=True, text=True, cwd=ROOT, timeout=600, env=env)
     assert r.returncode == 0 and r.stdout.strip() == ""
+
+
+def test_traffic_figures_belong_to_the_sources():
+    """Every recorded figure is reported: the kernels it was taken on are those in the tree (a figure of other sources
+    is taken anew or taken out, not left to read null)."""
+    for (fam, key, m), (digest, _) in bench.NCU_TRAFFIC.items():
+        assert bench.kernel_source_hash(fam) == digest, (fam, key, m)

@@ -11,7 +11,7 @@
 
 #include "b4moe.h"
 #include "fp4.cuh"
-#include "tma.cuh"
+#include "fp4_ptx.cuh"
 
 namespace b4 {
 void set_last_error(const char* fmt, ...);

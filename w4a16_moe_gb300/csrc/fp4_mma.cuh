@@ -9,8 +9,7 @@
 #include <type_traits>
 
 #include "fp4.cuh"
-#include "ptx.cuh"
-#include "tma.cuh"
+#include "fp4_ptx.cuh"
 
 namespace b4 {
 namespace fp4 {

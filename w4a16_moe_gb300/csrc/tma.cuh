@@ -47,50 +47,12 @@ inline bool make_tmap_bf16_2d(CUtensorMap* tm, const void* base, uint64_t rows, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A row-major byte matrix [rows][cols] with a row pitch of `pitch` bytes (a
-// multiple of 16): boxes of 128 bytes x `box_rows`, 128-byte swizzle.
-inline bool make_tmap_bytes_2d(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch,
-                               uint32_t box_rows) {
-  TmapEncodeFn fn = tmap_encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {pitch};
-  const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Scale tiles as rows of 512 bytes: boxes of `box_tiles` consecutive tiles.
-inline bool make_tmap_tiles(CUtensorMap* tm, const void* base, uint64_t tiles, uint32_t box_tiles) {
-  TmapEncodeFn fn = tmap_encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {128, tiles};
-  const cuuint64_t strides[1] = {512};
-  const cuuint32_t box[2] = {128, box_tiles};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Box at (column c0, row r0) -> shared memory (1024-byte aligned for the swizzle).
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* tm, int c0, int r0, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
       "[%4];" ::"r"(smem_u32(dst)),
       "l"(tm), "r"(c0), "r"(r0), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// As tma_load_2d into this CTA, signalling a barrier of either CTA of the pair
-// (`bar`: its cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int c0, int r0, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-      "%3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(tm), "r"(c0), "r"(r0), "r"(bar)
       : "memory");
 }
 
