@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 
 import torch
@@ -401,6 +402,7 @@ class Fp4Config:
                                   -1 if activation is None else activation, gs_mode, scale_layout, int(row_div),
                                   int(x_rows), *swiglu, int(x_stride), int(out_stride))
         self._ref = ctypes.byref(self._struct)
+        self._elements = (self.m * self.num_groups * self.x_stride, self.m * self.x_stride)  # of x: a stack's, ragged
         self._sizes = {}
         self._gather = (-1, None)
 
@@ -417,18 +419,18 @@ class Fp4Config:
         return s
 
     def _weight_sizes(self):
-        """(code bytes, scale bytes) of the weights."""
+        """(code bytes, scale bytes, shape of row-major scales) of the weights."""
         s = self._sizes.get("w")
         if s is None:
-            s = self._sizes["w"] = _stack_bytes(self.num_groups, self.n, self.k, self.format)
+            s = self._sizes["w"] = _stack_sizes(self.num_groups, self.n, self.k, self.format)
         return s
 
 
-def _wider(t, pitch, elements):
-    """Whether the rows of a contiguous tensor are longer than the config's, so that read in one go its rows would
-    not be the config's; a tensor of exactly ``elements`` (None: never) or of one row is taken as its elements."""
+def _wider(t, pitch):
+    """Whether a contiguous tensor has several rows that are longer than the config's, so that read in one go its rows
+    would not be the config's.  (Callers ask it of tensors that hold more than the config's elements.)"""
     shape = t.shape
-    return len(shape) > 1 and shape[-1] > pitch and shape[-1] != t.numel() != elements
+    return len(shape) > 1 and shape[-1] > pitch and shape[-1] != t.numel()
 
 
 def _fp4_x(cfg, x, rows, ragged):
@@ -438,8 +440,10 @@ def _fp4_x(cfg, x, rows, ragged):
         raise TypeError(f"x must be {cfg.x_dtype}, got {x.dtype}")
     if x.is_contiguous():
         have = x.numel()
+        if rows is None and have == cfg._elements[ragged]:
+            return cfg._ref
         n = 0 if have < cfg.width else (have - cfg.width) // cfg.x_stride + 1
-        if _wider(x, cfg.x_stride, None if rows is not None else cfg.rows(ragged) * cfg.x_stride):
+        if _wider(x, cfg.x_stride):
             raise ValueError(f"x has rows of {x.shape[-1]} elements, the config rows of {cfg.x_stride} (x_stride)")
     else:
         if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) != cfg.x_stride:
@@ -475,15 +479,17 @@ def _fp4_buffer(t, dtype, n, name):
     raise ValueError(f"{name} needs {n} elements, got {t.numel()}")
 
 
-def _fp4_tiles(t, nbytes, name, e, n, blocks):
-    """Address of the tiled scales of e matrices of n rows of ``blocks`` scales.  The row-major scales of a checkpoint
-    have the same size where the matrices fill their tiles, so they are told by their shape (rows of 512 are left
-    alone: that may be a view of the tiles)."""
-    p = _fp4_buffer(t, _U8, nbytes, name)
-    if t is not None and t.dim() == 3 and t.shape == (e, n, blocks) and blocks != 512:
-        raise ValueError(f"{name} has the row-major shape of a checkpoint's scales; "
-                         "tiled scales are needed (fp4_tile_scales)")
-    return p
+def _fp4_tiles(t, nbytes, name, shape):
+    """Address of tiled scales.  ``shape`` is that of the same scales row by row, [matrices, rows, K / g], as a
+    checkpoint holds them: they have the same size where the matrices fill their tiles, and are told by it (rows of
+    512 scales are left alone: that may be a view of the tiles)."""
+    if (isinstance(t, _Tensor) and t.dtype is _U8 and t.numel() >= nbytes and t.is_contiguous()
+            and (t.dim() != 3 or t.shape != shape or shape[2] == 512)):
+        return t.data_ptr()
+    if _fp4_buffer(t, _U8, nbytes, name) is None:
+        return None
+    raise ValueError(f"{name} has the row-major shape of a checkpoint's scales; "
+                     "tiled scales are needed (fp4_tile_scales)")
 
 
 def fp4_codes_bytes(cfg: Fp4Config, ragged=False) -> int:
@@ -560,7 +566,7 @@ def _fp4_out(cfg, out, rows):
     else:
         if not out.is_contiguous():
             raise ValueError("out must be contiguous, or two-dimensional with rows out_stride elements apart")
-        if _wider(out, cfg.out_stride, rows * cfg.out_stride):
+        if out.numel() != rows * cfg.out_stride and _wider(out, cfg.out_stride):
             raise ValueError(f"out has rows of {shape[-1]} elements, the config rows of {cfg.out_stride} (out_stride)")
         ok = rows == 0 or out.numel() >= (rows - 1) * cfg.out_stride + cfg.n
     if not ok:
@@ -572,16 +578,17 @@ def fp4_matmul(cfg: Fp4Config, a_codes, a_scales, a_gs, w_codes, w_scales, w_gs,
                device_status=None, stream=None):
     """Enqueue the product of two quantised operands (``b4_fp4_matmul``)."""
     n, code_bytes, scale_bytes, gs_n = cfg._operand(offsets is not None)
-    w_bytes, ws_bytes = cfg._weight_sizes()
+    w_bytes, ws_bytes, ws_rows = cfg._weight_sizes()
     st = _lib.b4_fp4_matmul(
-        cfg._ref, _fp4_buffer(a_codes, torch.uint8, code_bytes, "a_codes"),
-        _fp4_tiles(a_scales, scale_bytes, "a_scales", cfg.num_groups, cfg.m, cfg.blocks), _fp4_buffer(a_gs, torch.float32, gs_n, "a_gs"),
-        _fp4_buffer(w_codes, torch.uint8, w_bytes, "w_codes"),
-        _fp4_tiles(w_scales, ws_bytes, "w_scales", cfg.num_groups, cfg.n, cfg.blocks),
-        _fp4_buffer(w_gs, torch.float32, cfg.num_groups, "w_gs"),
-        _fp4_buffer(offsets, torch.int32, cfg.num_groups + 1, "offsets"),
-        _fp4_buffer(out_rows, torch.int32, n, "out_rows"), _fp4_out(cfg, out, n),
-        _fp4_buffer(device_status, torch.int32, 2, "device_status"), _stream_of(stream, a_codes))
+        cfg._ref, _fp4_buffer(a_codes, _U8, code_bytes, "a_codes"),
+        _fp4_tiles(a_scales, scale_bytes, "a_scales", (cfg.num_groups, cfg.m, cfg.blocks)),
+        a_gs if a_gs is None else _fp4_buffer(a_gs, _F32, gs_n, "a_gs"),
+        _fp4_buffer(w_codes, _U8, w_bytes, "w_codes"), _fp4_tiles(w_scales, ws_bytes, "w_scales", ws_rows),
+        w_gs if w_gs is None else _fp4_buffer(w_gs, _F32, cfg.num_groups, "w_gs"),
+        offsets if offsets is None else _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets"),
+        out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, n, "out_rows"), _fp4_out(cfg, out, n),
+        device_status if device_status is None else _fp4_buffer(device_status, _I32, 2, "device_status"),
+        _stream_of(stream, a_codes))
     if st:
         _check(st)
 
@@ -601,15 +608,14 @@ def fp4_linear(cfg: Fp4Config, x, w_codes, w_scales, w_gs, out, workspace, x_gs=
     operand is x row rows[i] // row_div) and ``out_rows`` scatters the result.
     """
     m = cfg.m
-    w_bytes, ws_bytes = cfg._weight_sizes()
+    w_bytes, ws_bytes, ws_rows = cfg._weight_sizes()
     ragged = offsets is not None
     st = _lib.b4_fp4_linear(
         _fp4_x(cfg, x, rows, ragged), x.data_ptr(),
         x_gs if x_gs is None else _fp4_buffer(x_gs, _F32, cfg.num_groups, "x_gs"),
         rows if rows is None else _fp4_buffer(rows, _I32, m, "rows"),
         _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None,
-        _fp4_buffer(w_codes, _U8, w_bytes, "w_codes"),
-        _fp4_tiles(w_scales, ws_bytes, "w_scales", cfg.num_groups, cfg.n, cfg.blocks),
+        _fp4_buffer(w_codes, _U8, w_bytes, "w_codes"), _fp4_tiles(w_scales, ws_bytes, "w_scales", ws_rows),
         w_gs if w_gs is None else _fp4_buffer(w_gs, _F32, cfg.num_groups, "w_gs"),
         out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, m, "out_rows"), _fp4_out(cfg, out, m),
         _fp4_buffer(workspace, _U8, 0, "workspace"), workspace.numel(), _stream_of(stream, x))
@@ -625,22 +631,16 @@ def fused_moe_a4_workspace_bytes(cfg: MoEConfig, activation: int) -> int:
     return int(n)
 
 
-def _layer_buffer(t, dtype, n, name):
-    """As _fp4_buffer, for an argument that has to be there."""
-    if t is None:
-        _need(t, dtype, name)
-    return _fp4_buffer(t, dtype, n, name)
+def _stack_sizes(e, n, k, format):
+    """(code bytes, scale bytes, shape of row-major scales) of a stack of e quantised [n, k] matrices."""
+    g = 16 if format == NVFP4 else 32
+    return e * n * ((k // 2 + 15) // 16 * 16), 512 * e * -(-n // 128) * -(-k // (4 * g)), (e, n, k // g)
 
 
-def _layer_tiles(t, nbytes, name, e, n, blocks):
-    if t is None:
-        _need(t, _U8, name)
-    return _fp4_tiles(t, nbytes, name, e, n, blocks)
-
-
-def _stack_bytes(e, n, k, format):
-    """(code bytes, scale bytes) of a stack of e quantised [n, k] matrices."""
-    return e * n * ((k // 2 + 15) // 16 * 16), 512 * e * -(-n // 128) * -(-k // (64 if format == NVFP4 else 128))
+@functools.lru_cache(maxsize=64)
+def _layer_sizes(e, h, i, format, activation):
+    """The sizes of W13 and of W2."""
+    return _stack_sizes(e, i if activation == RELU2 else 2 * i, h, format) + _stack_sizes(e, h, i, format)
 
 
 def fused_moe_a4(cfg: MoEConfig, x, w13, s13, gs13, w2, s2, gs2, topk_ids, topk_weights, activation, out, workspace,
@@ -650,22 +650,28 @@ def fused_moe_a4(cfg: MoEConfig, x, w13, s13, gs13, w2, s2, gs2, topk_ids, topk_
     apart, so a checkpoint's codes are used as they are where hidden and inter are multiples of 32); ``out`` [m, H]
     bf16 is written in full."""
     e, m, h, i = cfg.num_local_experts, cfg.m, cfg.hidden, cfg.inter
-    n1, g = i if activation == RELU2 else 2 * i, 16 if cfg.format == NVFP4 else 32
-    w13_bytes, s13_bytes = _stack_bytes(e, n1, h, cfg.format)
-    w2_bytes, s2_bytes = _stack_bytes(e, h, i, cfg.format)
-    _need(workspace, torch.uint8, "workspace")
+    w13_bytes, s13_bytes, s13_rows, w2_bytes, s2_bytes, s2_rows = _layer_sizes(e, h, i, cfg.format, activation)
+    rows, routes = m * h, m * cfg.top_k
+    xp, op = _fp4_buffer(x, torch.bfloat16, rows, "x"), _fp4_buffer(out, torch.bfloat16, rows, "out")
+    w13p, s13p = _fp4_buffer(w13, _U8, w13_bytes, "w13"), _fp4_tiles(s13, s13_bytes, "s13", s13_rows)
+    w2p, s2p = _fp4_buffer(w2, _U8, w2_bytes, "w2"), _fp4_tiles(s2, s2_bytes, "s2", s2_rows)
+    idp = _fp4_buffer(topk_ids, _I32, routes, "topk_ids")
+    wtp = _fp4_buffer(topk_weights, _F32, routes, "topk_weights")
+    _need(workspace, _U8, "workspace")
+    if None in (xp, op, w13p, s13p, w2p, s2p, idp, wtp):
+        for t, name in ((x, "x"), (out, "out"), (topk_ids, "topk_ids"), (topk_weights, "topk_weights"), (w13, "w13"),
+                        (s13, "s13"), (w2, "w2"), (s2, "s2")):
+            if t is None:
+                raise TypeError(f"{name} must be a torch tensor")
     for t, name in ((x, "x"), (out, "out")):
-        if t is not None and _wider(t, h, m * h):
+        if t.numel() != rows and _wider(t, h):
             raise ValueError(f"{name} has rows of {t.shape[-1]} elements, the config rows of {h}")
     c = cfg._c()
-    _check(_lib.b4_fused_moe_a4(
-        ctypes.byref(c), _layer_buffer(x, torch.bfloat16, m * h, "x"), _layer_buffer(w13, _U8, w13_bytes, "w13"),
-        _layer_tiles(s13, s13_bytes, "s13", e, n1, h // g), _fp4_buffer(gs13, _F32, e, "gs13"),
-        _layer_buffer(w2, _U8, w2_bytes, "w2"), _layer_tiles(s2, s2_bytes, "s2", e, h, i // g),
-        _fp4_buffer(gs2, _F32, e, "gs2"),
-        _layer_buffer(topk_ids, _I32, m * cfg.top_k, "topk_ids"),
-        _layer_buffer(topk_weights, _F32, m * cfg.top_k, "topk_weights"), int(activation),
-        _layer_buffer(out, torch.bfloat16, m * h, "out"), _ptr(workspace), workspace.numel(), _stream(stream)))
+    st = _lib.b4_fused_moe_a4(ctypes.byref(c), xp, w13p, s13p, _fp4_buffer(gs13, _F32, e, "gs13"), w2p, s2p,
+                              _fp4_buffer(gs2, _F32, e, "gs2"), idp, wtp, int(activation), op, workspace.data_ptr(),
+                              workspace.numel(), _stream(stream))
+    if st:
+        _check(st)
 
 
 def fused_moe_raw(cfg: MoEConfig, ptrs: dict, activation: int, workspace_ptr: int, workspace_bytes_: int,
