@@ -152,3 +152,22 @@ def test_layer_at_full_size_and_in_a_graph(b4, name, wl, ms):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("m", [2, 40])
+@pytest.mark.parametrize("act", ["silu", "relu2"])
+def test_layer_whose_rows_of_codes_are_padded(b4, act, m):
+    """hidden and inter odd multiples of 16: the codes' rows end 8 bytes before the next begin."""
+    wl = W.Workload("odd", NV, 5, 5, 2, 336, 176, act, (m,))
+    (c13, s13, g13), w13 = T._weights(NV, 5, wl.n1, 336, 96)
+    (c2, s2, g2), w2 = T._weights(NV, 5, 336, 176, 97)
+    x_bits, x = W.activations(wl, m, 98)
+    ids, wts = W.routing(wl, m, 98)
+    cfg = b4.MoEConfig(m, 2, 5, 5, 336, 176)
+    ws = torch.empty(b4.fused_moe_a4_workspace_bytes(cfg, b4.ACTIVATIONS[act]), dtype=torch.uint8, device="cuda")
+    out = torch.full((m, 336), float("nan"), dtype=BF, device="cuda")
+    b4.fused_moe_a4(cfg, dev(x_bits).view(BF), *w13, *w2, dev(ids), dev(wts), b4.ACTIVATIONS[act], out, ws)
+    torch.cuda.synchronize()
+    b4.check_status(ws)
+    want = O.fused_moe_a4(x, c13, s13, g13, c2, s2, g2, ids, wts, act, NV, 5)
+    assert_parity(bf16_to_np(out), want, f"padded codes m={m}")
