@@ -421,6 +421,7 @@ size_t b4_fp4_scale_bytes(const b4_fp4_config* cfg, int32_t ragged);
  * gs * scale * e2m1(code) in x's type, [rows][k].  A NaN in a block makes its scale
  * NaN; under ROW and TENSOR an infinity or NaN makes gs non-finite and the values it
  * scales NaN; under GIVEN and MXFP4 an infinity saturates (MXFP4: scale 2^127).
+ * A zero block's scale is 0, under a gs of 0 too (values and products are then 0).
  * Tiled scales of a stack are written in full, the missing rows of its last row
  * tiles as zeros; those of a ragged operand only where rows are live, and its rows
  * past offsets[num_groups] are not written at all.

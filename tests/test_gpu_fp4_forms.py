@@ -171,3 +171,58 @@ def test_layer_whose_rows_of_codes_are_padded(b4, act, m):
     b4.check_status(ws)
     want = O.fused_moe_a4(x, c13, s13, g13, c2, s2, g2, ids, wts, act, NV, 5)
     assert_parity(bf16_to_np(out), want, f"padded codes m={m}")
+
+
+@pytest.mark.parametrize("mode", ["given", "tensor"])
+def test_zero_blocks_under_a_scale_of_zero(b4, mode):
+    """A global scale of 0 (calibrated on nothing but zeros; or amax / 2688 below fp32's least number) makes every value
+    0, the zero blocks' too, and the products with them."""
+    m, n, k = 3, 40, 96
+    x = torch.zeros(m, k)
+    x[1, 40] = 1.0 if mode == "given" else 1e-42
+    cfg = b4.Fp4Config(m=m, n=n, k=k, x_dtype=F32, out_dtype=F32, gs_mode=getattr(b4, "GS_" + mode.upper()))
+    codes, scales, gs = b4.fp4_empty(cfg, "cuda")
+    gs.zero_()
+    values = torch.full((m, k), float("nan"), device="cuda")
+    b4.fp4_quantize(cfg, x.cuda(), codes, scales, gs, values=values)
+    assert float(gs[0]) == 0 and not values.any() and not codes[..., : k // 2].any()
+    sc = T._untile(scales, m, k // 16)[0]
+    assert np.isfinite(e4m3_decode(sc)).all() and not np.delete(sc.reshape(-1), 1 * (k // 16) + 40 // 16).any()
+    _, wd = T._weights(NV, 1, n, k, 99)
+    out = torch.full((m, n), float("nan"), device="cuda")
+    b4.fp4_matmul(cfg, codes, scales, gs, *wd, out)
+    assert not out.any()
+    if mode == "given":
+        ws = torch.empty(b4.fp4_linear_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+        out.fill_(float("nan"))
+        b4.fp4_linear(cfg, x.cuda(), *wd, out, ws, x_gs=gs)
+        assert not out.any()
+
+
+@pytest.mark.parametrize("m", [2, 40, 300])
+def test_calls_behind_copies_and_fills_in_a_graph(b4, m):
+    """A captured call whose stream did a copy and a fill before it (nodes that are no kernels)."""
+    n, k = 300, 272
+    cfg = b4.Fp4Config(m=m, n=n, k=k)
+    src = T._randn((2, m, k), 100, BF).cuda()
+    x, out = torch.empty(m, k, dtype=BF, device="cuda"), torch.empty(m, n, dtype=BF, device="cuda")
+    parts, prod = b4.fp4_empty(cfg, "cuda"), torch.empty_like(out)
+    _, wd = T._weights(NV, 1, n, k, 101)
+    ws = torch.empty(b4.fp4_linear_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    picked = src[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.copy_(picked)
+        out.zero_()
+        b4.fp4_linear(cfg, x, *wd, out, ws)
+        x.copy_(picked)
+        prod.zero_()
+        b4.fp4_quantize(cfg, x, *parts)
+        b4.fp4_matmul(cfg, *parts, *wd, prod)
+    want = torch.empty_like(out)
+    for i in (0, 1):
+        picked.copy_(src[i])
+        b4.fp4_linear(cfg, src[i], *wd, want, ws)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(prod, want)

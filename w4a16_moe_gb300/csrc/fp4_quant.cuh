@@ -317,7 +317,8 @@ __device__ __forceinline__ Quantized quantize_block(const C& h, uint32_t a, cons
     q.w = encode<FMT>(h, recip(q.d));
     if (q.code == 0) q.w = make_uint2(0, 0);
   } else {
-    ratio = true_quotient(amax, r.six);
+    // (under a global scale of zero, or one so small that 6 gs is, a zero block is zero, not 0 / 0)
+    ratio = r.six == 0.f && a == 0 ? 0.f : true_quotient(amax, r.six);
     q.code = ratio != ratio ? 0x7fu : (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
     q.d = q.code == 0x7fu ? __uint_as_float(0x7fffffffu) : __fmul_rn(e4m3_value(q.code), r.gs);
     q.w = q.d > 0.f && a <= kInfBits ? encode_by_division(h, q.d) : make_uint2(0, 0);
