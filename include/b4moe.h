@@ -416,7 +416,12 @@ size_t b4_fp4_scale_bytes(const b4_fp4_config* cfg, int32_t ragged);
 /* Quantises rows of x (after the activation, in fp32):
  *   NVFP4  s = e4m3(amax_block / (6 gs)), d = s gs, c = e2m1(h / d), c = 0 where d = 0
  *   MXFP4  s = 2^j, j >= -127 the least with amax_block <= 6 * 2^j, c = e2m1(h / s)
- * every step IEEE fp32, conversions to nearest even, saturating.  rows (or NULL)
+ * in fp32, conversions to nearest even, saturating.  The quotients by d and 6 gs are
+ * products with a reciprocal known to 46 bits, rounded once: scales and codes are the
+ * formula's bit for bit for 16-bit x under power-of-two scales (ROW, MXFP4), and else
+ * but for quotients within 2^-21 of a tie between two of them.  The sigmoid of the
+ * gated activations takes the machine's approximate exponential and reciprocal:
+ * relative error about 2^-21 + |alpha g| 2^-23.  rows (or NULL)
  * gathers: a negative entry gives a zero row.  values (or NULL) receives
  * gs * scale * e2m1(code) in x's type, [rows][k].  A NaN in a block makes its scale
  * NaN; under ROW and TENSOR an infinity or NaN makes gs non-finite and the values it
@@ -435,7 +440,8 @@ b4_status b4_fp4_quantize(const b4_fp4_config* cfg, const void* x, const int32_t
 b4_status b4_fp4_tile_scales(const b4_fp4_config* cfg, const uint8_t* src, uint8_t* dst, b4_stream_t stream);
 
 /* out[t][n] = gs_a gs_w[e] sum_k (scale e2m1)_a[t][k] (scale e2m1)_w[e][n][k] for the
- * rows t of group e, accumulated in fp32 by the tensor cores and rounded once.
+ * rows t of group e, accumulated in fp32 by the tensor cores and rounded once.  gs_a gs_w
+ * is formed first, in fp32: below 2^-126 it loses bits.
  *
  * a_codes, a_scales  quantised activations, tiled scales (a scale_layout of ROWS is
  *               refused); a_gs by gs_mode: per row (ROW), per group (GIVEN, TENSOR),
@@ -447,7 +453,8 @@ b4_status b4_fp4_tile_scales(const b4_fp4_config* cfg, const uint8_t* src, uint8
  *               past offsets[num_groups] as zeros.
  * out_rows      NULL, or the output row of each operand row ([rows] int32, rows = m of
  *               a ragged operand and num_groups * m of a stack; entries outside
- *               [0, rows) are dropped): packed routes go back to route order.
+ *               [0, rows) are dropped, the others distinct): packed routes go back to
+ *               route order.
  * device_status NULL, or 2 uint32 that the caller has zeroed: B4_ERR_TIMEOUT and the
  *               wait site if a bounded wait ran out, untouched otherwise.
  * 1 launch.  Does not read x_dtype, x_rows, x_stride, row_div, activation. */

@@ -21,9 +21,9 @@
 // unit's products.  Roles of the warps as in fp4_gemm.cuh (2 and 3 also look up the
 // rows' scales and places ahead of the epilogue).
 //
-// Measured: N = K = 4096, 4096 rows 28.1 us (4.9 PFLOP/s; the tensor pipe busy 48 % of
-// it), 8192 x 8192 x 4096 81.9 us (6.7 PFLOP/s); 64 groups of 256 rows, N = 2816, K = 2048
-// 55.0 us (318 MB moved, 5.8 TB/s).
+// Measured (three sets of operands in turn): N = K = 4096, 4096 rows 28.7 us (4.8 PFLOP/s; the
+// tensor pipe busy 48 % of it), 8192 x 8192 x 4096 87.4 us (6.3 PFLOP/s); 64 groups of 256 rows,
+// N = 2816, K = 2048 55.0 us (318 MB moved, 5.8 TB/s).
 
 #include "fp4_mma.cuh"
 
@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     if (rank == 0) {
       // Where a pair takes many units the loop over a stage's slot is unrolled over the
       // ring, so that slots and scale columns are constants: with them in registers a
-      // stage takes longer to issue than its products take to run (8192 x 8192 x 4096 82.0
-      // us, rolled 84.0).  In one round or two the smaller code, fetched cold, gains more
+      // stage takes longer to issue than its products take to run (8192 x 8192 x 4096 87.5
+      // us, rolled 88.2; 4096^3 28.7 and 29.0).  In one round or two the smaller code, fetched cold, gains more
       // (N = K = 4096, 1024 rows 11.3 us, unrolled 11.7; N = 2048, K = 1408, 1024 rows 6.5, 6.8).
       const uint32_t w_desc = desc_lo(smem_u32(smem)), a_desc = desc_lo(smem_u32(s_a)), s_desc = desc_lo(smem_u32(s_sf));
       uint32_t phase = 0, acc_i = 0, d = 0, abuf = 0;

@@ -179,8 +179,10 @@ struct Chunk<T, true> : Raw<float> {
     g.load(row + 16 * c, p.vec);
     if (p.act == 0) {
       // g sigmoid(alpha g) (u + beta) of the clamped g and u, two columns an instruction; the
-      // exponential and the reciprocal are the machine's approximations (2^-22 each), and
-      // the sigmoid is 0 where 1 + e^(-alpha g) passes 2^126
+      // exponential and the reciprocal are the machine's approximations (2^-22 each), on an
+      // argument rounded to fp32 (another |alpha g| 2^-23 of the exponential: 2^-20 at g = -10,
+      // alpha = 1), and the sigmoid is 0 where 1 + e^(-alpha g) passes 2^126.  The codes keep
+      // two bits, so an error of 2^-19 moves one only next to a tie.
       u.load(row + p.k + 16 * c, p.vec);
       const float limit = p.glu.limit, scale = -1.44269504f * p.glu.alpha;
       const uint64_t scale2 = pack2(scale, scale), beta2 = pack2(p.glu.beta, p.glu.beta), one2 = pack2(1.f, 1.f);

@@ -15,18 +15,20 @@
 // side, so a chunk is one 32-byte load of a contiguous stretch (two of fp32) and
 // its codes one 8-byte store; a thread loads all of its chunks (cached_chunks)
 // before it uses any, and keeps them between the row's maximum and its codes
-// (longer rows are read again, from L1).  Every step is IEEE fp32 in the order of
-// the formula, but for h / d, which is h y + h z in one fused multiply-add, y an
-// approximate reciprocal of d and z what it lacks (z = (1 - y d) y, the residual exact):
-// the quotient to 46 bits before its one rounding, so every tie of the codes is
-// met, in two operations an element, two elements an instruction, where a
-// division costs a dozen.
+// (longer rows are read again, from L1).  Every step is fp32 in the order of
+// the formula, rounded to nearest, but for the quotients amax / (6 gs) and h / d: h / d is
+// h y + h z in one fused multiply-add, y an approximate reciprocal of d and z what it
+// lacks (z = (1 - y d) y, the residual exact): the quotient to 46 bits before its one
+// rounding, so every tie of the codes is met where d is exact, in two operations an
+// element, two elements an instruction, where a division costs a dozen.
 //
 // Bound by DRAM where rows are many, but for the gated prologue: 16384 rows of 4096
 // bf16, per matrix (given) 29.1 us, 5.9 TB/s, by row 31.7 us, as MXFP4 26.9 us, 6.3 TB/s;
 // by the ramp of one wave below (4096 rows 10.8 us, 512 rows 2.9 us, one row 2.2 us).
-// SwiGLU reads two elements and spends two transcendental operations for each: 12288
-// rows of 1408 23.7 us, 3.3 TB/s.
+// Behind SwiGLU by the issue of instructions: 12288 rows of 1408 23.8 us, 3.3 TB/s, at 37
+// instructions an element, 0.71 a cycle and scheduler (DRAM 34 % busy, the pipe of the two
+// transcendental operations 19 to 26 %), 6.7 warps a scheduler of which 1.75 are ready: a
+// block has one row, and nothing of the next is in flight while it waits for its loads.
 
 #include <algorithm>
 
