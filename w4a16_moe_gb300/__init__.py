@@ -528,7 +528,10 @@ def fp4_empty(cfg: Fp4Config, device, ragged=False):
 
 
 def fp4_quantize(cfg: Fp4Config, x, codes, scales, gs=None, values=None, rows=None, offsets=None, stream=None):
-    """Enqueue the quantisation of x rows into ``codes``, ``scales`` and ``gs`` (an input with GS_GIVEN)."""
+    """Enqueue the quantisation of x rows into ``codes``, ``scales`` and ``gs`` (an input with GS_GIVEN).
+
+    x: rows of the config's width, x_stride elements apart, or a contiguous tensor of any shape that holds exactly the
+    config's elements.  ``rows`` gathers from x's rows (entries that name none give zero rows)."""
     ragged = offsets is not None
     n, code_bytes, scale_bytes, gs_n = cfg._operand(ragged)
     st = _lib.b4_fp4_quantize(
