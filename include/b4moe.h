@@ -490,6 +490,127 @@ b4_status b4_fused_moe_a4(const b4_moe_config* cfg, const uint16_t* x, const uin
                           const int32_t* topk_ids, const float* topk_weights, int32_t activation, uint16_t* out,
                           void* workspace, size_t workspace_bytes, b4_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Routing to experts: from a router's logits to the ids and weights that the layers and
+ * b4_route_pack read.  The pages take both as inputs.
+ *
+ * For the logits z of a token, s = softmax(z) or sigmoid(z) over its experts and
+ * c = s + bias; without a bias the order is that of z.  With num_groups > 1 the experts
+ * are cut into equal neighbouring groups; a group counts with its largest c, or with the
+ * sum of its two largest (group_top = 2; of what it has), and the experts of the
+ * top_groups best groups stay.  The ids are the top_k experts of largest c in
+ * descending order; the weights are s, over their sum where renormalised, times scale.
+ * Ties, of groups too, go to the lowest index.  The order is that of the real numbers:
+ * where fp32 does not separate two of them the row is done again in 64 bits.
+ * (Renormalised softmax weights are the softmax over the chosen logits.)
+ *
+ * An expert whose logit or bias is NaN or -inf is never chosen and adds nothing; where
+ * fewer than top_k can be, the rest of the row is id -1 with weight 0, which the layers
+ * drop.  A logit of +inf counts as the limit: softmax shares 1 among those.  A bias of
+ * +inf puts its expert first. */
+typedef enum b4_score { B4_SCORE_SOFTMAX = 0, B4_SCORE_SIGMOID = 1 } b4_score;
+
+typedef struct b4_route_config {
+  int32_t m;             /* tokens, 0 .. 2^25 */
+  int32_t num_experts;   /* 1 .. 1024 */
+  int32_t top_k;         /* 1 .. min(32, num_experts) */
+  int32_t num_groups;    /* 1 .. 32, divides num_experts; 1: no groups */
+  int32_t top_groups;    /* 1 .. num_groups; their experts number at least top_k */
+  int32_t group_top;     /* 1: a group counts with its largest c; 2: the sum of its two largest */
+  int32_t score;         /* b4_score */
+  int32_t renormalize;   /* nonzero: weights over their sum */
+  int32_t logits_dtype;  /* b4_dtype */
+  float scale;           /* finite; multiplies the weights */
+  int64_t logits_stride; /* elements between rows of logits; 0: num_experts */
+} b4_route_config;
+
+/* logits [m][num_experts] by logits_stride; bias NULL or [num_experts] fp32; num_tokens
+ * NULL or one int32: rows from *num_tokens on (a padded batch) get ids of -1 and weights
+ * of 0, their logits are not read.  Writes topk_ids and topk_weights, [m][top_k], in
+ * full.  1 launch, no workspace; neither allocates nor synchronises (capture-safe);
+ * the same bits every time. */
+b4_status b4_route_topk(const b4_route_config* cfg, const void* logits, const float* bias, const int32_t* num_tokens,
+                        int32_t* topk_ids, float* topk_weights, b4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * FP8 (W8A8): E4M3 operands with an fp32 scale per block of 128 along K -- their
+ * quantisation, their product, the product grouped by expert with ragged sizes, and the
+ * MoE layer of them.  The pages have no counterpart.
+ *
+ * A quantised operand of R rows and K columns:
+ *   codes   [R][K] uint8, E4M3 bit patterns (K a multiple of 16).
+ *   scales  fp32: [R][ceil(K / 128)] for activation rows (block_rows = 1);
+ *           [matrix][ceil(R / 128)][ceil(K / 128)] for weight matrices (128): the value of an
+ *           element is e4m3(code) times the scale of its block.  Any fp32 scales will do.
+ * Stacks and ragged operands (offsets) are as for FP4 above, rows following one another
+ * without gaps.  Every call validates on the host before it launches, enqueues on
+ * `stream`, and neither allocates nor synchronises (capture-safe).  Results are bitwise
+ * reproducible. */
+typedef enum b4_fp8_scale { B4_FP8_SCALE_F32 = 0, B4_FP8_SCALE_POW2 = 1 } b4_fp8_scale;
+
+typedef struct b4_fp8_config {
+  int32_t m;           /* rows per matrix of a stack, or row capacity of a ragged operand; 0 .. 2^25 */
+  int32_t n;           /* rows of each weight matrix (outputs); any value >= 1; unused by b4_fp8_quantize */
+  int32_t k;           /* quantised columns: multiple of 16, <= 65536 */
+  int32_t num_groups;  /* 1 .. B4_MAX_LOCAL_EXPERTS */
+  int32_t x_dtype;     /* b4_dtype of x and values */
+  int32_t out_dtype;   /* b4_dtype of the product */
+  int32_t activation;  /* -1: none; else b4_activation applied to x first (see b4_fp4_config) */
+  int32_t scale_mode;  /* b4_fp8_scale of the quantiser's scales */
+  int32_t block_rows;  /* rows that share a scale: 1, or 128 (b4_fp8_quantize of weights) */
+  int32_t row_div;     /* with `rows`: row i of the operand is x row rows[i] / row_div (top_k for packed routes) */
+  int32_t x_rows;      /* with `rows`: x rows outside [0, x_rows) read as zeros (0: not checked above) */
+  float swiglu_alpha, swiglu_beta, swiglu_limit; /* B4_ACT_SWIGLU_OAI only */
+  int64_t x_stride;    /* elements between rows of x; 0: the row's own width */
+  int64_t out_stride;  /* elements between rows of out; 0: n */
+} b4_fp8_config;
+
+/* Quantises rows of x (after the activation, in fp32), for each block's largest magnitude a:
+ *   F32   s = a / 448 in fp32        POW2  s = 2^j, j the least with a <= 448 * 2^j
+ *   (at least 2^-126; 1 where a is 0)   c = e4m3(h / s), to nearest even
+ * The quotient is a product with a reciprocal known to 46 bits, rounded once to fp32; the
+ * gated activations as in b4_fp4_quantize.  A block with a NaN or an infinity has the scale
+ * NaN and codes NaN.  rows (or NULL) gathers: a negative entry gives a zero row (scales 1).
+ * values (or NULL) receives scale * e4m3(code) in x's type, [rows][k].  Rows of a ragged
+ * operand past offsets[num_groups] are not written.  block_rows = 128 takes neither rows nor
+ * offsets.  1 launch; m = 0 launches nothing. */
+b4_status b4_fp8_quantize(const b4_fp8_config* cfg, const void* x, const int32_t* rows, const int32_t* offsets,
+                          uint8_t* codes, float* scales, void* values, b4_stream_t stream);
+
+/* out[t][n] = sum over blocks b of s_a[t][b] s_w[e][n / 128][b] sum_{k in b} a[t][k] w[e][n][k] for
+ * the rows t of group e: the tensor cores multiply and add the codes of a block in fp32, the
+ * scaled blocks are added in fp32 in order of k, and the result is rounded once.
+ *
+ * a_codes, a_scales  quantised activations, [rows][k] and [rows][ceil(k / 128)].
+ * w_codes       [num_groups][n][k], w_scales [num_groups][ceil(n / 128)][ceil(k / 128)].
+ * offsets, out, out_rows, device_status  as for b4_fp4_matmul.
+ * 1 launch.  Does not read x_dtype, x_rows, x_stride, row_div, activation, scale_mode. */
+b4_status b4_fp8_matmul(const b4_fp8_config* cfg, const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
+                        const float* w_scales, const int32_t* offsets, const int32_t* out_rows, void* out,
+                        uint32_t* device_status, b4_stream_t stream);
+
+/* b4_fp8_quantize of x into the workspace, then b4_fp8_matmul: 2 launches, the second set up
+ * under the first.  num_groups is 1 unless offsets is given.
+ * workspace: >= b4_fp8_linear_workspace_bytes(cfg), 256-byte aligned; holds the status word
+ * that b4_check_status reads. */
+size_t b4_fp8_linear_workspace_bytes(const b4_fp8_config* cfg);
+b4_status b4_fp8_linear(const b4_fp8_config* cfg, const void* x, const int32_t* rows, const int32_t* offsets,
+                        const uint8_t* w_codes, const float* w_scales, const int32_t* out_rows, void* out,
+                        void* workspace, size_t workspace_bytes, b4_stream_t stream);
+
+/* The fused MoE layer with 8-bit weights and activations: route packing, x rows gathered and
+ * quantised, grouped FC1 (fp32 out), activation and quantisation, grouped FC2 stored in route
+ * order (bf16), and the weighted sum of each token's valid routes in fp32 with one rounding.
+ * cfg, routing and activations as b4_fused_moe (cfg->format and cfg->path are not read; hidden
+ * and inter multiples of 16); weights as quantised operands: w13 [E_l][2 I or I][H] with gate
+ * rows first and s13 [E_l][ceil(rows / 128)][ceil(H / 128)], w2 [E_l][H][I] and s2 likewise.
+ * 6 launches. */
+size_t b4_fused_moe_fp8_workspace_bytes(const b4_moe_config* cfg, int32_t activation);
+b4_status b4_fused_moe_fp8(const b4_moe_config* cfg, const uint16_t* x, const uint8_t* w13, const float* s13,
+                           const uint8_t* w2, const float* s2, const int32_t* topk_ids, const float* topk_weights,
+                           int32_t activation, uint16_t* out, void* workspace, size_t workspace_bytes,
+                           b4_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* b4_status_string(int32_t status);
 

@@ -32,6 +32,9 @@ moe       the fused MoE layer itself.
 linear    the dense W4A16 linear layer (one weight matrix, no routing).
 fp4       quantised (FP4) activations, the FP4 x FP4 products and the MoE layer
           built of them (no counterpart on the pages).
+router    the choice of experts from router logits (no counterpart).
+fp8       block-scaled FP8 operands, their products and the MoE layer of them
+          (no counterpart).
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test in
 ``tests/test_oracle_*.py`` against something other than itself (torch casts,
@@ -39,4 +42,4 @@ bit-field definitions, brute force, closed forms, a dense-MLP special case,
 exact integer arithmetic and invariances).  No function is "parity unpinned".
 """
 
-from . import formats, quant, routing, moe, linear, fp4  # noqa: F401
+from . import formats, quant, routing, moe, linear, fp4, router, fp8  # noqa: F401

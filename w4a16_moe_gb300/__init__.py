@@ -49,6 +49,13 @@ GS_ROW = 2
 GS_TENSOR = 3
 SCALES_TILED = 0
 SCALES_ROWS = 1
+# routing scores; FP8 operators: scale modes and element type
+SOFTMAX = 0
+SIGMOID = 1
+SCORES = {"softmax": SOFTMAX, "sigmoid": SIGMOID}
+FP8_SCALE_F32 = 0
+FP8_SCALE_POW2 = 1
+E4M3 = torch.float8_e4m3fn
 # the gpt-oss models' clamped-swiglu parameters (alpha, beta, limit)
 SWIGLU_OAI_DEFAULTS = (1.702, 1.0, 7.0)
 
@@ -98,6 +105,43 @@ class _Fp4Config(ctypes.Structure):
     ]
 
 
+class _Fp8Config(ctypes.Structure):
+    _fields_ = [
+        ("m", ctypes.c_int32),
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("scale_mode", ctypes.c_int32),
+        ("block_rows", ctypes.c_int32),
+        ("row_div", ctypes.c_int32),
+        ("x_rows", ctypes.c_int32),
+        ("swiglu_alpha", ctypes.c_float),
+        ("swiglu_beta", ctypes.c_float),
+        ("swiglu_limit", ctypes.c_float),
+        ("x_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+    ]
+
+
+class _RouteConfig(ctypes.Structure):
+    _fields_ = [
+        ("m", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("logits_stride", ctypes.c_int64),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -110,6 +154,8 @@ def _load():
     I32 = ctypes.c_int32
     CP = ctypes.POINTER(_Config)
     FP = ctypes.POINTER(_Fp4Config)
+    EP = ctypes.POINTER(_Fp8Config)
+    RP = ctypes.POINTER(_RouteConfig)
     sigs = {
         "b4_route_capacity_tokens": (I32, [I32]),
         "b4_workspace_bytes": (S, [CP, I32]),
@@ -133,6 +179,13 @@ def _load():
         "b4_fp4_linear": (I32, [FP, P, P, P, P, P, P, P, P, P, P, S, P]),
         "b4_fused_moe_a4_workspace_bytes": (S, [CP, I32]),
         "b4_fused_moe_a4": (I32, [CP, P, P, P, P, P, P, P, P, P, I32, P, P, S, P]),
+        "b4_route_topk": (I32, [RP, P, P, P, P, P, P]),
+        "b4_fp8_quantize": (I32, [EP, P, P, P, P, P, P, P]),
+        "b4_fp8_matmul": (I32, [EP, P, P, P, P, P, P, P, P, P]),
+        "b4_fp8_linear_workspace_bytes": (S, [EP]),
+        "b4_fp8_linear": (I32, [EP, P, P, P, P, P, P, P, P, S, P]),
+        "b4_fused_moe_fp8_workspace_bytes": (S, [CP, I32]),
+        "b4_fused_moe_fp8": (I32, [CP, P, P, P, P, P, P, P, I32, P, P, S, P]),
         "b4_status_string": (ctypes.c_char_p, [I32]),
         "b4_last_error": (ctypes.c_char_p, []),
     }
@@ -167,6 +220,13 @@ EXPORTED = (
     "b4_fp4_linear",
     "b4_fused_moe_a4_workspace_bytes",
     "b4_fused_moe_a4",
+    "b4_route_topk",
+    "b4_fp8_quantize",
+    "b4_fp8_matmul",
+    "b4_fp8_linear_workspace_bytes",
+    "b4_fp8_linear",
+    "b4_fused_moe_fp8_workspace_bytes",
+    "b4_fused_moe_fp8",
     "b4_status_string",
     "b4_last_error",
 )
@@ -433,7 +493,7 @@ def _wider(t, pitch):
     return len(shape) > 1 and shape[-1] > pitch and shape[-1] != t.numel()
 
 
-def _fp4_x(cfg, x, rows, ragged):
+def _fp4_x(cfg, x, rows, ragged, struct=_Fp4Config):
     """x as the config describes it: a 2-D view of rows, or any contiguous shape with that many elements.
     Returns the call's config: with gathered rows, bounded by the rows x holds."""
     if x.dtype is not cfg.x_dtype:
@@ -459,7 +519,7 @@ def _fp4_x(cfg, x, rows, ragged):
     elif not 0 < cfg._struct.x_rows <= n:
         bounded = cfg._gather
         if bounded[0] != n:
-            c = _Fp4Config.from_buffer_copy(cfg._struct)
+            c = struct.from_buffer_copy(cfg._struct)
             c.x_rows = n
             bounded = cfg._gather = (n, ctypes.byref(c))
         return bounded[1]
@@ -673,6 +733,238 @@ def fused_moe_a4(cfg: MoEConfig, x, w13, s13, gs13, w2, s2, gs2, topk_ids, topk_
     st = _lib.b4_fused_moe_a4(ctypes.byref(c), xp, w13p, s13p, _fp4_buffer(gs13, _F32, e, "gs13"), w2p, s2p,
                               _fp4_buffer(gs2, _F32, e, "gs2"), idp, wtp, int(activation), op, workspace.data_ptr(),
                               workspace.numel(), _stream(stream))
+    if st:
+        _check(st)
+
+
+# ------------------------------------------------------- routing to experts
+
+
+class RouterConfig:
+    """Shape of one routing call (``b4_route_config`` in b4moe.h); read-only once made.
+
+    ``score``: SOFTMAX or SIGMOID.  ``num_groups`` equal groups of experts, of which ``top_groups`` stay (default:
+    all), each counted with its ``group_top`` (1 or 2) largest scores.  ``dtype`` of the logits, whose rows are
+    ``stride`` elements apart (0: num_experts).
+    """
+
+    def __init__(self, m, num_experts, top_k, score=SOFTMAX, renormalize=True, scale=1.0, num_groups=1, top_groups=None,
+                 group_top=1, dtype=torch.bfloat16, stride=0):
+        if dtype not in DTYPES:
+            raise TypeError(f"dtype must be one of {list(DTYPES)}, got {dtype}")
+        top_groups = num_groups if top_groups is None else top_groups
+        self.m, self.num_experts, self.top_k, self.dtype = int(m), int(num_experts), int(top_k), dtype
+        self.stride = int(stride) or self.num_experts
+        self.routes = self.m * self.top_k
+        self._struct = _RouteConfig(self.m, self.num_experts, self.top_k, int(num_groups), int(top_groups),
+                                    int(group_top), int(score), int(bool(renormalize)), DTYPES[dtype], float(scale),
+                                    int(stride))
+        self._ref = ctypes.byref(self._struct)
+
+
+def _on_device(t, name):
+    """The kernels run on the current device: a tensor of another is refused."""
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def route_topk(cfg: RouterConfig, logits, topk_ids, topk_weights, bias=None, num_tokens=None, stream=None):
+    """Enqueue the choice of experts (``b4_route_topk``): ``topk_ids`` [m, top_k] int32 and ``topk_weights`` [m, top_k]
+    fp32 are written in full.  ``bias`` [num_experts] fp32 is added to the scores for the choice alone; rows from
+    ``num_tokens`` (a device int32) on get ids of -1, which the layers drop."""
+    if logits.dtype is not cfg.dtype:
+        raise TypeError(f"logits must be {cfg.dtype}, got {logits.dtype}")
+    _on_device(logits, "logits")
+    shape = logits.shape
+    if len(shape) != 2 or shape[0] < cfg.m or shape[1] < cfg.num_experts:
+        raise ValueError(f"logits must be [{cfg.m}, {cfg.num_experts}], got {list(shape)}")
+    if cfg.m and (logits.stride(1) != 1 or (shape[0] > 1 and logits.stride(0) != cfg.stride)):
+        raise ValueError(f"logits rows must be contiguous and {cfg.stride} elements apart (stride)")
+    st = _lib.b4_route_topk(
+        cfg._ref, logits.data_ptr(), bias if bias is None else _fp4_buffer(bias, _F32, cfg.num_experts, "bias"),
+        num_tokens if num_tokens is None else _fp4_buffer(num_tokens, _I32, 1, "num_tokens"),
+        _route_out(topk_ids, _I32, cfg, "topk_ids"), _route_out(topk_weights, _F32, cfg, "topk_weights"),
+        _stream_of(stream, logits))
+    if st:
+        _check(st)
+
+
+def _route_out(t, dtype, cfg, name):
+    p = _fp4_buffer(t, dtype, cfg.routes, name)
+    if p is not None and t.numel() != cfg.routes and _wider(t, cfg.top_k):
+        raise ValueError(f"{name} has rows of {t.shape[-1]} elements, the config rows of {cfg.top_k}")
+    return p
+
+
+# ------------------------------------------------------- FP8 operators
+
+
+class Fp8Config:
+    """Shape of one call of the FP8 operators (``b4_fp8_config`` in b4moe.h); read-only once made.
+
+    ``m`` rows (per matrix of a stack, or the row capacity with ``offsets``), ``n`` outputs, ``k`` quantised
+    columns.  ``activation``: None, or SILU / RELU2 / SWIGLU_OAI applied to x first.  ``scale_mode``: FP8_SCALE_F32 or
+    FP8_SCALE_POW2.  ``block_rows``: 1 (activations, a scale per row and 128 columns) or 128 (weights).
+    """
+
+    def __init__(self, m, k, n=1, num_groups=1, x_dtype=torch.bfloat16, out_dtype=torch.bfloat16, activation=None,
+                 scale_mode=FP8_SCALE_F32, block_rows=1, row_div=1, x_rows=0, swiglu=SWIGLU_OAI_DEFAULTS, x_stride=0,
+                 out_stride=0):
+        for t, name in ((x_dtype, "x_dtype"), (out_dtype, "out_dtype")):
+            if t not in DTYPES:
+                raise TypeError(f"{name} must be one of {list(DTYPES)}, got {t}")
+        self.m, self.k, self.n, self.num_groups = int(m), int(k), int(n), int(num_groups)
+        self.x_dtype, self.out_dtype, self.block_rows = x_dtype, out_dtype, int(block_rows)
+        self.width = 2 * self.k if activation in (SILU, SWIGLU_OAI) else self.k
+        self.x_stride = int(x_stride) or self.width
+        self.out_stride = int(out_stride) or self.n
+        self.blocks = -(-self.k // 128)
+        self._struct = _Fp8Config(self.m, self.n, self.k, self.num_groups, DTYPES[x_dtype], DTYPES[out_dtype],
+                                  -1 if activation is None else activation, int(scale_mode), self.block_rows,
+                                  int(row_div), int(x_rows), *swiglu, int(x_stride), int(out_stride))
+        self._ref = ctypes.byref(self._struct)
+        self._elements = (self.m * self.num_groups * self.x_stride, self.m * self.x_stride)  # of x: a stack's, ragged
+        self._gather = (-1, None)
+
+    def rows(self, ragged):
+        return self.m if ragged else self.m * self.num_groups
+
+    def _scales(self, ragged):
+        """Scales of the quantised operand."""
+        rows = self.rows(ragged) if self.block_rows == 1 else self.num_groups * -(-self.m // self.block_rows)
+        return rows * self.blocks
+
+
+def _fp8_codes(t, n, name):
+    """Address of a contiguous tensor of at least n E4M3 codes, as torch's type or as bytes (None stays None)."""
+    if isinstance(t, _Tensor) and t.dtype is E4M3:
+        t = t.view(_U8)
+    return _fp4_buffer(t, _U8, n, name)
+
+
+def _fp8_weights(cfg, w_codes, w_scales):
+    e, n, k = cfg.num_groups, cfg.n, cfg.k
+    return _fp8_weight(w_codes, w_scales, e, n, k, "w_codes", "w_scales")
+
+
+def _fp8_weight(codes, scales, e, n, k, name, scales_name):
+    """Addresses of e quantised [n, k] matrices and of their scales [e, ceil(n / 128), ceil(k / 128)]."""
+    cp = _fp8_codes(codes, e * n * k, name)
+    sp = _fp4_buffer(scales, _F32, e * -(-n // 128) * -(-k // 128), scales_name)
+    if cp is not None and codes.numel() != e * n * k and _wider(codes, k):
+        raise ValueError(f"{name} has rows of {codes.shape[-1]} codes, the config rows of {k}")
+    if sp is not None and scales.numel() != e * -(-n // 128) * -(-k // 128) and _wider(scales, -(-k // 128)):
+        raise ValueError(f"{scales_name} has rows of {scales.shape[-1]} scales, the config rows of {-(-k // 128)}")
+    return cp, sp
+
+
+def _fp8_x(cfg, x, rows, ragged):
+    return _fp4_x(cfg, x, rows, ragged, _Fp8Config)
+
+
+def fp8_empty(cfg: Fp8Config, device, ragged=False):
+    """Output buffers of ``fp8_quantize``: codes [.., m, k] E4M3, scales [.., m or ceil(m / 128), ceil(k / 128)] fp32."""
+    lead = () if ragged else (cfg.num_groups,)
+    rows = cfg.m if cfg.block_rows == 1 else -(-cfg.m // cfg.block_rows)
+    return (torch.empty(*lead, cfg.m, cfg.k, dtype=E4M3, device=device),
+            torch.empty(*lead, rows, cfg.blocks, dtype=torch.float32, device=device))
+
+
+def fp8_quantize(cfg: Fp8Config, x, codes, scales, values=None, rows=None, offsets=None, stream=None):
+    """Enqueue the quantisation of x rows into ``codes`` and ``scales`` (``b4_fp8_quantize``).
+
+    x: rows of the config's width, x_stride elements apart, or a contiguous tensor of any shape that holds exactly the
+    config's elements.  ``rows`` gathers from x's rows (entries that name none give zero rows)."""
+    ragged = offsets is not None
+    n = cfg.rows(ragged)
+    _on_device(x, "x")
+    st = _lib.b4_fp8_quantize(
+        _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _fp4_buffer(rows, _I32, n, "rows"),
+        _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None,
+        _fp8_codes(codes, n * cfg.k, "codes"), _fp4_buffer(scales, _F32, cfg._scales(ragged), "scales"),
+        values if values is None else _fp4_buffer(values, cfg.x_dtype, n * cfg.k, "values"), _stream_of(stream, x))
+    if st:
+        _check(st)
+
+
+def fp8_matmul(cfg: Fp8Config, a_codes, a_scales, w_codes, w_scales, out, offsets=None, out_rows=None,
+               device_status=None, stream=None):
+    """Enqueue the product of two quantised operands (``b4_fp8_matmul``)."""
+    n = cfg.rows(offsets is not None)
+    _on_device(a_codes, "a_codes")
+    wp, sp = _fp8_weights(cfg, w_codes, w_scales)
+    st = _lib.b4_fp8_matmul(
+        cfg._ref, _fp8_codes(a_codes, n * cfg.k, "a_codes"), _fp4_buffer(a_scales, _F32, n * cfg.blocks, "a_scales"),
+        wp, sp, offsets if offsets is None else _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets"),
+        out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, n, "out_rows"), _fp4_out(cfg, out, n),
+        device_status if device_status is None else _fp4_buffer(device_status, _I32, 2, "device_status"),
+        _stream_of(stream, a_codes))
+    if st:
+        _check(st)
+
+
+def fp8_linear_workspace_bytes(cfg: Fp8Config) -> int:
+    n = _lib.b4_fp8_linear_workspace_bytes(cfg._ref)
+    if n == 0:
+        raise B4Error(B4_ERR_INVALID_ARGUMENT, last_error())
+    return int(n)
+
+
+def fp8_linear(cfg: Fp8Config, x, w_codes, w_scales, out, workspace, rows=None, offsets=None, out_rows=None, stream=None):
+    """Enqueue quantisation of x and the product with the quantised weights: ``out`` [m, n].
+
+    ``w_codes`` [groups, n, k] and ``w_scales`` [groups, ceil(n / 128), ceil(k / 128)] as a checkpoint holds them.  With
+    ``offsets`` [groups + 1] the rows are grouped by expert; ``rows`` gathers them from x (row i of the operand is x
+    row rows[i] // row_div) and ``out_rows`` scatters the result.
+    """
+    m = cfg.m
+    ragged = offsets is not None
+    _on_device(x, "x")
+    wp, sp = _fp8_weights(cfg, w_codes, w_scales)
+    st = _lib.b4_fp8_linear(
+        _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _fp4_buffer(rows, _I32, m, "rows"),
+        _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None, wp, sp,
+        out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, m, "out_rows"), _fp4_out(cfg, out, m),
+        _fp4_buffer(workspace, _U8, 0, "workspace"), workspace.numel(), _stream_of(stream, x))
+    if st:
+        _check(st)
+
+
+def fused_moe_fp8_workspace_bytes(cfg: MoEConfig, activation: int) -> int:
+    c = cfg._c()
+    n = _lib.b4_fused_moe_fp8_workspace_bytes(ctypes.byref(c), int(activation))
+    if n == 0:
+        raise B4Error(B4_ERR_INVALID_ARGUMENT, last_error())
+    return int(n)
+
+
+def fused_moe_fp8(cfg: MoEConfig, x, w13, s13, w2, s2, topk_ids, topk_weights, activation, out, workspace, stream=None):
+    """The fused layer with 8-bit weights and activations (``b4_fused_moe_fp8``): weights as a checkpoint of E4M3 codes
+    with an fp32 scale per 128 x 128 holds them (or ``fp8_quantize`` with block_rows = 128 makes them); ``out`` [m, H]
+    bf16 is written in full.  The config's format and path are not read."""
+    e, m, h, i = cfg.num_local_experts, cfg.m, cfg.hidden, cfg.inter
+    rows, routes = m * h, m * cfg.top_k
+    xp, op = _fp4_buffer(x, torch.bfloat16, rows, "x"), _fp4_buffer(out, torch.bfloat16, rows, "out")
+    w13p, s13p = _fp8_weight(w13, s13, e, i if activation == RELU2 else 2 * i, h, "w13", "s13")
+    w2p, s2p = _fp8_weight(w2, s2, e, h, i, "w2", "s2")
+    idp = _fp4_buffer(topk_ids, _I32, routes, "topk_ids")
+    wtp = _fp4_buffer(topk_weights, _F32, routes, "topk_weights")
+    _need(workspace, _U8, "workspace")
+    if None in (xp, op, w13p, s13p, w2p, s2p, idp, wtp):
+        for t, name in ((x, "x"), (out, "out"), (topk_ids, "topk_ids"), (topk_weights, "topk_weights"), (w13, "w13"),
+                        (s13, "s13"), (w2, "w2"), (s2, "s2")):
+            if t is None:
+                raise TypeError(f"{name} must be a torch tensor")
+    for t, name in ((x, "x"), (out, "out")):
+        if t.numel() != rows and _wider(t, h):
+            raise ValueError(f"{name} has rows of {t.shape[-1]} elements, the config rows of {h}")
+    _on_device(x, "x")
+    c = cfg._c()
+    st = _lib.b4_fused_moe_fp8(ctypes.byref(c), xp, w13p, s13p, w2p, s2p, idp, wtp, int(activation), op,
+                               workspace.data_ptr(), workspace.numel(), _stream_of(stream, x))
     if st:
         _check(st)
 

@@ -1,0 +1,33 @@
+// Parameter blocks of the FP8 operators (b4_fp8_* and b4_fused_moe_fp8 in b4moe.h):
+// E4M3 operands with an fp32 scale per block of 128 along K.
+//
+// A quantised operand of R rows and K columns is
+//   codes   [R][K] bytes of E4M3 (K a multiple of 16, so rows are 16-byte pieces);
+//   scales  [R][ceil(K / 128)] fp32 for activation rows, [ceil(R / 128)][ceil(K / 128)]
+//           for each weight matrix: the layout in which checkpoints hold them.
+#pragma once
+
+#include "fp4.cuh"
+
+namespace b4 {
+
+constexpr int kFp8Block = 128;
+
+struct Fp8QuantParams {
+  Fp4QuantParams q;  // source rows, gathering, activation, codes, values, status (scales and gs unused)
+  float* scales;
+  int kb;            // blocks along K
+  int pow2;          // scales are powers of two
+};
+
+struct Fp8GemmParams {
+  CUtensorMap tmap_w;     // weight codes [E N][K], box 128 bytes x 128 rows
+  CUtensorMap tmap_a;     // activation codes [rows][K], box 128 bytes x the kernel's rows
+  Fp4GemmParams g;        // groups, sizes, offsets, output, status (operands and scales unused)
+  const float* w_scales;  // [E][ceil(N / 128)][kb]
+  const float* a_scales;  // [rows][kb]
+  int kb;
+  int a_vec;              // rows of a_scales are 16-byte aligned
+};
+
+}  // namespace b4

@@ -1,0 +1,232 @@
+// FP8 block quantisation: rows of x (gathered through an index, behind SwiGLU / clamped
+// swiglu / ReLU^2) into E4M3 codes with an fp32 scale per block of 128 along K, or weight
+// matrices with one per 128 x 128.
+//
+//   s = amax / 448, or 2^j, j the least with amax <= 448 2^j;  at least 2^-126; 1 where amax is 0
+//   c = e4m3(h / s), nearest even of the quotient in fp32; a block with an infinity or a
+//       NaN has the scale NaN
+//
+// A thread takes 16 consecutive elements: a 32-byte load (two of fp32) and a 16-byte store
+// of codes; eight neighbouring threads are a block of 128 and join their maxima by three
+// shuffles.  The quotient is h y + h z in one fused multiply-add, y an approximate reciprocal of
+// s and z what it lacks: to 46 bits before its rounding, two operations an element.
+
+#include <algorithm>
+
+#include "fp4_quant.cuh"
+#include "fp8.cuh"
+
+namespace b4 {
+
+using namespace fp4q;
+
+namespace {
+
+constexpr int kThreads8 = 128;
+constexpr int kBlockThreads = 256;  // of a 128 x 128 block: four chunks a thread
+
+// The scale of a block from the bits of its largest magnitude.
+template <bool POW2>
+__device__ __forceinline__ float block_scale(uint32_t a) {
+  if (a == 0) return 1.f;
+  if (a >= kInfBits) return __uint_as_float(0x7fffffffu);
+  if (POW2) {
+    const int e = (int)(a >> 23) - 8 + ((a & 0x7fffffu) > 0x600000u);  // 448 = 1.75 2^8
+    return __uint_as_float((uint32_t)max(e, 1) << 23);
+  }
+  return fmaxf(__fdiv_rn(__uint_as_float(a), 448.f), 0x1p-126f);
+}
+
+// Sixteen codes of a chunk under the scale s.
+template <bool POW2, typename C>
+__device__ __forceinline__ uint4 encode8(const C& h, float s) {
+  float2 q[8];
+  if (POW2 && s == s) {
+    const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 x = h.pair(j);
+      q[j] = make_float2(x.x * inv, x.y * inv);
+    }
+  } else if (s >= 0x1p-80f && s <= 0x1p80f) {
+    const Recip r = recip(s);
+    const uint64_t y = pack2(r.y, r.y), z = pack2(r.z, r.z);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 x = h.pair(j);
+      const uint64_t xx = pack2(x.x, x.y);
+      q[j] = unpack2(fma2(xx, y, mul2(xx, z)));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 x = h.pair(j);
+      q[j] = s == s ? make_float2(true_quotient(x.x, s), true_quotient(x.y, s)) : make_float2(s, s);
+    }
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = __nv_cvt_float2_to_fp8x2(q[j], __NV_SATFINITE, __NV_E4M3);
+  return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+}
+
+// What the codes stand for, in x's type.
+template <typename T>
+__device__ __forceinline__ void store_values8(T* dst, int level, const uint4& w, float s) {
+  const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+  T e[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const __nv_fp8x2_storage_t pair = (__nv_fp8x2_storage_t)(word[j >> 1] >> (16 * (j & 1)));
+    const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3)));
+    from_f32(&e[2 * j], __fmul_rn(v.x, s));
+    from_f32(&e[2 * j + 1], __fmul_rn(v.y, s));
+  }
+  uint32_t o[16 * sizeof(T) / 4];
+  memcpy(o, e, sizeof(o));
+  store_words(dst, level, o);
+}
+
+template <typename T, bool ACT>
+__host__ __device__ constexpr int chunks_of_thread() {
+  return ACT ? 1 : sizeof(T) == 2 ? 4 : 2;
+}
+
+}  // namespace
+
+// A scale per row and 128 columns.
+template <typename T, bool ACT, bool POW2, int N>
+__global__ void __launch_bounds__(kThreads8) fp8_quantize_kernel(const __grid_constant__ Fp8QuantParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const Fp4QuantParams& q = p.q;
+  if (q.status && blockIdx.x == 0 && threadIdx.x < 2) q.status[threadIdx.x] = 0;
+  const uint32_t slots = 8u * p.kb;  // chunks of a row, whole blocks
+  int64_t rows = (int64_t)q.groups * q.m;
+  if (q.offsets) rows = min(max(__ldg(q.offsets + q.groups), 0), q.m);
+  const int64_t base = (int64_t)blockIdx.x * (kThreads8 * N);
+  const int64_t r0 = base / slots;
+  const uint32_t c0 = (uint32_t)(base - r0 * slots);
+  Chunk<T, ACT> h[N];
+  int64_t row[N];
+  int chunk[N];
+  bool live[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t j = c0 + i * kThreads8 + threadIdx.x;
+    row[i] = r0 + j / slots;
+    chunk[i] = (int)(j % slots);
+    live[i] = row[i] < rows;
+    int64_t src = row[i];
+    if (q.rows && live[i]) {
+      const int r = __ldg(q.rows + row[i]);
+      src = r < 0 ? -1 : r / q.row_div;
+      if (q.x_rows > 0 && src >= q.x_rows) src = -1;
+    }
+    if (live[i] && src >= 0 && 16 * chunk[i] < q.k)
+      h[i].get(q, reinterpret_cast<const T*>(q.x) + src * q.x_stride, chunk[i]);
+    else h[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t a = h[i].amax();
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const float s = block_scale<POW2>(a);
+    if (!live[i]) continue;
+    if ((chunk[i] & 7) == 0) p.scales[row[i] * p.kb + (chunk[i] >> 3)] = s;
+    if (16 * chunk[i] < q.k) {
+      const uint4 w = encode8<POW2>(h[i], s);
+      *reinterpret_cast<uint4*>(q.codes + row[i] * q.ld + 16 * chunk[i]) = w;
+      if (q.values) store_values8(reinterpret_cast<T*>(q.values) + row[i] * q.k + 16 * chunk[i], q.values_vec, w, s);
+    }
+  }
+}
+
+// A scale per 128 x 128: a block of threads takes one.
+template <typename T, bool ACT, bool POW2>
+__global__ void __launch_bounds__(kBlockThreads) fp8_quantize_block_kernel(const __grid_constant__ Fp8QuantParams p) {
+  __shared__ uint32_t s_max[kBlockThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const Fp4QuantParams& q = p.q;
+  const int row_blocks = cdiv(q.m, kFp8Block);
+  const int64_t gb = blockIdx.x / (uint32_t)p.kb;  // group and row block
+  const int kb = blockIdx.x % (uint32_t)p.kb;
+  const int64_t group = gb / row_blocks;
+  const int r0 = (int)(gb - group * row_blocks) * kFp8Block + (threadIdx.x >> 3);
+  const int chunk = 8 * kb + (threadIdx.x & 7);
+  const bool in = 16 * chunk < q.k;
+  Chunk<T, ACT> h[4];
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 32 * i;
+    if (in && r < q.m) h[i].get(q, reinterpret_cast<const T*>(q.x) + (group * q.m + r) * q.x_stride, chunk);
+    else h[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a = max(a, h[i].amax());
+  a = __reduce_max_sync(0xffffffffu, a);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kBlockThreads / 32; ++w) a = max(a, s_max[w]);
+  const float s = block_scale<POW2>(a);
+  if (threadIdx.x == 0) p.scales[blockIdx.x] = s;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 32 * i;
+    if (in && r < q.m) {
+      const int64_t row = group * q.m + r;
+      const uint4 w = encode8<POW2>(h[i], s);
+      *reinterpret_cast<uint4*>(q.codes + row * q.ld + 16 * chunk) = w;
+      if (q.values) store_values8(reinterpret_cast<T*>(q.values) + row * q.k + 16 * chunk, q.values_vec, w, s);
+    }
+  }
+}
+
+namespace {
+
+template <typename K>
+cudaError_t launch8(K kern, int64_t grid, int threads, cudaStream_t stream, const Fp8QuantParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <typename T, bool ACT, bool POW2>
+cudaError_t quantize8(const Fp8QuantParams& p, int block_rows, int sms, cudaStream_t stream) {
+  const Fp4QuantParams& q = p.q;
+  if (block_rows > 1)
+    return launch8(fp8_quantize_block_kernel<T, ACT, POW2>, (int64_t)q.groups * cdiv(q.m, kFp8Block) * p.kb, kBlockThreads,
+                   stream, p);
+  const int64_t chunks = (q.offsets ? q.m : (int64_t)q.groups * q.m) * p.kb * 8;
+  constexpr int N = chunks_of_thread<T, ACT>();
+  if (chunks <= (int64_t)sms * 512) return launch8(fp8_quantize_kernel<T, ACT, POW2, 1>, (chunks + kThreads8 - 1) / kThreads8, kThreads8, stream, p);
+  return launch8(fp8_quantize_kernel<T, ACT, POW2, N>, (chunks + kThreads8 * N - 1) / (kThreads8 * N), kThreads8, stream, p);
+}
+
+template <typename T>
+cudaError_t quantize8_t(const Fp8QuantParams& p, int block_rows, int sms, cudaStream_t stream) {
+  if (p.q.act < 0)
+    return p.pow2 ? quantize8<T, false, true>(p, block_rows, sms, stream) : quantize8<T, false, false>(p, block_rows, sms, stream);
+  return p.pow2 ? quantize8<T, true, true>(p, block_rows, sms, stream) : quantize8<T, true, false>(p, block_rows, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize(const Fp8QuantParams& p, int dtype, int block_rows, int num_sms, cudaStream_t stream) {
+  if (dtype == 0) return quantize8_t<__nv_bfloat16>(p, block_rows, num_sms, stream);
+  if (dtype == 1) return quantize8_t<__half>(p, block_rows, num_sms, stream);
+  return quantize8_t<float>(p, block_rows, num_sms, stream);
+}
+
+}  // namespace b4
