@@ -20,6 +20,15 @@ struct Fp8QuantParams {
   int pow2;          // scales are powers of two
 };
 
+// Shared memory for the partial sums of a unit that a cluster splits along K: 512 bytes for
+// every other CTA and activation row.
+constexpr int kFp8PartBytes = 56 * 1024;
+
+// Direct products: rows of a call that the kernel quantises for itself, rows of its operand in
+// shared memory, and stages of 128 K of them that a CTA keeps.
+constexpr int kFp8DirectRows = 8, kFp8DirectTile = 8;
+constexpr int kFp8DirectStages = 64, kFp8DirectSplitStages = 24;
+
 struct Fp8GemmParams {
   CUtensorMap tmap_w;     // weight codes [E N][K], box 128 bytes x 128 rows
   CUtensorMap tmap_a;     // activation codes [rows][K], box 128 bytes x the kernel's rows
@@ -28,6 +37,8 @@ struct Fp8GemmParams {
   const float* a_scales;  // [rows][kb]
   int kb;
   int a_vec;              // rows of a_scales are 16-byte aligned
+  Fp8QuantParams q;       // direct: the rows the kernel quantises for itself
+  int x_dtype;
 };
 
 }  // namespace b4

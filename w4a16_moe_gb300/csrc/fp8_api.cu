@@ -16,7 +16,9 @@ namespace b4 {
 void set_last_error(const char* fmt, ...);
 b4_status require_device(int* sms);
 cudaError_t launch_fp8_quantize(const Fp8QuantParams& p, int dtype, int block_rows, int num_sms, cudaStream_t stream);
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int rows, int grid, int splits, cudaStream_t stream);
+cudaError_t launch_fp8_gemm_direct(const Fp8GemmParams& p, int grid, int splits, cudaStream_t stream);
+cudaError_t launch_fp8_gemm_pair(const Fp8GemmParams& p, int pairs, cudaStream_t stream);
 cudaError_t launch_fp4_combine(const Fp4CombineParams& p, cudaStream_t stream);
 }  // namespace b4
 
@@ -111,17 +113,39 @@ Fp8QuantParams quant_params(const b4_fp8_config* c, const void* x, const int32_t
   return p;
 }
 
-// Units of 128 rows x 128 outputs a call can have at most: a group ends at most one
-// unit early, and holds at least one row.
-int64_t most_units(const b4_fp8_config* c, bool ragged) {
-  int64_t tok = (int64_t)cdiv(c->m, 128) * c->num_groups;
-  if (ragged) tok = c->m / 128 + c->num_groups < c->m ? c->m / 128 + c->num_groups : c->m;
-  return tok * cdiv(c->n, 128);
+// Activation rows of a unit: 32 or 128 (fp8_gemm.cuh, one SM a unit of 128 outputs), 256
+// (fp8_gemm_pair.cu, a pair of SMs, 256 outputs).  By the rows, of ragged groups their mean.
+// Measured in us at 32 / 128 / 256: N = K = 4096, m = 64 10.2 / 13.2 / 18.1, 128 13.1 / 14.3 / 19.8, 256 22.8 / 14.6 /
+// 20.0, 512 41.8 / 15.1 / 20.4, 1024 - / 29 / 21.6; 64 groups, N = 2816, K = 2048, mean 6 61.8 / 63.8 / 78.2, 16 62.6 / 64.5 /
+// 81.5, 96 176 / 75.9 / 111, 192 321 / 145 / 120; 28 groups, N = K = 2880, mean 32 59.4 / 49.1 / 68.0, 64 87.6 / 51.5 / 74.6.
+int unit_rows(const b4_fp8_config* c, bool ragged) {
+  if (ragged) {
+    const int64_t per = c->m / c->num_groups;
+    return per <= 16 ? 32 : per <= 128 ? 128 : 256;
+  }
+  return c->m <= 128 ? 32 : c->m <= 512 ? 128 : 256;
 }
 
-b4_status launch_product(const b4_fp8_config* c, const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
-                         const float* w_scales, const int32_t* offsets, const int32_t* out_rows, void* out,
-                         uint32_t* status, bool a_is_new, int sms, cudaStream_t stream) {
+// Most units a call can have: a group ends at most one unit early, and holds at least one
+// row.
+int64_t most_units(const b4_fp8_config* c, bool ragged, int rows) {
+  int64_t tok = (int64_t)cdiv(c->m, rows) * c->num_groups;
+  if (ragged) tok = c->m / rows + c->num_groups < c->m ? c->m / rows + c->num_groups : c->m;
+  return tok * cdiv(c->n, rows == 256 ? 256 : 128);
+}
+
+// CTAs that share a unit along K where the units are fewer than the SMs.
+int k_splits(const b4_fp8_config* c, int64_t units, int sms) {
+  const int stages = cdiv(c->k, kFp8Block);
+  const int rows = c->m < 32 ? c->m : 32;
+  int splits = 8;
+  while (splits > 1 && (splits * units > sms || stages < 3 * splits || (splits - 1) * rows * 512 > kFp8PartBytes)) splits /= 2;
+  return splits;
+}
+
+// The fields of a product that do not depend on where its activations come from.
+Fp8GemmParams product_params(const b4_fp8_config* c, const float* w_scales, const int32_t* offsets, const int32_t* out_rows,
+                             void* out, uint32_t* status) {
   Fp8GemmParams p{};
   Fp4GemmParams& g = p.g;
   g.groups = c->num_groups;
@@ -137,18 +161,51 @@ b4_status launch_product(const b4_fp8_config* c, const uint8_t* a_codes, const f
   const int per16 = 16 / dtype_bytes(c->out_dtype);
   g.vec = aligned(out, 16) && g.out_stride % per16 == 0 && c->n % per16 == 0;
   g.halves_from = INT_MAX;
-  g.a_is_new = a_is_new;
   g.status = status;
   p.w_scales = w_scales;
-  p.a_scales = a_scales;
   p.kb = cdiv(c->k, kFp8Block);
-  p.a_vec = aligned(a_scales, 16) && p.kb % 4 == 0;
-  if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k, c->k, 128) ||
-      !make_tmap_bytes_2d(&p.tmap_a, a_codes, (uint64_t)operand_rows(c, offsets), c->k, c->k, 128))
+  return p;
+}
+
+// K splits of a direct product (0: the call takes the two launches): few rows, every unit has a
+// CTA or a cluster of its own, and a CTA's part of the quantised rows fits in shared memory.
+int direct_splits(const b4_fp8_config* c, bool ragged, int sms) {
+  if (c->m > kFp8DirectRows) return 0;
+  const int64_t units = most_units(c, ragged, 32);
+  if (units > sms) return 0;
+  const int splits = k_splits(c, units, sms);
+  return cdiv(cdiv(c->k, kFp8Block), splits) <= (splits > 1 ? kFp8DirectSplitStages : kFp8DirectStages) ? splits : 0;
+}
+
+b4_status launch_direct(const b4_fp8_config* c, const Fp8QuantParams& q, const uint8_t* w_codes, const float* w_scales,
+                        const int32_t* out_rows, void* out, uint32_t* clear, uint32_t* status, int splits,
+                        cudaStream_t stream) {
+  Fp8GemmParams p = product_params(c, w_scales, q.q.offsets, out_rows, out, status);
+  if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k, c->k, 128))
     FP8_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
-  const int64_t units = most_units(c, offsets);
+  p.q = q;
+  p.x_dtype = c->x_dtype;
+  p.g.clear_status = clear != nullptr;
+  return cuda_status(launch_fp8_gemm_direct(p, (int)most_units(c, q.q.offsets, 32), splits, stream), "fp8 product");
+}
+
+b4_status launch_product(const b4_fp8_config* c, const uint8_t* a_codes, const float* a_scales, const uint8_t* w_codes,
+                         const float* w_scales, const int32_t* offsets, const int32_t* out_rows, void* out,
+                         uint32_t* status, bool a_is_new, int sms, cudaStream_t stream) {
+  Fp8GemmParams p = product_params(c, w_scales, offsets, out_rows, out, status);
+  const int rows = unit_rows(c, offsets);
+  if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k, c->k, rows == 256 ? 64 : 128) ||
+      !make_tmap_bytes_2d(&p.tmap_a, a_codes, (uint64_t)operand_rows(c, offsets), c->k, c->k, rows == 256 ? 64 : 32))
+    FP8_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
+  p.a_scales = a_scales;
+  p.a_vec = aligned(a_scales, 16) && p.kb % 4 == 0;
+  p.g.a_is_new = a_is_new;
+  const int64_t units = most_units(c, offsets, rows);
   if (units > (1 << 30)) FP8_INVALID("too many units of work: m, n and num_groups too large together");
-  return cuda_status(launch_fp8_gemm(p, (int)(units < sms ? units : sms), stream), "fp8 product");
+  if (rows == 256)
+    return cuda_status(launch_fp8_gemm_pair(p, (int)(units < sms / 2 ? units : sms / 2), stream), "fp8 product");
+  const int splits = rows == 32 ? k_splits(c, units, sms) : 1;
+  return cuda_status(launch_fp8_gemm(p, rows, (int)(splits > 1 || units < sms ? units : sms), splits, stream), "fp8 product");
 }
 
 // Workspace of b4_fp8_linear: the quantised activation operand of m rows.
@@ -178,6 +235,8 @@ b4_status quantize_and_multiply(const b4_fp8_config* c, const void* x, const int
   uint8_t* codes = ws + L.codes;
   float* scales = reinterpret_cast<float*>(ws + L.scales);
   Fp8QuantParams q = quant_params(c, x, rows, offsets, codes, scales, nullptr);
+  if (const int splits = direct_splits(c, offsets, sms))
+    return launch_direct(c, q, w_codes, w_scales, out_rows, out, clear, status, splits, stream);
   q.q.status = clear;
   const cudaError_t e = launch_fp8_quantize(q, c->x_dtype, 1, sms, stream);
   if (e != cudaSuccess) return cuda_status(e, "fp8 quantise");
