@@ -762,13 +762,21 @@ class RouterConfig:
         self._ref = ctypes.byref(self._struct)
 
 
-def _on_device(t, name):
-    """The kernels run on the current device: a tensor of another is refused."""
-    device = t.device
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {device}, the current device is cuda:{torch.cuda.current_device()}")
+# the current device without torch.cuda's own checks (0.5 us a call)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _launch_stream(stream, t, name):
+    """Handle of ``stream``, or of the current stream.  The kernels run on the current device: a tensor of another is
+    refused."""
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    if index != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+    if stream is not None:
+        return stream.cuda_stream
+    return _stream(None) if _raw_stream is None else _raw_stream(index)
 
 
 def route_topk(cfg: RouterConfig, logits, topk_ids, topk_weights, bias=None, num_tokens=None, stream=None):
@@ -777,7 +785,7 @@ def route_topk(cfg: RouterConfig, logits, topk_ids, topk_weights, bias=None, num
     ``num_tokens`` (a device int32) on get ids of -1, which the layers drop."""
     if logits.dtype is not cfg.dtype:
         raise TypeError(f"logits must be {cfg.dtype}, got {logits.dtype}")
-    _on_device(logits, "logits")
+    handle = _launch_stream(stream, logits, "logits")
     shape = logits.shape
     if len(shape) != 2 or shape[0] < cfg.m or shape[1] < cfg.num_experts:
         raise ValueError(f"logits must be [{cfg.m}, {cfg.num_experts}], got {list(shape)}")
@@ -786,8 +794,7 @@ def route_topk(cfg: RouterConfig, logits, topk_ids, topk_weights, bias=None, num
     st = _lib.b4_route_topk(
         cfg._ref, logits.data_ptr(), bias if bias is None else _fp4_buffer(bias, _F32, cfg.num_experts, "bias"),
         num_tokens if num_tokens is None else _fp4_buffer(num_tokens, _I32, 1, "num_tokens"),
-        _route_out(topk_ids, _I32, cfg, "topk_ids"), _route_out(topk_weights, _F32, cfg, "topk_weights"),
-        _stream_of(stream, logits))
+        _route_out(topk_ids, _I32, cfg, "topk_ids"), _route_out(topk_weights, _F32, cfg, "topk_weights"), handle)
     if st:
         _check(st)
 
@@ -880,12 +887,12 @@ def fp8_quantize(cfg: Fp8Config, x, codes, scales, values=None, rows=None, offse
     config's elements.  ``rows`` gathers from x's rows (entries that name none give zero rows)."""
     ragged = offsets is not None
     n = cfg.rows(ragged)
-    _on_device(x, "x")
+    handle = _launch_stream(stream, x, "x")
     st = _lib.b4_fp8_quantize(
         _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _fp4_buffer(rows, _I32, n, "rows"),
         _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None,
         _fp8_codes(codes, n * cfg.k, "codes"), _fp4_buffer(scales, _F32, cfg._scales(ragged), "scales"),
-        values if values is None else _fp4_buffer(values, cfg.x_dtype, n * cfg.k, "values"), _stream_of(stream, x))
+        values if values is None else _fp4_buffer(values, cfg.x_dtype, n * cfg.k, "values"), handle)
     if st:
         _check(st)
 
@@ -894,14 +901,14 @@ def fp8_matmul(cfg: Fp8Config, a_codes, a_scales, w_codes, w_scales, out, offset
                device_status=None, stream=None):
     """Enqueue the product of two quantised operands (``b4_fp8_matmul``)."""
     n = cfg.rows(offsets is not None)
-    _on_device(a_codes, "a_codes")
+    handle = _launch_stream(stream, a_codes, "a_codes")
     wp, sp = _fp8_weights(cfg, w_codes, w_scales)
     st = _lib.b4_fp8_matmul(
         cfg._ref, _fp8_codes(a_codes, n * cfg.k, "a_codes"), _fp4_buffer(a_scales, _F32, n * cfg.blocks, "a_scales"),
         wp, sp, offsets if offsets is None else _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets"),
         out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, n, "out_rows"), _fp4_out(cfg, out, n),
         device_status if device_status is None else _fp4_buffer(device_status, _I32, 2, "device_status"),
-        _stream_of(stream, a_codes))
+        handle)
     if st:
         _check(st)
 
@@ -922,13 +929,13 @@ def fp8_linear(cfg: Fp8Config, x, w_codes, w_scales, out, workspace, rows=None, 
     """
     m = cfg.m
     ragged = offsets is not None
-    _on_device(x, "x")
+    handle = _launch_stream(stream, x, "x")
     wp, sp = _fp8_weights(cfg, w_codes, w_scales)
     st = _lib.b4_fp8_linear(
         _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _fp4_buffer(rows, _I32, m, "rows"),
         _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None, wp, sp,
         out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, m, "out_rows"), _fp4_out(cfg, out, m),
-        _fp4_buffer(workspace, _U8, 0, "workspace"), workspace.numel(), _stream_of(stream, x))
+        _fp4_buffer(workspace, _U8, 0, "workspace"), workspace.numel(), handle)
     if st:
         _check(st)
 
@@ -961,10 +968,10 @@ def fused_moe_fp8(cfg: MoEConfig, x, w13, s13, w2, s2, topk_ids, topk_weights, a
     for t, name in ((x, "x"), (out, "out")):
         if t.numel() != rows and _wider(t, h):
             raise ValueError(f"{name} has rows of {t.shape[-1]} elements, the config rows of {h}")
-    _on_device(x, "x")
+    handle = _launch_stream(stream, x, "x")
     c = cfg._c()
     st = _lib.b4_fused_moe_fp8(ctypes.byref(c), xp, w13p, s13p, w2p, s2p, idp, wtp, int(activation), op,
-                               workspace.data_ptr(), workspace.numel(), _stream_of(stream, x))
+                               workspace.data_ptr(), workspace.numel(), handle)
     if st:
         _check(st)
 

@@ -211,15 +211,16 @@ __device__ __forceinline__ Unit get_unit(const Fp4GemmParams& p, const Groups& g
   return U;
 }
 
-// Rows of a ragged output past the last group are zero: 64 threads.
+// Rows of a ragged output past the last group are zero: THREADS threads.
+template <int THREADS = 64>
 __device__ __forceinline__ void clear_tail(const Fp4GemmParams& p, int live, int thread) {
   const int width = p.out_dtype == 2 ? 4 : 2;
   for (int r = live + blockIdx.x; r < p.m; r += gridDim.x) {
     uint8_t* row = reinterpret_cast<uint8_t*>(p.out) + (int64_t)r * p.out_stride * width;
     if (p.vec) {
-      for (int c = thread; c < p.n * width / 16; c += 64) reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
+      for (int c = thread; c < p.n * width / 16; c += THREADS) reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
     } else {
-      for (int c = thread; c < p.n; c += 64) {
+      for (int c = thread; c < p.n; c += THREADS) {
         if (width == 4) reinterpret_cast<uint32_t*>(row)[c] = 0;
         else reinterpret_cast<uint16_t*>(row)[c] = 0;
       }

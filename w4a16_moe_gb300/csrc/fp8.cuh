@@ -32,11 +32,13 @@ constexpr int kFp8DirectStages = 64, kFp8DirectSplitStages = 24;
 struct Fp8GemmParams {
   CUtensorMap tmap_w;     // weight codes [E N][K], box 128 bytes x 128 rows
   CUtensorMap tmap_a;     // activation codes [rows][K], box 128 bytes x the kernel's rows
+  CUtensorMap tmap_out;   // 16-bit outputs [rows][n], box 64 x 32 rows (pair kernel, where out_boxes)
+  int out_boxes;
   Fp4GemmParams g;        // groups, sizes, offsets, output, status (operands and scales unused)
   const float* w_scales;  // [E][ceil(N / 128)][kb]
   const float* a_scales;  // [rows][kb]
   int kb;
-  int a_vec;              // rows of a_scales are 16-byte aligned
+  int a_vec, w_vec;       // rows of a_scales, of w_scales are 16-byte aligned
   Fp8QuantParams q;       // direct: the rows the kernel quantises for itself
   int x_dtype;
 };

@@ -115,9 +115,10 @@ Fp8QuantParams quant_params(const b4_fp8_config* c, const void* x, const int32_t
 
 // Activation rows of a unit: 32 or 128 (fp8_gemm.cuh, one SM a unit of 128 outputs), 256
 // (fp8_gemm_pair.cu, a pair of SMs, 256 outputs).  By the rows, of ragged groups their mean.
-// Measured in us at 32 / 128 / 256: N = K = 4096, m = 64 10.2 / 13.2 / 18.1, 128 13.1 / 14.3 / 19.8, 256 22.8 / 14.6 /
-// 20.0, 512 41.8 / 15.1 / 20.4, 1024 - / 29 / 21.6; 64 groups, N = 2816, K = 2048, mean 6 61.8 / 63.8 / 78.2, 16 62.6 / 64.5 /
-// 81.5, 96 176 / 75.9 / 111, 192 321 / 145 / 120; 28 groups, N = K = 2880, mean 32 59.4 / 49.1 / 68.0, 64 87.6 / 51.5 / 74.6.
+// Measured in us at 32 / 128 / 256: N = K = 4096, m = 64 10.2 / 13.4 / 17.7, 128 13.3 / 13.9 / 19.7, 256 23.2 / 14.3 /
+// 18.9, 512 42.3 / 14.6 / 20.2, 1024 71 / 25.7 / 21.1; 64 groups, N = 2816, K = 2048, mean 6 62.9 / 64.2 / 89, 16 63.9 / 65.1 /
+// 89, 96 181 / 70.6 / 98, 128 230 / 93.4 / 99, 192 331 / 125 / 103; 28 groups, N = K = 2880, mean 32 56.6 / 48.1 / 64, 64 85.9 /
+// 49.4 / 65.
 int unit_rows(const b4_fp8_config* c, bool ragged) {
   if (ragged) {
     const int64_t per = c->m / c->num_groups;
@@ -143,6 +144,18 @@ int k_splits(const b4_fp8_config* c, int64_t units, int sms) {
   return splits;
 }
 
+// 16-bit outputs as boxes of 64 columns x 32 rows, 128-byte swizzle.
+bool make_tmap_out16(CUtensorMap* tm, void* out, uint64_t rows, uint64_t cols, uint64_t stride) {
+  TmapEncodeFn fn = tmap_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {stride * 2};
+  const cuuint32_t box[2] = {64, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The fields of a product that do not depend on where its activations come from.
 Fp8GemmParams product_params(const b4_fp8_config* c, const float* w_scales, const int32_t* offsets, const int32_t* out_rows,
                              void* out, uint32_t* status) {
@@ -164,6 +177,7 @@ Fp8GemmParams product_params(const b4_fp8_config* c, const float* w_scales, cons
   g.status = status;
   p.w_scales = w_scales;
   p.kb = cdiv(c->k, kFp8Block);
+  p.w_vec = aligned(w_scales, 16) && p.kb % 4 == 0;
   return p;
 }
 
@@ -194,9 +208,12 @@ b4_status launch_product(const b4_fp8_config* c, const uint8_t* a_codes, const f
                          uint32_t* status, bool a_is_new, int sms, cudaStream_t stream) {
   Fp8GemmParams p = product_params(c, w_scales, offsets, out_rows, out, status);
   const int rows = unit_rows(c, offsets);
-  if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k, c->k, rows == 256 ? 64 : 128) ||
+  if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k, c->k, 128) ||
       !make_tmap_bytes_2d(&p.tmap_a, a_codes, (uint64_t)operand_rows(c, offsets), c->k, c->k, rows == 256 ? 64 : 32))
     FP8_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
+  p.out_boxes = rows == 256 && !out_rows && p.g.vec && c->out_dtype != B4_DTYPE_F32;
+  if (p.out_boxes && !make_tmap_out16(&p.tmap_out, out, (uint64_t)operand_rows(c, offsets), c->n, p.g.out_stride))
+    FP8_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an output map");
   p.a_scales = a_scales;
   p.a_vec = aligned(a_scales, 16) && p.kb % 4 == 0;
   p.g.a_is_new = a_is_new;

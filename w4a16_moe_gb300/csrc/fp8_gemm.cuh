@@ -51,13 +51,14 @@ struct Cfg {
   static constexpr int kStage = kWStage + (DIRECT ? 0 : kAStage);
   static constexpr int kScaleRows = DIRECT ? kFp8DirectTile : ROWS;
   static constexpr int kScales = (DIRECT ? kOwnStages : kScaleRing) * kScaleRows * 4;
-  static constexpr int kFit = (208 * 1024 - kPart - kOwn - kScales) / kStage;
+  static constexpr int kFit = (200 * 1024 - kPart - kOwn - kScales) / kStage;
   static constexpr int kSlots = kFit < 12 ? kFit : 12;
   // activations first: the instructions read 128 rows of 128 bytes from each tile's start
   static constexpr size_t w = DIRECT ? kOwn : (size_t)kSlots * kAStage;
   static constexpr size_t part = w + (size_t)kSlots * kWStage;
   static constexpr size_t scales = part + kPart;
-  static constexpr size_t bars = scales + kScales;
+  static constexpr size_t stage = scales + kScales;
+  static constexpr size_t bars = stage + kEpiWarps * kStagePiece;
   static constexpr int kNumBars = 2 * kSlots + 2 * kAccs + 3;
   static constexpr size_t misc = bars + 8 * (kNumBars + 1);
   static constexpr size_t total(bool ragged) { return misc + 16 + (ragged ? sizeof(Groups) : 0); }
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const int q4 = warp & 3, half = (warp - 4) >> 2;
     const int r = 32 * q4 + lane;
     const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + 64 * half;
+    uint8_t* stage = smem + C::stage + (warp - 4) * kStagePiece;
     uint32_t i = 0;
     bool ok = true;
     for (int u = u0; u < n_units && ok; u += du) {
@@ -332,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
         continue;
       }
+      const int to = output_row(g, U.first + r, r < U.rows);
       float2 acc[32];
 #pragma unroll
       for (int c = 0; c < 32; ++c) acc[c] = make_float2(0.f, 0.f);
@@ -382,10 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             }
           }
       }
-      if (r >= U.rows) continue;
-      int to = U.first + r;
-      if (g.out_rows) to = __ldg(g.out_rows + to);
-      if (to >= 0 && to < g.out_rows_end) store_row<OUT>(g, (int64_t)to * g.out_stride, U.wtile * 128 + 64 * half, acc);
+      store_rows<OUT>(g, to, U.wtile * 128 + 64 * half, acc, stage, lane);
     }
   }
 

@@ -1,14 +1,25 @@
-// Product of two FP8 operands with scales per block of 128 along K on pairs of SMs
-// (tcgen05 cta_group::2): the form for many rows.  The formula is that of fp8_gemm.cu.
+// Product of two FP8 operands with scales per block of 128 along K on pairs of SMs: the
+// form for many rows.  The formula is that of fp8_gemm.cuh.
 //
-// A pair takes units of 256 activation rows x 256 weight rows: each CTA holds its own 128
-// activation rows and half of the weight rows (32 KB a stage of 128 K, for 512 cycles of
-// products), and accumulates its 128 rows x 256 outputs in its own tensor memory.  A stage is
-// one block of K.  It has two accumulators of 128 columns, one for each block of 128 weight
-// rows, twice: while the tensor core fills one of each pair, four warps read the other,
+// A pair takes units of 256 activation rows x 256 weight rows, each CTA 128 of the activation
+// rows.  Both need all of the weight rows: each CTA loads a block of 128 of them and multicasts
+// it to both, so an SM asks L2 for 32 KB a stage of 128 K and takes in 48 KB, for 512 cycles
+// of products (measured with copies alone: 480 cycles a stage on all SMs, 756 without
+// sharing).
+//
+// A stage is one block of K.  It has two accumulators of 128 columns, one for each block of 128
+// weight rows, twice: while the tensor core fills one of each pair, four warps read the other,
 // 32 lanes x 128 columns each, and add it to fp32 registers times the row's scale and the
-// weights'.
-// The 128 registers a thread holds its sums in come from the other warps (setmaxnreg).
+// weights'.  What is in tensor memory, 512 columns, takes a chain of steps to renew: 256 cycles
+// of products, 270 until a waiting warp has seen them done, 500 of promotion (of which 350 are
+// the loads and multiply-adds of two warps a scheduler), 200 until the next products issue; that
+// chain, 760 to 830 cycles for two stages' worth of one half, is what bounds the kernel, not
+// the 512 cycles of products.  Scales come through shared memory from a warp of their own, and the
+// products' issue is shared by two: what those warps looked up or issued themselves held up
+// the chain.
+//
+// Measured: N = K = 4096, 4096 rows 65 us (2.1 PFLOP/s), 8192 x 8192 x 4096 218 us (2.5 PFLOP/s); 64 groups of 192
+// rows, N = 2816, K = 2048 103 us.
 
 #include "fp8_mma.cuh"
 
@@ -19,46 +30,39 @@ cudaError_t ensure_smem_limit(const void* func, size_t bytes);
 namespace fp8 {
 
 constexpr int kPairRows = 256;
-constexpr int kPairSlots = 6;
+constexpr int kPairSlots = 3;
 constexpr int kPairBox = 64;                    // activation rows of a box
 constexpr int kPairAStage = 128 * 128;
-constexpr size_t kPairOffA = (size_t)kPairSlots * kWStage;
-constexpr size_t kPairOffBars = kPairOffA + (size_t)kPairSlots * kPairAStage;
+constexpr int kOutTile = 2 * 32 * 128;          // staged outputs of a warp: 32 rows of two times 64, 128-byte swizzle
+constexpr int kPairWStage = 2 * kWStage;        // both blocks of weight rows
+constexpr size_t kPairOffA = (size_t)kPairSlots * kPairWStage;
+constexpr size_t kPairOffStage = kPairOffA + (size_t)kPairSlots * kPairAStage;
+constexpr size_t kPairOffBars = kPairOffStage + kEpiWarps * kOutTile;
+constexpr int kPrefetch = 10;                   // stages of weights asked into L2 ahead of their copies
 constexpr int kAhead = 4;                       // units looked up ahead of the promoting warps
-constexpr int kPairBars = 2 * kPairSlots + 8 + 1 + 2 * kAhead;
-constexpr size_t kPairOffUnits = kPairOffBars + 8 * (kPairBars + 1);
-constexpr int kScaleDepth = 4;                  // stages of scales
+constexpr int kPairBars = 2 * kPairSlots + 8 + 1 + 2 * kAhead + 4;
+constexpr size_t kPairOffUnits = (kPairOffBars + 8 * kPairBars + 15) / 16 * 16;
+constexpr int kScaleQuad = 130 * 4;             // scales of four stages: 128 rows, two blocks of weights; two of these
 constexpr size_t kPairOffScales = kPairOffUnits + 16 * kAhead;
-constexpr size_t kPairOffMisc = kPairOffScales + kScaleDepth * 2 * 128 * sizeof(float);
+constexpr size_t kPairOffMisc = kPairOffScales + 2 * kScaleQuad * sizeof(float);
 constexpr size_t pair_smem(bool ragged) { return kPairOffMisc + 16 + (ragged ? sizeof(Groups) : 0); }
-
-// Registers of a thread after the split: 128 x 136 + 256 x 184 = 384 x 168, what the block is launched with.
-constexpr int kRegsLaunch = 168, kRegsIssue = 136, kRegsPromote = 184;
-static_assert(128 * kRegsIssue + 256 * kRegsPromote <= kThreads * kRegsLaunch, "the split fits the launch's registers");
-
-// A wait that is a link of the chain between products and promotion: looked at without
-// pause first (a suspended thread wakes late).
-__device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, const Abort& ab, uint32_t where) {
-#pragma unroll 1
-  for (int i = 0; i < 256; ++i)
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, where));
-}
 
 template <int OUT, bool RAGGED>
 __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_constant__ Fp8GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Groups& groups = *reinterpret_cast<Groups*>(smem + kPairOffMisc + 16);  // ragged only
   uint8_t* s_a = smem + kPairOffA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairOffBars);  // the leader's: copies of both CTAs
-  uint64_t* empty = full + kPairSlots;                                // each CTA's own
-  uint64_t* full_acc = empty + kPairSlots;                            // each CTA's own
-  uint64_t* empty_acc = full_acc + 4;                                 // the leader's: promoting warps of both
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairOffBars);
+  uint64_t* empty = full + kPairSlots;                                // the products of both CTAs are through with the slot
+  uint64_t* full_acc = empty + kPairSlots;
+  uint64_t* empty_acc = full_acc + 4;
   uint64_t* drain = empty_acc + 4;
-  uint64_t* full_unit = drain + 1;                                    // each CTA's own
+  uint64_t* full_unit = drain + 1;
   uint64_t* empty_unit = full_unit + kAhead;
+  uint64_t* full_scale = empty_unit + kAhead;
+  uint64_t* empty_scale = full_scale + 2;
   int4* s_unit = reinterpret_cast<int4*>(smem + kPairOffUnits);       // group, weight unit, first row, rows
-  float* s_scale = reinterpret_cast<float*>(smem + kPairOffScales);   // [stage][block of weights][row]
+  float* s_scale = reinterpret_cast<float*>(smem + kPairOffScales);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kPairOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kPairOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -70,12 +74,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
     *s_abort = 0;
     for (int i = 0; i < kPairSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&full_acc[i], 3);              // the products and two warps' scales
-      mbar_init(&empty_acc[i], kEpiWarps);  // four warps of each CTA
+      mbar_init(&full_acc[i], 1);
+      mbar_init(&empty_acc[i], kEpiWarps / 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full_scale[i], 1);
+      mbar_init(&empty_scale[i], kEpiWarps);
     }
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(&full_unit[i], 1);
@@ -84,8 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(s_tmem, 512);
-    tmem_relinquish_pair();
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
   }
   if (!g.a_is_new) pdl_wait();  // alone in its call: every input may come from the kernel before
   const int wpairs = cdiv(g.n, 256);
@@ -100,176 +108,165 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   const int u0 = blockIdx.x >> 1, du = gridDim.x >> 1;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 0) {
       // --------------------------------------------------------- copies
-      if (g.a_is_new) pdl_wait();
+      // Weights are asked into L2 kPrefetch stages ahead of their copies (across units, and
+      // from the start, under the quantiser): the ring alone has 48 KB of them on their way, a
+      // third of what DRAM's latency takes.
       uint32_t i = 0;
       bool ok = true;
-      const uint32_t full0 = warp_uniform(map_rank(full, 0));
+      int pu = u0, ps = 0, prow = 0;
+      auto weight_row = [&](const Unit& U) {
+        return (int)warp_uniform(U.group) * g.n + (2 * (int)warp_uniform(U.wtile) + (int)rank) * 128;
+      };
+      auto prefetch = [&]() {
+        if (pu >= n_units) return;
+        if (ps == 0) prow = weight_row(get_unit<kPairRows, RAGGED>(g, groups, wpairs, pu));
+        if (elect_one()) tma_prefetch_2d(&p.tmap_w, ps * 128, prow);
+        __syncwarp();
+        if (++ps == p.kb) ps = 0, pu += du;
+      };
+      for (int j = 0; j < kPrefetch; ++j) prefetch();
+      if (g.a_is_new) pdl_wait();
       for (int u = u0; u < n_units && ok; u += du) {
         const Unit U = get_unit<kPairRows, RAGGED>(g, groups, wpairs, u);
-        const int rows = (int)warp_uniform(U.rows);
+        const int rows = min(max((int)warp_uniform(U.rows) - 128 * (int)rank, 0), 128);
         const int first = (int)warp_uniform(U.first) + 128 * (int)rank;
-        const int wrow = (int)warp_uniform(U.group) * g.n + (int)warp_uniform(U.wtile) * 256 + (int)rank * 64;
-        const int boxes = cdiv(min(max(rows - 128 * (int)rank, 0), 128), kPairBox);
-        const int all_boxes = cdiv(min(rows, 128), kPairBox) + cdiv(max(rows - 128, 0), kPairBox);
-        const uint32_t bytes = 2 * kWStage + all_boxes * kPairBox * 128;
+        const int wrow = weight_row(U);
+        const int boxes = cdiv(rows, kPairBox);
         for (int s = 0; s < p.kb; ++s, ++i) {
           const uint32_t slot = i % kPairSlots;
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ((i / kPairSlots) & 1) ^ 1, ab, 131));
+          ok = __all_sync(0xffffffffu, wait(&empty[slot], ((i / kPairSlots) & 1) ^ 1, ab, 131));
           if (!ok) break;
-          const uint32_t bar = full0 + 8 * slot;
           if (elect_one()) {
-            if (rank == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-            // of each block of 128 weight rows, which is N of one accumulator, a CTA holds half
-            tma_load_2d_pair(smem + slot * kWStage, &p.tmap_w, s * 128, wrow, bar);
-            tma_load_2d_pair(smem + slot * kWStage + kWStage / 2, &p.tmap_w, s * 128, wrow + 128, bar);
-            if (boxes > 0) tma_load_2d_pair(s_a + slot * kPairAStage, &p.tmap_a, s * 128, first, bar);
+            mbar_arrive_expect_tx(&full[slot], kPairWStage + boxes * kPairBox * 128);
+            tma_load_2d_both(smem + slot * kPairWStage + rank * kWStage, &p.tmap_w, s * 128, wrow, &full[slot]);
+            if (boxes > 0) tma_load_2d(s_a + slot * kPairAStage, &p.tmap_a, s * 128, first, &full[slot]);
             if (boxes > 1)
-              tma_load_2d_pair(s_a + slot * kPairAStage + kPairBox * 128, &p.tmap_a, s * 128, first + kPairBox, bar);
+              tma_load_2d(s_a + slot * kPairAStage + kPairBox * 128, &p.tmap_a, s * 128, first + kPairBox, &full[slot]);
           }
           __syncwarp();
+          prefetch();
         }
       }
       if (ab.raised() && lane == 0) {
-        // copies already issued land before the CTA's shared memory goes away:
-        // their barrier may be the other CTA's, so give them a fixed time
+        // copies already issued, the other CTA's too, land before the shared memory goes away:
+        // give them a fixed time
         const unsigned long long t0 = globaltimer();
         while (globaltimer() - t0 < 2000000ull) {
         }
       }
       __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp & 1) {
       // -------------------------------------------- matrix instructions
-      if (rank == 0) {
-        const uint32_t w_desc = desc_lo(smem_u32(smem)), a_desc = desc_lo(smem_u32(s_a));
-        constexpr uint32_t idesc = idesc_fp8(256, 128);
-        // Every unit has kb stages, so units do not show here.  The loop is unrolled over the ring, so
-        // that slots and accumulators are constants, and each barrier is looked at while the
-        // instructions before those that wait for it issue: otherwise a stage takes longer to
-        // issue (1300 cycles) than its products to run.
-        int left = u0 < n_units ? ((n_units - 1 - u0) / du + 1) * p.kb : 0;
-        uint32_t phase = 0, acc_phase = 1;
-        bool ok = left > 0, full_seen = false, acc_seen = false;
-        while (ok) {
+      // Warp 1 issues the even stages, warp 3 the odd ones: between waits, votes and the fetching of
+      // its code a warp takes some 800 cycles to issue a stage's eight, longer than they take to
+      // run.  Every unit has kb stages, so units do not show here.
+      const int w = warp >> 1;
+      const uint32_t w_desc = desc_lo(smem_u32(smem)), a_desc = desc_lo(smem_u32(s_a));
+      const uint32_t d = tmem + 256 * w;
+      constexpr uint32_t idesc = idesc_fp8(128, 128);
+      const int total = u0 < n_units ? ((n_units - 1 - u0) / du + 1) * p.kb : 0;
+      uint32_t slot = w, phase = 0, acc_phase = 1;
+      for (int i = w; i < total; i += 2) {
+        // (the accumulator first: it is free once the stage before the last is promoted, and with it the
+        // stage before has run, so that the slot's barrier is not two phases behind, where it would
+        // look complete)
+        if (!__all_sync(0xffffffffu, wait(&empty_acc[2 * w], acc_phase, ab, 132))) break;
+        if (!__all_sync(0xffffffffu, wait(&full[slot], phase, ab, 133))) break;
+        tc_fence_after();
+        const bool look = mbar_test(&empty_acc[2 * w + 1], acc_phase);
+        const uint32_t wd = w_desc + slot * (kPairWStage / 16), ad = a_desc + slot * (kPairAStage / 16);
+        if (elect_one()) {
 #pragma unroll
-          for (int slot = 0; slot < kPairSlots; ++slot) {
-            constexpr int kHalf = kWStage / 32;
-            const uint32_t wd = w_desc + slot * (kWStage / 16), ad = a_desc + slot * (kPairAStage / 16);
-            const int acc = 2 * (slot & 1), next = (slot + 1) % kPairSlots;
-            if (!full_seen) ok = wait_spin(&full[slot], phase, ab, 133);
-            if (!acc_seen) ok = ok && wait_spin(&empty_acc[acc], acc_phase, ab, 132);
-            if (!ok) break;
-            tc_fence_after();
-            const bool look1 = mbar_test(&empty_acc[acc + 1], acc_phase);
-            if (elect_one()) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma_fp8<2>(acc * 128, ad + 2 * j, wd + 2 * j, idesc, j > 0);
-              mma_commit_pair(&full_acc[acc]);
-            }
-            if (!__all_sync(0xffffffffu, look1)) {
-              ok = wait_spin(&empty_acc[acc + 1], acc_phase, ab, 132);
-              if (!ok) break;
-            }
-            tc_fence_after();
-            if (slot & 1) acc_phase ^= 1;
-            const bool look_full = mbar_test(&full[next], next == 0 ? phase ^ 1 : phase);
-            const bool look_acc = mbar_test(&empty_acc[2 * (next & 1)], acc_phase);
-            if (elect_one()) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma_fp8<2>((acc + 1) * 128, ad + 2 * j, wd + kHalf + 2 * j, idesc, j > 0);
-              mma_commit_pair(&full_acc[acc + 1]);
-              mma_commit_pair(&empty[slot]);
-            }
-            full_seen = __all_sync(0xffffffffu, look_full);
-            acc_seen = __all_sync(0xffffffffu, look_acc);
-            if (--left == 0) {
-              ok = false;
-              break;
-            }
-          }
-          phase ^= 1;
+          for (int j = 0; j < 4; ++j) mma_fp8<1>(d, ad + 2 * j, wd + 2 * j, idesc, j > 0);
+          mma_commit(&full_acc[2 * w]);
         }
-        // drain: every instruction issued has completed
-        if (elect_one()) mma_commit_pair(drain);
-        const unsigned long long t0 = globaltimer();
-        while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
+        if (!__all_sync(0xffffffffu, look) && !__all_sync(0xffffffffu, wait(&empty_acc[2 * w + 1], acc_phase, ab, 132))) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_fp8<1>(d + 128, ad + 2 * j, wd + kWStage / 16 + 2 * j, idesc, j > 0);
+          mma_commit(&full_acc[2 * w + 1]);
+          mma_commit_both(&empty[slot]);
         }
         __syncwarp();
+        slot += 2;
+        if (slot >= kPairSlots) slot -= kPairSlots, phase ^= 1;
+        acc_phase ^= 1;
       }
+      // drain: every instruction issued has completed
+      if (elect_one()) mma_commit(drain);
+      const unsigned long long t0 = globaltimer();
+      while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+      __syncwarp();
     } else {
       // --- units and scales for the promoting warps, ahead of them (their registers are all taken, and
       // what they look up themselves holds up their sums); rows past the last group are zero
       if (g.a_is_new) pdl_wait();
-      const int j = threadIdx.x - 64;
       uint32_t i = 0, n = 0;
       bool ok = true;
       for (int u = u0; u < n_units && ok; u += du, ++n) {
         const Unit U = get_unit<kPairRows, RAGGED>(g, groups, wpairs, u);
         const uint32_t b = n % kAhead;
-        if (warp == 2) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty_unit[b], ((n / kAhead) & 1) ^ 1, ab, 135));
-          if (!ok) break;
-          if (lane == 0) {
-            s_unit[b] = make_int4(U.group, U.wtile, U.first, U.rows);
-            mbar_arrive(&full_unit[b]);
-          }
-          __syncwarp();
+        ok = __all_sync(0xffffffffu, wait(&empty_unit[b], ((n / kAhead) & 1) ^ 1, ab, 135));
+        if (!ok) break;
+        if (lane == 0) {
+          s_unit[b] = make_int4(U.group, U.wtile, U.first, U.rows);
+          mbar_arrive(&full_unit[b]);
         }
-        const int r0 = 128 * (int)rank + j, r1 = r0 + 64;
-        const float* sa0 = p.a_scales + (int64_t)(U.first + min(r0, U.rows - 1)) * p.kb;
-        const float* sa1 = p.a_scales + (int64_t)(U.first + min(r1, U.rows - 1)) * p.kb;
+        __syncwarp();
+        const float* sa[4];  // rows lane, lane + 32, ...
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sa[j] = p.a_scales + (int64_t)(U.first + min(128 * (int)rank + 32 * j + lane, U.rows - 1)) * p.kb;
         const float* sw0 = p.w_scales + ((int64_t)U.group * wtiles + 2 * U.wtile) * p.kb;
         const float* sw1 = 2 * U.wtile + 1 < wtiles ? sw0 + p.kb : sw0;
-        float4 now0 = load_scales(p, sa0, 0, true), now1 = load_scales(p, sa1, 0, true);
-        float4 next0 = now0, next1 = now1;
-        float w0 = 0.f, w1 = 0.f;
-        for (int s = 0; s < p.kb; ++s, ++i) {
-          if ((s & 31) == 0 && s + lane < p.kb) w0 = __ldg(sw0 + s + lane), w1 = __ldg(sw1 + s + lane);
-          if ((s & 3) == 0) {
-            if (s > 0) now0 = next0, now1 = next1;
-            next0 = load_scales(p, sa0, s + 4, true), next1 = load_scales(p, sa1, s + 4, true);
-          }
-          const float a0 = (s & 3) == 0 ? now0.x : (s & 3) == 1 ? now0.y : (s & 3) == 2 ? now0.z : now0.w;
-          const float a1 = (s & 3) == 0 ? now1.x : (s & 3) == 1 ? now1.y : (s & 3) == 2 ? now1.z : now1.w;
-          const float v0 = __shfl_sync(0xffffffffu, w0, s & 31), v1 = __shfl_sync(0xffffffffu, w1, s & 31);
-          // The stage before the last on these barriers is complete: so its products were issued,
-          // after the promoters had let go of the stage two further back, whose scales lie where
-          // this stage's go.
-          if (i >= 2) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&full_acc[2 * (i & 1)], ((i >> 1) & 1) ^ 1, ab, 137) &&
-                                             mbar_wait(&full_acc[2 * (i & 1) + 1], ((i >> 1) & 1) ^ 1, ab, 137));
-            if (!ok) break;
-          }
-          float* to = s_scale + (i % kScaleDepth) * 256 + j;
-          to[0] = a0 * v0;
-          to[64] = a1 * v0;
-          to[128] = a0 * v1;
-          to[192] = a1 * v1;
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full_acc[2 * (i & 1)]);
-            mbar_arrive(&full_acc[2 * (i & 1) + 1]);
-          }
+        // four stages at a time, loaded eight stages ahead
+        float4 next[2][4], w[2];
+        auto load = [&](int s, int d) {
+          if (lane < 2) w[d] = load_scales(lane == 0 ? sw0 : sw1, s, p.kb, p.w_vec);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) next[d][j] = load_scales(sa[j], s, p.kb, p.a_vec);
+        };
+        load(0, 0);
+        load(4, 1);
+        for (int s = 0; s < p.kb && ok; s += 8) {
+#pragma unroll
+          for (int d = 0; d < 2; ++d)
+            if (s + 4 * d < p.kb && ok) {
+              const uint32_t q = i & 1;
+              ok = __all_sync(0xffffffffu, wait(&empty_scale[q], ((i >> 1) & 1) ^ 1, ab, 137));
+              if (ok) {
+                float4* to = reinterpret_cast<float4*>(s_scale + q * kScaleQuad) + lane;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) to[32 * j] = next[d][j];
+                if (lane < 2) to[128] = w[d];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full_scale[q]);
+                load(s + 4 * d + 8, d);
+              }
+              ++i;
+            }
         }
       }
-      if (RAGGED && !g.out_rows) clear_tail(g, groups.first[g.groups], threadIdx.x - 64);
+      if (RAGGED && !g.out_rows) clear_tail<32>(g, groups.first[g.groups], lane);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsPromote));
     // ------------------------------------------- promotion and epilogue
     if (g.a_is_new) pdl_wait();  // (the output's last readers)
     const int q4 = warp & 3, half = (warp - 4) >> 2;
     const int r = 128 * (int)rank + 32 * q4 + lane;
     const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + 128 * half;
     uint64_t* mine_acc = full_acc + half;  // this warp's two accumulators: 2 apart
-    const uint32_t done = map_rank(empty_acc + half, 0);
-    const float* scales = s_scale + 128 * half + 32 * q4 + lane;
-    uint32_t i = 0, n = 0;
+    uint64_t* done = empty_acc + half;
+    uint8_t* stage = smem + kPairOffStage + (warp - 4) * kOutTile;
+    const float4* scales = reinterpret_cast<const float4*>(s_scale);
+    uint32_t i = 0, n = 0, quad = 0;
     bool ok = true;
     for (int u = u0; u < n_units && ok; u += du, ++n) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&full_unit[n % kAhead], (n / kAhead) & 1, ab, 136));
+      ok = __all_sync(0xffffffffu,  wait(&full_unit[n % kAhead], (n / kAhead) & 1, ab, 136));
       if (!ok) break;
       const int4 U = s_unit[n % kAhead];  // group, weight unit, first row, rows
       __syncwarp();
@@ -277,51 +274,107 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       const int col = U.y * 256 + 128 * half;
       if (r - lane >= U.w || col >= g.n) {  // nothing of this warp's
         for (int s = 0; s < p.kb && ok; ++s, ++i) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&mine_acc[2 * (i & 1)], (i >> 1) & 1, ab, 134));
-          if (ok && lane == 0) mbar_arrive_cluster(done + 16 * (i & 1));
+          if ((s & 3) == 0) {
+            ok = __all_sync(0xffffffffu,  wait(&full_scale[quad & 1], (quad >> 1) & 1, ab, 138));
+            if (ok && lane == 0) mbar_arrive(&empty_scale[quad & 1]);
+            ++quad;
+          }
+          ok = ok && __all_sync(0xffffffffu,  wait(&mine_acc[2 * (i & 1)], (i >> 1) & 1, ab, 134));
+          if (ok && lane == 0) mbar_arrive(&done[2 * (i & 1)]);
         }
         continue;
       }
-      const bool live = r < U.w;
+      const int to = output_row(g, U.z + r, r < U.w);
       float2 acc[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
       bool seen = false;  // the block's accumulator was seen complete during the block before
       // (one way out of the loop: with a second the compiler copies the sums every time round; once a
       // wait has run out, the others return at once and nothing is stored)
+      float4 four = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int s = 0; s < p.kb; ++s, ++i) {
-        if (!seen) ok = wait_spin(&mine_acc[2 * (i & 1)], (i >> 1) & 1, ab, 134) && ok;
+        if ((s & 3) == 0) {
+          ok = __all_sync(0xffffffffu, wait(&full_scale[quad & 1], (quad >> 1) & 1, ab, 138)) && ok;
+          four = scales[(quad & 1) * (kScaleQuad / 4) + 32 * q4 + lane];
+          const float4 w = scales[(quad & 1) * (kScaleQuad / 4) + 128 + half];
+          four = make_float4(four.x * w.x, four.y * w.y, four.z * w.z, four.w * w.w);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty_scale[quad & 1]);
+          ++quad;
+        }
+        const float scale = four.x;
+        four = make_float4(four.y, four.z, four.w, 0.f);
+        if (!seen) ok = __all_sync(0xffffffffu, wait(&mine_acc[2 * (i & 1)], (i >> 1) & 1, ab, 134)) && ok;
         tc_fence_after();
         const uint32_t at = taddr + 256 * (i & 1);
-        const float scale = scales[(i % kScaleDepth) * 256];
         bool look = false;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t t[32];
-          tmem_ld32(at + 32 * c, t);
+        for (int c = 0; c < 8; ++c) {
+          uint32_t t[16];
+          tmem_ld16(at + 16 * c, t);
           tmem_ld_wait();
-          if (c == 3) {
+          if (c == 7) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(done + 16 * (i & 1));
+            if (lane == 0) mbar_arrive(&done[2 * (i & 1)]);
             look = mbar_test(&mine_acc[2 * (~i & 1)], ((i + 1) >> 1) & 1);
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) fma2(acc[16 * c + e], t[2 * e], t[2 * e + 1], scale);
+          for (int e = 0; e < 8; ++e) fma2(acc[8 * c + e], t[2 * e], t[2 * e + 1], scale);
         }
         seen = __all_sync(0xffffffffu, look);
       }
-      if (!ok || !live) continue;
-      int to = U.z + r;
-      if (g.out_rows) to = __ldg(g.out_rows + to);
-      if (to >= 0 && to < g.out_rows_end) store_row<OUT>(g, (int64_t)to * g.out_stride, col, acc);
+      if (!ok) break;
+      if (OUT < 2 && g.vec) {
+        // Through shared memory.  Full tiles leave from there as boxes of 32 rows x 64, under the next
+        // unit: stores of all SMs at once take 4000 cycles to drain, and what the warp does next
+        // queues behind them.  Others (rows by an index, the end of a group) as 256 bytes of two
+        // rows a store.
+        const bool boxes = p.out_boxes && (__all_sync(0xffffffffu, to >= 0) || (!RAGGED && g.groups == 1));
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          *reinterpret_cast<uint4*>(stage + (c >> 3) * (kOutTile / 2) + lane * 128 + (((c ^ lane) & 7) << 4)) =
+              make_uint4(pack16<OUT & 1>(acc[4 * c]), pack16<OUT & 1>(acc[4 * c + 1]), pack16<OUT & 1>(acc[4 * c + 2]),
+                         pack16<OUT & 1>(acc[4 * c + 3]));
+        if (boxes) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&p.tmap_out, col, U.z + r, stage);
+            if (col + 64 < g.n) tma_store_2d(&p.tmap_out, col + 64, U.z + r, stage + kOutTile / 2);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          const int half8 = (lane >> 3) & 1;
+          uint16_t* out = reinterpret_cast<uint16_t*>(g.out) + col + 8 * (lane & 15);
+          const bool inside = col + 8 * (lane & 15) < g.n;
+          uint4 piece[16];
+          int o[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int row = 2 * c + (lane >> 4);
+            piece[c] = *reinterpret_cast<const uint4*>(stage + half8 * (kOutTile / 2) + row * 128 + (((row ^ lane) & 7) << 4));
+            o[c] = __shfl_sync(0xffffffffu, to, row);
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (o[c] >= 0 && inside) *reinterpret_cast<uint4*>(out + (int64_t)o[c] * g.out_stride) = piece[c];
+          __syncwarp();
+        }
+      } else {
+        store_rows<OUT>(g, to, col, acc, stage, lane);
+      }
     }
   }
 
+  if (warp >= 4 && lane == 0) bulk_wait();  // the boxes have left
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the pair's copies, products or signals may touch it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 template <int OUT, bool RAGGED>

@@ -27,6 +27,22 @@ __device__ __forceinline__ void mma_fp8(uint32_t d, uint32_t a, uint32_t b, uint
   else FP8_MMA("2");
 #undef FP8_MMA
 }
+// A box into the same place of both CTAs' shared memory, each CTA's barrier counting its copy.
+__device__ __forceinline__ void tma_load_2d_both(void* dst, const CUtensorMap* tm, int c0, int r0, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
+      "%3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(tm), "r"(c0), "r"(r0), "r"(smem_u32(bar)), "h"((uint16_t)3)
+      : "memory");
+}
+// Arrive once on `bar` in both CTAs when every instruction this thread issued so far completes.
+__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -43,40 +59,70 @@ __device__ __forceinline__ void fma2(float2& acc, uint32_t a, uint32_t b, float 
   acc = __ffma2_rn(make_float2(__uint_as_float(a), __uint_as_float(b)), make_float2(s, s), acc);
 }
 
-// A lane's scales of activation row `row`, four blocks at a time.
-__device__ __forceinline__ float4 load_scales(const Fp8GemmParams& p, const float* row, int b, bool live) {
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (live && b < p.kb) {
-    if (p.a_vec) return *reinterpret_cast<const float4*>(row + b);
-    v.x = row[b];
-    if (b + 1 < p.kb) v.y = row[b + 1];
-    if (b + 2 < p.kb) v.z = row[b + 2];
-    if (b + 3 < p.kb) v.w = row[b + 3];
-  }
-  return v;
+// Four neighbouring scales of a row of kb, from block b on (0 past the last).
+__device__ __forceinline__ float4 load_scales(const float* row, int b, int kb, bool vec) {
+  if (vec && b < kb) return __ldg(reinterpret_cast<const float4*>(row + b));
+  return make_float4(b < kb ? __ldg(row + b) : 0.f, b + 1 < kb ? __ldg(row + b + 1) : 0.f,
+                     b + 2 < kb ? __ldg(row + b + 2) : 0.f, b + 3 < kb ? __ldg(row + b + 3) : 0.f);
 }
 
-// Columns [n, n + 2 C) of a row from registers.
+constexpr int kStagePiece = 32 * 64;  // bytes a warp stages at a time: 64 of each of 32 rows
+
+// Columns [n, n + 2 C) of 32 rows, a lane's in v, to rows `to` of the output (-1: none).  In
+// 16-byte pieces they go through the warp's staging area, 64 bytes of a row at a time
+// (pieces swizzled by the row), so that four neighbouring lanes write 64 bytes of one row: a
+// lane writing its own row touches 32 lines an instruction (4096 cycles for a unit of
+// 256 x 256, during which the tensor core runs out of accumulators).
 template <int OUT, int C>
-__device__ __forceinline__ void store_row(const Fp4GemmParams& g, int64_t at, int n, const float2 (&v)[C]) {
-  if (OUT < 2 && g.vec && n + 2 * C <= g.n) {
-    uint16_t* out = reinterpret_cast<uint16_t*>(g.out) + at + n;
+__device__ __forceinline__ void store_rows(const Fp4GemmParams& g, int to, int n, const float2 (&v)[C], uint8_t* stage,
+                                           int lane) {
+  if (g.vec) {
+    constexpr int kCols = OUT == 2 ? 16 : 32;  // of a piece
+    uint8_t* mine = stage + lane * 64;
+    const int key = (lane >> 1) & 3;
+    const uint8_t* from = stage + (lane >> 2) * 64;
 #pragma unroll
-    for (int i = 0; i < C / 4; ++i)
-      reinterpret_cast<uint4*>(out)[i] = make_uint4(pack16<OUT & 1>(v[4 * i]), pack16<OUT & 1>(v[4 * i + 1]),
-                                                    pack16<OUT & 1>(v[4 * i + 2]), pack16<OUT & 1>(v[4 * i + 3]));
-  } else if (OUT == 2 && g.vec && n + 2 * C <= g.n) {
-    float* out = reinterpret_cast<float*>(g.out) + at + n;
+    for (int c = 0; c < 2 * C / kCols; ++c) {
 #pragma unroll
-    for (int i = 0; i < C / 2; ++i)
-      reinterpret_cast<float4*>(out)[i] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
-  } else {
+      for (int i = 0; i < 4; ++i) {
+        uint4 w;
+        if constexpr (OUT == 2) {
+          const float2 x = v[8 * c + 2 * i], y = v[8 * c + 2 * i + 1];
+          w = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+        } else {
+          const float2* x = v + 16 * c + 4 * i;
+          w = make_uint4(pack16<OUT>(x[0]), pack16<OUT>(x[1]), pack16<OUT>(x[2]), pack16<OUT>(x[3]));
+        }
+        *reinterpret_cast<uint4*>(mine + ((i ^ key) << 4)) = w;
+      }
+      __syncwarp();
+      const int col = n + kCols * c + (kCols / 4) * (lane & 3);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2);
+        const int o = __shfl_sync(0xffffffffu, to, row);
+        const uint4 w = *reinterpret_cast<const uint4*>(from + 512 * i + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+        if (o >= 0 && col < g.n)
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(g.out) + ((int64_t)o * g.out_stride + col) * (OUT == 2 ? 4 : 2)) = w;
+      }
+      __syncwarp();
+    }
+  } else if (to >= 0) {
+    const int64_t at = (int64_t)to * g.out_stride;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       if (n + 2 * i < g.n) store_out(g, at + n + 2 * i, v[i].x);
       if (n + 2 * i + 1 < g.n) store_out(g, at + n + 2 * i + 1, v[i].y);
     }
   }
+}
+
+// Output row of operand row `at`, -1 where it is dropped.
+__device__ __forceinline__ int output_row(const Fp4GemmParams& g, int at, bool live) {
+  if (!live) return -1;
+  if (!g.out_rows) return at;
+  const int to = __ldg(g.out_rows + at);
+  return to < g.out_rows_end ? to : -1;
 }
 
 // Calls f with the output's type and whether the rows are grouped as compile-time values.

@@ -9,31 +9,35 @@
 //
 // A warp takes a token: lane l holds up to V neighbouring experts in registers, a power of
 // two of lanes to a group, so that lanes in order are experts in order and a tie's lowest
-// index is the lowest lane.  A choice is one redux over order-preserving integer keys and
-// one ballot.
+// index is the lowest lane.  A lane sorts its experts once; a choice is then one redux over
+// the lanes' first keys (integers of the floats' order) and one ballot.
 //
 // The order is that of the real numbers c, not of their roundings: scores differ by less
 // than fp32 resolves about once in a thousand tokens, and another order there would send
 // a token to another expert.  Without a bias the logits' own order decides (scores are
-// monotone).  With one, neighbours in the order (and the last group taken and the first
-// left) closer than fp32's error have their row done again in 64 bits, unless their
-// logits and biases are equal, which is a true tie.
+// monotone).  With one, where neighbours in the order are closer than fp32's error, the
+// chosen and the next are compared again in 64 bits, a lane each; where the last group taken
+// and the first left are, or a third comes close, the row is done again in 64 bits.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
 #include "b4moe.h"
-#include "ptx.cuh"
+#include "fp4_quant.cuh"
 
 namespace b4 {
 void set_last_error(const char* fmt, ...);
 b4_status require_device(int* sms);
 
 namespace {
+
+using fp4q::exp2_approx;
+using fp4q::rcp_approx;
 
 struct RouteParams {
   const void* logits;
@@ -43,7 +47,7 @@ struct RouteParams {
   int m, experts, top_k;
   int groups, top_groups, group_top;
   int per, lanes_log2, each;  // experts of a group, lanes of a group, experts of a lane
-  int vec;                    // a lane's logits are one aligned piece
+  int vec, bias_vec;          // a lane's logits, its biases are one aligned piece
   int softmax, renorm;
   float scale;
   int32_t* ids;
@@ -82,6 +86,10 @@ __device__ __forceinline__ R sigmoid(R z) {
   return (z >= R(0) ? R(1) : e) / (R(1) + e);
 }
 
+// For the order alone: the machine's exponential and reciprocal (2^-22 each), far cheaper.
+__device__ __forceinline__ float exp_order(float x) { return exp2_approx(1.44269504f * x); }
+__device__ __forceinline__ float sigmoid_order(float z) { return rcp_approx(1.f + exp_order(-z)); }
+
 // A logit as it counts: a NaN does not.
 template <typename T>
 __device__ __forceinline__ float logit(const T* row, int e) {
@@ -90,9 +98,9 @@ __device__ __forceinline__ float logit(const T* row, int e) {
 }
 
 template <int V, typename T>
-__device__ __forceinline__ void load_logits(const RouteParams& p, const T* row, int first, int count, float (&z)[V]) {
+__device__ __forceinline__ void load_logits(const RouteParams& p, const T* row, int first, int count, int vec, float (&z)[V]) {
   constexpr int kBytes = V * (int)sizeof(T);
-  if (kBytes >= 4 && p.vec) {
+  if (kBytes >= 4 && vec) {
     T raw[V];
     if (count > 0) {
       if constexpr (kBytes >= 16) {
@@ -141,39 +149,49 @@ __device__ __forceinline__ int group_rank(const RouteParams& p, R value, int gro
   return rank;
 }
 
+// 64-bit values as integers of the same order.
+__device__ __forceinline__ long long key64(double c) {
+  const long long b = __double_as_longlong(c + 0.0);
+  return b ^ ((b >> 63) & 0x7fffffffffffffffll);
+}
+constexpr long long kNone64 = LLONG_MIN + 0xfffffffffffffll;  // the key of -inf
+__device__ __forceinline__ long long warp_max(long long v) {
+  for (int o = 16; o > 0; o >>= 1) {
+    const long long x = __shfl_xor_sync(kAll, v, o);
+    v = x > v ? x : v;
+  }
+  return v;
+}
+
 // The row's choice in 64 bits: expert j of the order in lane j, -1 past the last.
 template <int V, typename T>
 __device__ __noinline__ int choose64(const RouteParams& p, const T* row, int lane) {
   const int group = lane >> p.lanes_log2, at = (lane & ((1 << p.lanes_log2) - 1)) * p.each;
   const int count = group < p.groups ? max(min(p.each, p.per - at), 0) : 0, first = group * p.per + at;
-  double c[V];
-  double top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    c[i] = i < count ? (double)logit(row, first + i) : -INFINITY;
-    top = fmax(top, c[i]);
-  }
-  double sum = 1.0;
+  double top = -INFINITY, sum = 1.0;
   if (p.softmax) {
-    for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, o));
+    float t = -INFINITY;
+    for (int i = 0; i < count; ++i) t = fmaxf(t, logit(row, first + i));
+    top = warp_max(t);
     sum = 0.0;
 #pragma unroll 1
-    for (int i = 0; i < V; ++i)
-      if (c[i] > -INFINITY) sum += exp_below(c[i], top);
+    for (int i = 0; i < count; ++i) {
+      const double z = logit(row, first + i);
+      if (z > -INFINITY) sum += exp_below(z, top);
+    }
     sum = warp_sum(sum);
   }
+  long long key[V];
   double a = -INFINITY, b = -INFINITY;  // the lane's largest two
 #pragma unroll 1
   for (int i = 0; i < V; ++i) {
-    if (c[i] > -INFINITY) {
-      const double z = c[i];
-      const double s = p.softmax ? exp_below(z, top) / sum : sigmoid(z);
-      const float bias = p.bias ? __ldg(p.bias + first + i) : 0.f;
-      const double v = bias > -INFINITY ? s + (double)bias : -INFINITY;
-      c[i] = p.bias ? v : z;
-      b = fmax(b, fmin(a, v));
-      a = fmax(a, v);
-    }
+    const double z = i < count ? (double)logit(row, first + i) : -INFINITY;
+    const float bias = p.bias && i < count ? __ldg(p.bias + first + i) : 0.f;
+    double v = -INFINITY;
+    if (z > -INFINITY && bias > -INFINITY) v = (p.softmax ? exp_below(z, top) / sum : sigmoid(z)) + (double)bias;
+    key[i] = key64(p.bias ? v : z);
+    b = fmax(b, fmin(a, v));
+    a = fmax(a, v);
   }
   bool keep = true;
   if (p.groups > 1) {
@@ -184,28 +202,47 @@ __device__ __noinline__ int choose64(const RouteParams& p, const T* row, int lan
   }
   int chosen = -1;
   for (int j = 0; j < p.top_k; ++j) {
-    double best = -INFINITY;
+    long long best = kNone64;
     int pos = 0;
-    if (keep)
-      for (int i = 0; i < V; ++i)
-        if (c[i] > best) best = c[i], pos = i;
-    double all = best;
-    for (int o = 16; o > 0; o >>= 1) all = fmax(all, __shfl_xor_sync(kAll, all, o));
-    if (!(all > -INFINITY)) break;
+    for (int i = 0; i < V; ++i)
+      if (keep && key[i] > best) best = key[i], pos = i;
+    const long long all = warp_max(best);
+    if (all <= kNone64) break;
     const int owner = __ffs(__ballot_sync(kAll, best == all)) - 1;
     const int e = __shfl_sync(kAll, first + pos, owner);
     if (lane == j) chosen = e;
-    if (lane == owner) c[pos] = -INFINITY;
+    if (lane == owner) key[pos] = kNone64;
   }
   return chosen;
 }
 
 // Whether two values of the order may stand the other way round: the sum of what their
-// fp32 forms can be off by.  A score is at most 1 and off by 2^-21 (its exponential one ulp of
-// an argument off by 2^-24 |z - top|, the sum of exponentials and the quotient another
-// three); the sum with the bias adds 2^-24 of itself.
-__device__ __forceinline__ bool close_(float a, float b, float terms) {
-  return a - b <= terms * (0x1p-20f + 0x1p-23f * fabsf(a));
+// fp32 forms can be off by.  A score is at most `most` (1, or the largest of a softmax) and off by
+// 2^-21 of that (its exponential 2^-22 and an argument off by 2^-24 |z|, which a score of at
+// most e^-|z| makes small; the sum of exponentials and the quotient another three roundings);
+// the sum with the bias adds 2^-24 of itself.
+__device__ __forceinline__ bool close_(float a, float b, float terms, float most) {
+  return a - b <= terms * (0x1p-20f * most + 0x1p-23f * fabsf(a));
+}
+
+// A lane's experts, sorted: keys descending, equal ones by index.  (An odd-even merge network.)
+template <int V>
+__device__ __forceinline__ void sort_keys(int (&key)[V], int (&pos)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const int a = i + j, b = i + j + k;
+            const bool swap = key[b] > key[a] || (key[b] == key[a] && pos[b] < pos[a]);
+            const int ka = key[a], pa = pos[a];
+            key[a] = swap ? key[b] : ka, pos[a] = swap ? pos[b] : pa;
+            key[b] = swap ? ka : key[b], pos[b] = swap ? pa : pos[b];
+          }
 }
 
 template <int V, typename T>
@@ -226,10 +263,10 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const __grid_constant__
   const int count = group < p.groups ? max(min(p.each, p.per - at), 0) : 0, first = group * p.per + at;
 
   float z[V];
-  load_logits<V>(p, row, first, count, z);
+  load_logits<V>(p, row, first, count, p.vec, z);
   // softmax over all experts, where more than its order is needed
   const bool scores = p.bias || (p.groups > 1 && p.group_top == 2);
-  float top = 0.f, inv = 1.f;
+  float top = 0.f, inv = 1.f;  // (1 / the sum: the largest of the softmax)
   if (p.softmax && (scores || !p.renorm)) {
     float t = z[0];
 #pragma unroll
@@ -240,21 +277,26 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const __grid_constant__
     for (int i = 0; i < V; ++i) sum += z[i] > -INFINITY ? exp_below(z[i], top) : 0.f;
     inv = 1.f / warp_sum(sum);
   }
-  int key[V];
+  int key[V], pos[V];
   float a = -INFINITY, b = -INFINITY;
+  if (scores) {
+    float bias[V];
+    if (p.bias) load_logits<V>(p, p.bias, first, count, p.bias_vec, bias);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float c = z[i];
-    if (scores && c > -INFINITY) {
-      c = p.softmax ? exp_below(c, top) * inv : sigmoid(c);
-      if (p.bias) {
-        const float bias = __ldg(p.bias + first + i);
-        c = bias > -INFINITY ? c + bias : -INFINITY;
-      }
+    for (int i = 0; i < V; ++i) {
+      float c = z[i];
+      if (c > -INFINITY) c = p.softmax ? (c == top ? 1.f : exp_order(c - top)) * inv : sigmoid_order(c);
+      if (p.bias) c = c > -INFINITY && bias[i] > -INFINITY ? c + bias[i] : -INFINITY;
+      key[i] = key_of(p.bias ? c : z[i]);
+      b = fmaxf(b, fminf(a, c));
+      a = fmaxf(a, c);
     }
-    key[i] = key_of(p.bias ? c : z[i]);
-    b = fmaxf(b, fminf(a, c));
-    a = fmaxf(a, c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      key[i] = key_of(z[i]);
+      a = fmaxf(a, z[i]);
+    }
   }
   bool again = false;  // fp32 does not decide
   if (p.groups > 1) {
@@ -265,36 +307,72 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const __grid_constant__
       const uint32_t in = __ballot_sync(kAll, rank == p.top_groups - 1 && group < p.groups);
       const uint32_t out = __ballot_sync(kAll, rank == p.top_groups && group < p.groups);
       const float last = __shfl_sync(kAll, value, __ffs(in) - 1), next = __shfl_sync(kAll, value, __ffs(out) - 1);
-      again = next > -INFINITY && close_(last, next, 4.f);
+      again = next > -INFINITY && close_(last, next, 4.f, inv);
     }
     if (rank >= p.top_groups || group >= p.groups) {
 #pragma unroll
       for (int i = 0; i < V; ++i) key[i] = kNone;
     }
   }
-  int chosen = -1, its_key = kNone;
-  const int rounds = p.bias ? p.top_k + 1 : p.top_k;  // with a bias the first left is looked at too
-  for (int j = 0; j < rounds; ++j) {
-    int best = key[0];
 #pragma unroll
-    for (int i = 1; i < V; ++i) best = max(best, key[i]);
-    const int all = warp_max(best);
-    if (all <= kNone) break;
-    const int owner = __ffs(__ballot_sync(kAll, best == all)) - 1;
-    int pos = 0;
+  for (int i = 0; i < V; ++i) pos[i] = i;
+  sort_keys<V>(key, pos);
+  int chosen = -1, its_key = kNone, next_key = kNone;
+  auto take = [&](int j) {  // the best that is left, into lane j
+    const int all = warp_max(key[0]);
+    const int owner = __ffs(__ballot_sync(kAll, key[0] == all)) - 1;
+    const int e = __shfl_sync(kAll, first + pos[0], owner);
+    if (lane == j && all > kNone) chosen = e, its_key = all;
+    const bool mine = lane == owner;
 #pragma unroll
-    for (int i = V - 1; i >= 0; --i) pos = key[i] == all ? i : pos;
-    const int e = __shfl_sync(kAll, first + pos, owner);
-    if (lane == owner) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = i == pos ? kNone : key[i];
+    for (int i = 0; i + 1 < V; ++i) key[i] = mine ? key[i + 1] : key[i], pos[i] = mine ? pos[i + 1] : pos[i];
+    if (mine) key[V - 1] = kNone;
+  };
+  for (int j = 0; j < p.top_k; ++j) take(j);
+  if (p.bias && !again) {
+    // neighbours of the order, the last chosen and the first left among them
+    next_key = warp_max(key[0]);
+    const int below = __shfl_down_sync(kAll, its_key, 1);
+    const int after = lane == p.top_k - 1 ? next_key : below;
+    bool tie = lane < p.top_k && after > kNone && close_(value_of(its_key), value_of(after), 2.f, inv);
+    if (__any_sync(kAll, tie)) {
+      const int owner = __ffs(__ballot_sync(kAll, key[0] == next_key)) - 1;
+      const int extra = next_key > kNone ? __shfl_sync(kAll, first + pos[0], owner) : -1;
+      // equal logits and biases are a true tie, which stands as it is
+      const int mine = lane < p.top_k ? chosen : extra;
+      const float zm = mine >= 0 ? logit(row, mine) : 0.f, bm = mine >= 0 ? __ldg(p.bias + mine) : 0.f;
+      const float zn = __shfl_down_sync(kAll, zm, 1), bn = __shfl_down_sync(kAll, bm, 1);
+      const float ze = extra >= 0 ? logit(row, extra) : 0.f, be = extra >= 0 ? __ldg(p.bias + extra) : 0.f;
+      const bool last_lane = lane == p.top_k - 1;
+      tie = tie && !(zm == (last_lane ? ze : zn) && bm == (last_lane ? be : bn));
     }
-    if (lane == j) chosen = e, its_key = all;
-    if (p.bias && j > 0 && !again) {
-      // neighbours j - 1 and j of the order
-      const int before = __shfl_sync(kAll, its_key, j - 1), e0 = __shfl_sync(kAll, chosen, j - 1);
-      if (close_(value_of(before), value_of(all), 2.f))
-        again = !(logit(row, e0) == logit(row, e) && __ldg(p.bias + e0) == __ldg(p.bias + e));
+    if (__any_sync(kAll, tie)) {
+      // one more, and who stands behind it; then, unless that one may belong among them too, only
+      // these in 64 bits (softmax needs the row's sum for it: the whole row)
+      const int owner = __ffs(__ballot_sync(kAll, key[0] == next_key)) - 1;
+      const int extra = next_key > kNone ? __shfl_sync(kAll, first + pos[0], owner) : -1;
+      if (p.top_k < 32) take(p.top_k);
+      const int third = warp_max(key[0]), last = __shfl_sync(kAll, its_key, p.top_k - 1);
+      if (p.softmax || p.top_k == 32 || (third > kNone && close_(value_of(last), value_of(third), 2.f, inv))) {
+        again = true;
+      } else {
+        const int n = p.top_k + (extra >= 0 ? 1 : 0);
+        double c = 0.0;
+        if (lane < n && chosen >= 0) c = sigmoid((double)logit(row, chosen)) + (double)__ldg(p.bias + chosen);
+        const long long k64 = lane < n && chosen >= 0 ? key64(c) : kNone64;
+        int rank = 0;
+        for (int j = 0; j < n; ++j) {
+          const long long o = __shfl_sync(kAll, k64, j);
+          const int oe = __shfl_sync(kAll, chosen, j);
+          rank += o > k64 || (o == k64 && oe < chosen);
+        }
+        int sorted = -1;
+        for (int j = 0; j < n; ++j) {
+          const int to = __shfl_sync(kAll, rank, j), e = __shfl_sync(kAll, chosen, j);
+          if (lane == to) sorted = e;
+        }
+        chosen = lane < p.top_k ? sorted : -1;
+      }
     }
   }
   if (again) chosen = choose64<V>(p, row, lane);
@@ -346,6 +424,7 @@ cudaError_t launch_each(RouteParams& p, int sms, cudaStream_t stream) {
   const int bytes = v * (int)sizeof(T), align = bytes < 16 ? bytes : 16;
   p.vec = p.each == v && p.per % v == 0 && reinterpret_cast<uintptr_t>(p.logits) % align == 0 &&
           p.stride * (int)sizeof(T) % align == 0;
+  p.bias_vec = p.each == v && p.per % v == 0 && reinterpret_cast<uintptr_t>(p.bias) % (v < 4 ? 4 * v : 16) == 0;
   switch (v) {
     case 1: return launch_route<1, T>(p, sms, stream);
     case 2: return launch_route<2, T>(p, sms, stream);
