@@ -756,6 +756,7 @@ class RouterConfig:
         self.m, self.num_experts, self.top_k, self.dtype = int(m), int(num_experts), int(top_k), dtype
         self.stride = int(stride) or self.num_experts
         self.routes = self.m * self.top_k
+        self._shape = (self.m, self.stride)  # of contiguous logits
         self._struct = _RouteConfig(self.m, self.num_experts, self.top_k, int(num_groups), int(top_groups),
                                     int(group_top), int(score), int(bool(renormalize)), DTYPES[dtype], float(scale),
                                     int(stride))
@@ -787,10 +788,11 @@ def route_topk(cfg: RouterConfig, logits, topk_ids, topk_weights, bias=None, num
         raise TypeError(f"logits must be {cfg.dtype}, got {logits.dtype}")
     handle = _launch_stream(stream, logits, "logits")
     shape = logits.shape
-    if len(shape) != 2 or shape[0] < cfg.m or shape[1] < cfg.num_experts:
-        raise ValueError(f"logits must be [{cfg.m}, {cfg.num_experts}], got {list(shape)}")
-    if cfg.m and (logits.stride(1) != 1 or (shape[0] > 1 and logits.stride(0) != cfg.stride)):
-        raise ValueError(f"logits rows must be contiguous and {cfg.stride} elements apart (stride)")
+    if shape != cfg._shape or not logits.is_contiguous():
+        if len(shape) != 2 or shape[0] < cfg.m or shape[1] < cfg.num_experts:
+            raise ValueError(f"logits must be [{cfg.m}, {cfg.num_experts}], got {list(shape)}")
+        if cfg.m and (logits.stride(1) != 1 or (shape[0] > 1 and logits.stride(0) != cfg.stride)):
+            raise ValueError(f"logits rows must be contiguous and {cfg.stride} elements apart (stride)")
     st = _lib.b4_route_topk(
         cfg._ref, logits.data_ptr(), bias if bias is None else _fp4_buffer(bias, _F32, cfg.num_experts, "bias"),
         num_tokens if num_tokens is None else _fp4_buffer(num_tokens, _I32, 1, "num_tokens"),
@@ -835,37 +837,52 @@ class Fp8Config:
         self._ref = ctypes.byref(self._struct)
         self._elements = (self.m * self.num_groups * self.x_stride, self.m * self.x_stride)  # of x: a stack's, ragged
         self._gather = (-1, None)
+        self._weights = _fp8_sizes(self.num_groups, self.n, self.k)
+        # (rows, codes, scales) of the quantised operand: a stack's, ragged
+        blocks = self.num_groups * -(-self.m // max(self.block_rows, 1))
+        self._operands = tuple((r, r * self.k, (r if self.block_rows == 1 else blocks) * self.blocks)
+                               for r in (self.m * self.num_groups, self.m))
 
     def rows(self, ragged):
-        return self.m if ragged else self.m * self.num_groups
-
-    def _scales(self, ragged):
-        """Scales of the quantised operand."""
-        rows = self.rows(ragged) if self.block_rows == 1 else self.num_groups * -(-self.m // self.block_rows)
-        return rows * self.blocks
+        return self._operands[ragged][0]
 
 
 def _fp8_codes(t, n, name):
     """Address of a contiguous tensor of at least n E4M3 codes, as torch's type or as bytes (None stays None)."""
+    if isinstance(t, _Tensor) and (t.dtype is E4M3 or t.dtype is _U8) and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
     if isinstance(t, _Tensor) and t.dtype is E4M3:
         t = t.view(_U8)
     return _fp4_buffer(t, _U8, n, name)
 
 
 def _fp8_weights(cfg, w_codes, w_scales):
-    e, n, k = cfg.num_groups, cfg.n, cfg.k
-    return _fp8_weight(w_codes, w_scales, e, n, k, "w_codes", "w_scales")
+    """Addresses of the config's weight matrices and of their scales."""
+    return _fp8_weight(w_codes, w_scales, cfg._weights, "w_codes", "w_scales")
 
 
-def _fp8_weight(codes, scales, e, n, k, name, scales_name):
-    """Addresses of e quantised [n, k] matrices and of their scales [e, ceil(n / 128), ceil(k / 128)]."""
-    cp = _fp8_codes(codes, e * n * k, name)
-    sp = _fp4_buffer(scales, _F32, e * -(-n // 128) * -(-k // 128), scales_name)
-    if cp is not None and codes.numel() != e * n * k and _wider(codes, k):
+def _fp8_weight(codes, scales, sizes, name, scales_name):
+    """Addresses of quantised matrices and of their scales: sizes are their codes, scales, codes of a row, scales of a
+    row."""
+    n, ns, k, kb = sizes
+    cp, sp = _fp8_codes(codes, n, name), _fp4_buffer(scales, _F32, ns, scales_name)
+    if cp is not None and codes.numel() != n and _wider(codes, k):
         raise ValueError(f"{name} has rows of {codes.shape[-1]} codes, the config rows of {k}")
-    if sp is not None and scales.numel() != e * -(-n // 128) * -(-k // 128) and _wider(scales, -(-k // 128)):
-        raise ValueError(f"{scales_name} has rows of {scales.shape[-1]} scales, the config rows of {-(-k // 128)}")
+    if sp is not None and scales.numel() != ns and _wider(scales, kb):
+        raise ValueError(f"{scales_name} has rows of {scales.shape[-1]} scales, the config rows of {kb}")
     return cp, sp
+
+
+def _fp8_sizes(e, n, k):
+    """Of e quantised [n, k] matrices with scales [e, ceil(n / 128), ceil(k / 128)]."""
+    kb = -(-k // 128)
+    return e * n * k, e * -(-n // 128) * kb, k, kb
+
+
+@functools.lru_cache(maxsize=64)
+def _fp8_layer_sizes(e, h, i, activation):
+    """The sizes of W13 and of W2."""
+    return _fp8_sizes(e, i if activation == RELU2 else 2 * i, h), _fp8_sizes(e, h, i)
 
 
 def _fp8_x(cfg, x, rows, ragged):
@@ -886,13 +903,13 @@ def fp8_quantize(cfg: Fp8Config, x, codes, scales, values=None, rows=None, offse
     x: rows of the config's width, x_stride elements apart, or a contiguous tensor of any shape that holds exactly the
     config's elements.  ``rows`` gathers from x's rows (entries that name none give zero rows)."""
     ragged = offsets is not None
-    n = cfg.rows(ragged)
+    n, n_codes, n_scales = cfg._operands[ragged]
     handle = _launch_stream(stream, x, "x")
     st = _lib.b4_fp8_quantize(
         _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _fp4_buffer(rows, _I32, n, "rows"),
         _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None,
-        _fp8_codes(codes, n * cfg.k, "codes"), _fp4_buffer(scales, _F32, cfg._scales(ragged), "scales"),
-        values if values is None else _fp4_buffer(values, cfg.x_dtype, n * cfg.k, "values"), handle)
+        _fp8_codes(codes, n_codes, "codes"), _fp4_buffer(scales, _F32, n_scales, "scales"),
+        values if values is None else _fp4_buffer(values, cfg.x_dtype, n_codes, "values"), handle)
     if st:
         _check(st)
 
@@ -900,11 +917,11 @@ def fp8_quantize(cfg: Fp8Config, x, codes, scales, values=None, rows=None, offse
 def fp8_matmul(cfg: Fp8Config, a_codes, a_scales, w_codes, w_scales, out, offsets=None, out_rows=None,
                device_status=None, stream=None):
     """Enqueue the product of two quantised operands (``b4_fp8_matmul``)."""
-    n = cfg.rows(offsets is not None)
+    n, n_codes, n_scales = cfg._operands[offsets is not None]
     handle = _launch_stream(stream, a_codes, "a_codes")
     wp, sp = _fp8_weights(cfg, w_codes, w_scales)
     st = _lib.b4_fp8_matmul(
-        cfg._ref, _fp8_codes(a_codes, n * cfg.k, "a_codes"), _fp4_buffer(a_scales, _F32, n * cfg.blocks, "a_scales"),
+        cfg._ref, _fp8_codes(a_codes, n_codes, "a_codes"), _fp4_buffer(a_scales, _F32, n_scales, "a_scales"),
         wp, sp, offsets if offsets is None else _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets"),
         out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, n, "out_rows"), _fp4_out(cfg, out, n),
         device_status if device_status is None else _fp4_buffer(device_status, _I32, 2, "device_status"),
@@ -955,8 +972,9 @@ def fused_moe_fp8(cfg: MoEConfig, x, w13, s13, w2, s2, topk_ids, topk_weights, a
     e, m, h, i = cfg.num_local_experts, cfg.m, cfg.hidden, cfg.inter
     rows, routes = m * h, m * cfg.top_k
     xp, op = _fp4_buffer(x, torch.bfloat16, rows, "x"), _fp4_buffer(out, torch.bfloat16, rows, "out")
-    w13p, s13p = _fp8_weight(w13, s13, e, i if activation == RELU2 else 2 * i, h, "w13", "s13")
-    w2p, s2p = _fp8_weight(w2, s2, e, h, i, "w2", "s2")
+    sizes13, sizes2 = _fp8_layer_sizes(e, h, i, activation)
+    w13p, s13p = _fp8_weight(w13, s13, sizes13, "w13", "s13")
+    w2p, s2p = _fp8_weight(w2, s2, sizes2, "w2", "s2")
     idp = _fp4_buffer(topk_ids, _I32, routes, "topk_ids")
     wtp = _fp4_buffer(topk_weights, _F32, routes, "topk_weights")
     _need(workspace, _U8, "workspace")
