@@ -243,7 +243,7 @@ def test_stack_and_scatter(b4, groups, m, n, k):
 
 RAGGED = [  # counts, rows past the last group, n, k
     ([1] * 8, 0, 1536, 1024), ([0, 3, 0, 0, 4], 2, 140, 80), ([0, 0], 5, 100, 64), ([130, 0, 1, 257, 64], 7, 300, 528),
-    ([33, 17, 129, 128, 300, 2], 3, 640, 400), ([5], 0, 130, 2048), ([700, 1, 40], 0, 256, 640), ([0], 1, 16, 16),
+    ([33, 17, 129, 128, 300, 2], 3, 640, 400), ([5], 0, 130, 2048), ([257, 128, 129, 511, 384], 9, 1300, 272), ([1024, 3], 0, 128, 144), ([700, 1, 40], 0, 256, 640), ([0], 1, 16, 16),
 ]
 
 
@@ -368,6 +368,11 @@ LAYERS = [  # workload, tokens, router
     (W.WORKLOADS["small"].scaled(hidden=256, inter=192, experts=8).with_act("swiglu_oai", (1.702, 1.0, 0.4)), 33, dict(renorm=False)),
     (W.WORKLOADS["mxfp4"].scaled(hidden=352, inter=160, experts=7), 65, dict(bias=True)),
     (W.WORKLOADS["small"].scaled(hidden=256, inter=160, experts=8), 700, dict()),
+    # h quantised by FC1's own kernel: groups of hundreds of rows, whole blocks of h
+    (W.WORKLOADS["small"].scaled(hidden=256, inter=384, experts=8), 700, dict()),
+    (W.WORKLOADS["small"].scaled(hidden=272, inter=256, experts=8).with_act("swiglu_oai", (1.702, 1.0, 0.4)), 450, dict(score="sigmoid", bias=True)),
+    (W.WORKLOADS["decode"].scaled(hidden=400, inter=384, experts=16), 700, dict()),
+    (W.WORKLOADS["mxfp4"].scaled(hidden=352, inter=128, experts=7), 600, dict()),
 ]
 
 
@@ -390,7 +395,7 @@ def _layer(b4, wl, m, seed):
     return full, ops, em, cfg, act, ws
 
 
-@pytest.mark.parametrize("wl,m,router", LAYERS, ids=[f"{c[0].name}-{c[1]}" for c in LAYERS])
+@pytest.mark.parametrize("wl,m,router", LAYERS, ids=[f"{c[0].name}-{c[0].inter}-{c[1]}" for c in LAYERS])
 def test_layer_from_logits(b4, wl, m, router):
     """Weights quantised, experts chosen, the layer run: by the framework's calls alone, twice, and from a graph."""
     x_bits, x = W.activations(wl, m, 71)

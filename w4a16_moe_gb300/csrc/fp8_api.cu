@@ -19,6 +19,7 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams& p, int dtype, int block_ro
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int rows, int grid, int splits, cudaStream_t stream);
 cudaError_t launch_fp8_gemm_direct(const Fp8GemmParams& p, int grid, int splits, cudaStream_t stream);
 cudaError_t launch_fp8_gemm_pair(const Fp8GemmParams& p, int pairs, cudaStream_t stream);
+cudaError_t launch_fp8_gemm_h(const Fp8GemmParams& p, bool gated, int pairs, cudaStream_t stream);
 cudaError_t launch_fp4_combine(const Fp4CombineParams& p, cudaStream_t stream);
 }  // namespace b4
 
@@ -267,6 +268,32 @@ b4_status check_weights(const uint8_t* w_codes, const float* w_scales) {
   return B4_OK;
 }
 
+// The layer's FC1 for many rows: x quantised into `ws` (linear_ws of c), the product, and h = act(x W13^T)
+// quantised into h_codes and h_scales by the product's own kernel.
+b4_status quantize_and_make_h(const b4_fp8_config* c, const b4_fp8_config* act, const void* x, const int32_t* rows,
+                              const int32_t* offsets, const uint8_t* w_codes, const float* w_scales, uint8_t* ws,
+                              uint8_t* h_codes, float* h_scales, uint32_t* status, int sms, cudaStream_t stream) {
+  const LinearWs L = linear_ws(c);
+  uint8_t* codes = ws + L.codes;
+  float* scales = reinterpret_cast<float*>(ws + L.scales);
+  Fp8QuantParams q = quant_params(c, x, rows, offsets, codes, scales, nullptr);
+  q.q.status = status;
+  const cudaError_t e = launch_fp8_quantize(q, c->x_dtype, 1, sms, stream);
+  if (e != cudaSuccess) return cuda_status(e, "fp8 quantise");
+  Fp8GemmParams p = product_params(c, w_scales, offsets, nullptr, nullptr, status);
+  const bool gated = is_gated(act);
+  if (!make_tmap_bytes_2d(&p.tmap_w, w_codes, (uint64_t)c->n * c->num_groups, c->k, c->k, gated ? 64 : 128) ||
+      !make_tmap_bytes_2d(&p.tmap_a, codes, (uint64_t)c->m, c->k, c->k, 64))
+    FP8_FAIL(B4_ERR_CUDA, "cuTensorMapEncodeTiled rejected an operand map");
+  p.a_scales = scales;
+  p.a_vec = aligned(scales, 16) && p.kb % 4 == 0;
+  p.g.a_is_new = 1;
+  p.q = quant_params(act, nullptr, nullptr, offsets, h_codes, h_scales, nullptr);
+  const int64_t units = most_units(c, true, 256);
+  if (units > (1 << 30)) FP8_INVALID("too many units of work: m, n and num_groups too large together");
+  return cuda_status(launch_fp8_gemm_h(p, gated, (int)(units < sms / 2 ? units : sms / 2), stream), "fp8 product");
+}
+
 // The layer: the shapes of its two products and its workspace.
 struct MoeFp8 {
   b4_fp8_config c1, c2;
@@ -320,6 +347,22 @@ b4_status moe_plan(const b4_moe_config* cfg, int32_t activation, MoeFp8* M) {
   M->y = take(sizeof(uint16_t) * (size_t)r_cap * cfg->hidden);
   M->total = off;
   return B4_OK;
+}
+
+b4_status combine(const b4_moe_config* cfg, const uint16_t* y, const int32_t* topk_ids, const float* topk_weights,
+                  uint16_t* out, cudaStream_t s) {
+  Fp4CombineParams cp{};
+  cp.y = y;
+  cp.topk_ids = topk_ids;
+  cp.topk_weights = topk_weights;
+  cp.expert_map = cfg->expert_map;
+  cp.m = cfg->m;
+  cp.top_k = cfg->top_k;
+  cp.num_global_experts = cfg->num_global_experts;
+  cp.num_local_experts = cfg->num_local_experts;
+  cp.hidden = cfg->hidden;
+  cp.out = out;
+  return cuda_status(launch_fp4_combine(cp, s), "fp8 combine");
 }
 
 }  // namespace
@@ -431,6 +474,16 @@ b4_status b4_fused_moe_fp8(const b4_moe_config* cfg, const uint16_t* x, const ui
   pack.path = B4_PATH_AUTO;
   if ((st = b4_route_pack(&pack, topk_ids, reinterpret_cast<int32_t*>(ws + M.counts), offsets, sorted, stream)) != B4_OK)
     return st;
+  // many rows and whole blocks of h: FC1 leaves h quantised (in the room of its sums), then FC2
+  if (unit_rows(&M.c1, true) == 256 && unit_rows(&M.c2, true) == 256 && cfg->inter % kFp8Block == 0) {
+    uint8_t* h_codes = ws + M.fc1;
+    float* h_scales = reinterpret_cast<float*>(h_codes + align_up((size_t)M.c2.m * cfg->inter, 256));
+    if ((st = quantize_and_make_h(&M.c1, &M.c2, x, sorted, offsets, w13, s13, ws + M.quant, h_codes, h_scales, status, sms,
+                                  s)) != B4_OK ||
+        (st = launch_product(&M.c2, h_codes, h_scales, w2, s2, offsets, sorted, y, status, true, sms, s)) != B4_OK)
+      return st;
+    return combine(cfg, y, topk_ids, topk_weights, out, s);
+  }
   // FC1: gather x rows of the packed routes, quantise, multiply by W13
   if ((st = quantize_and_multiply(&M.c1, x, sorted, offsets, w13, s13, nullptr, fc1, ws + M.quant, status, status, sms,
                                   s)) != B4_OK)
@@ -439,18 +492,7 @@ b4_status b4_fused_moe_fp8(const b4_moe_config* cfg, const uint16_t* x, const ui
   if ((st = quantize_and_multiply(&M.c2, fc1, nullptr, offsets, w2, s2, sorted, y, ws + M.quant, nullptr, status, sms,
                                   s)) != B4_OK)
     return st;
-  Fp4CombineParams cp{};
-  cp.y = y;
-  cp.topk_ids = topk_ids;
-  cp.topk_weights = topk_weights;
-  cp.expert_map = cfg->expert_map;
-  cp.m = cfg->m;
-  cp.top_k = cfg->top_k;
-  cp.num_global_experts = cfg->num_global_experts;
-  cp.num_local_experts = cfg->num_local_experts;
-  cp.hidden = cfg->hidden;
-  cp.out = out;
-  return cuda_status(launch_fp4_combine(cp, s), "fp8 combine");
+  return combine(cfg, y, topk_ids, topk_weights, out, s);
 }
 
 }  // extern "C"

@@ -7,6 +7,14 @@
 // of products (measured with copies alone: 480 cycles a stage on all SMs, 756 without
 // sharing).
 //
+// The rows that are left of a group, 128 or fewer, make wide units: both CTAs take them, each
+// with 256 weight rows of its own and without sharing.
+//
+// H: the product is the first of a layer (b4_fused_moe_fp8).  A unit's sums become h, 128 columns of a
+// gated activation (its weight rows are 128 gate rows and the 128 up rows that go with them, 64 of each
+// in an accumulator, so that a lane holds both of a column) or 256 of ReLU^2, and h leaves quantised,
+// codes and scales as b4_fp8_quantize writes them: it never goes to memory in 32 bits.
+//
 // A stage is one block of K.  It has two accumulators of 128 columns, one for each block of 128
 // weight rows, twice: while the tensor core fills one of each pair, four warps read the other,
 // 32 lanes x 128 columns each, and add it to fp32 registers times the row's scale and the
@@ -22,6 +30,7 @@
 // rows, N = 2816, K = 2048 103 us.
 
 #include "fp8_mma.cuh"
+#include "fp8_quant.cuh"
 
 namespace b4 {
 
@@ -40,17 +49,134 @@ constexpr size_t kPairOffStage = kPairOffA + (size_t)kPairSlots * kPairAStage;
 constexpr size_t kPairOffBars = kPairOffStage + kEpiWarps * kOutTile;
 constexpr int kPrefetch = 10;                   // stages of weights asked into L2 ahead of their copies
 constexpr int kAhead = 4;                       // units looked up ahead of the promoting warps
-constexpr int kPairBars = 2 * kPairSlots + 8 + 1 + 2 * kAhead + 4;
+constexpr int kPairBars = 2 * kPairSlots + 8 + 1 + 2 * kAhead + 4 + 4;
 constexpr size_t kPairOffUnits = (kPairOffBars + 8 * kPairBars + 15) / 16 * 16;
 constexpr int kScaleQuad = 130 * 4;             // scales of four stages: 128 rows, two blocks of weights; two of these
 constexpr size_t kPairOffScales = kPairOffUnits + 16 * kAhead;
 constexpr size_t kPairOffMisc = kPairOffScales + 2 * kScaleQuad * sizeof(float);
-constexpr size_t pair_smem(bool ragged) { return kPairOffMisc + 16 + (ragged ? sizeof(Groups) : 0); }
+constexpr size_t pair_smem(bool ragged) { return kPairOffMisc + 16 + (ragged ? 2 * sizeof(int) * (kMaxGroups + 1) + sizeof(int) * kThreads / 32 : 0); }
 
-template <int OUT, bool RAGGED>
+enum PairH : int { kPlain = 0, kGated = 1, kRelu2 = 2 };
+
+// Tables of the groups in shared memory: first row, and units before the group.
+struct PairGroups {
+  int first[kMaxGroups + 1];
+  int units[kMaxGroups + 1];
+  int warp[kThreads / 32];
+};
+// Units of a group of `rows` rows, where all its weights are wp blocks of 256: tall ones, then wide.
+__device__ __forceinline__ int units_of(int rows, int wp) {
+  const int rest = rows % kPairRows;
+  return (rows / kPairRows + (rest > 128)) * wp + (rest > 0 && rest <= 128 ? (wp + 1) / 2 : 0);
+}
+
+// A block scan of the groups' units, four groups a thread; ends with the tables written but
+// not yet synchronised.
+__device__ __forceinline__ void build_pair_groups(const Fp4GemmParams& p, PairGroups& g, int wp) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int cnt[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = 4 * threadIdx.x + i;
+    cnt[i] = 0;
+    if (e <= p.groups) {
+      const int lo = min(max(__ldg(p.offsets + e), 0), p.m);
+      g.first[e] = lo;
+      if (e < p.groups) cnt[i] = units_of(max(min(__ldg(p.offsets + e + 1), p.m) - lo, 0), wp);
+    }
+    sum += cnt[i];
+  }
+  int scan = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) g.warp[warp] = scan;
+  __syncthreads();
+  int before = scan - sum;
+  for (int w = 0; w < warp; ++w) before += g.warp[w];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = 4 * threadIdx.x + i;
+    if (e <= p.groups) g.units[e] = before;
+    before += cnt[i];
+  }
+}
+
+// A CTA's part of unit u: its group, block of 256 weight rows, first row and rows (128 at most).  Weight
+// blocks are outermost within a group, so that neighbouring units read the same weights.
+// Ragged units are taken from each third of them in turn: those of large groups are bound by the
+// chain of promotion, those of small groups by the stream of weights, and the two mix better than they
+// follow one another.
+struct PairUnit {
+  int group, wt, first, rows;
+  bool wide;
+};
+template <bool RAGGED>
+__device__ __noinline__ static int4 find_pair_unit(int groups, int m, const PairGroups* g, int wp, int u, int rank) {
+  int e = 0, first, rows;
+  if constexpr (RAGGED) {
+    const int run = g->units[groups] / kMix;
+    if (u < run * kMix) u = u % kMix * run + u / kMix;
+    int hi = groups - 1;  // last group whose units start at or before this one
+    while (e < hi) {
+      const int mid = (e + hi + 1) >> 1;
+      if (g->units[mid] <= u) e = mid;
+      else hi = mid - 1;
+    }
+    u -= g->units[e];
+    first = g->first[e];
+    rows = g->first[e + 1] - first;
+  } else {
+    const int per = units_of(m, wp);
+    e = groups == 1 ? 0 : u / per;
+    u -= e * per;
+    first = e * m;
+    rows = m;
+  }
+  const int rest = rows % kPairRows, tall = rows / kPairRows + (rest > 128);
+  int wt, mine, wide = 0;
+  if (u < tall * wp) {
+    wt = tall == 1 ? u : u / tall;
+    const int t = u - wt * tall;
+    first += t * kPairRows + 128 * rank;
+    mine = min(max(rows - t * kPairRows - 128 * rank, 0), 128);
+  } else {
+    wide = 1;
+    wt = 2 * (u - tall * wp) + rank;
+    first += tall * kPairRows;
+    mine = wt < wp ? rest : 0;
+  }
+  return make_int4(e, wt, first, mine | wide << 16);
+}
+template <bool RAGGED>
+__device__ __forceinline__ PairUnit pair_unit(const Fp4GemmParams& p, const PairGroups& g, int wp, int u, int rank) {
+  const int4 v = find_pair_unit<RAGGED>(p.groups, p.m, &g, wp, u, rank);
+  return PairUnit{v.x, v.y, v.z, v.w & 0xffff, v.w >> 16 != 0};
+}
+
+// Two columns of h, as the quantiser's prologue forms them (fp4_quant.cuh).
+__device__ __forceinline__ float2 gated2(float2 a, float2 b, const GluParams& p) {
+  using namespace fp4q;
+  const float scale = -1.44269504f * p.alpha;
+  const float gx = min_nan(a.x, p.limit), gy = min_nan(a.y, p.limit);
+  const float ux = max_nan(min_nan(b.x, p.limit), -p.limit), uy = max_nan(min_nan(b.y, p.limit), -p.limit);
+  return make_float2(gx * rcp_approx(exp2_approx(gx * scale) + 1.f) * (ux + p.beta),
+                     gy * rcp_approx(exp2_approx(gy * scale) + 1.f) * (uy + p.beta));
+}
+
+// Sixteen values in registers as a chunk of the quantiser.
+struct Sixteen {
+  const float2* v;
+  __device__ __forceinline__ float2 pair(int j) const { return v[j]; }
+};
+
+// OUT: 0 bf16, 1 f16, 2 f32 outputs; H: kPlain, or h as the next product's operand.
+template <int OUT, bool RAGGED, int H>
 __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_constant__ Fp8GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  Groups& groups = *reinterpret_cast<Groups*>(smem + kPairOffMisc + 16);  // ragged only
+  PairGroups& groups = *reinterpret_cast<PairGroups*>(smem + kPairOffMisc + 16);  // ragged only
   uint8_t* s_a = smem + kPairOffA;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairOffBars);
   uint64_t* empty = full + kPairSlots;                                // the products of both CTAs are through with the slot
@@ -61,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   uint64_t* empty_unit = full_unit + kAhead;
   uint64_t* full_scale = empty_unit + kAhead;
   uint64_t* empty_scale = full_scale + 2;
+  uint64_t* both_halves = empty_scale + 2;                            // gated: a quarter's two warps have their maxima
   int4* s_unit = reinterpret_cast<int4*>(smem + kPairOffUnits);       // group, weight unit, first row, rows
   float* s_scale = reinterpret_cast<float*>(smem + kPairOffScales);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kPairOffMisc);
@@ -78,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
     }
     mbar_init(drain, 2);
     for (int i = 0; i < 4; ++i) {
+      mbar_init(&both_halves[i], 2);
       mbar_init(&full_acc[i], 1);
       mbar_init(&empty_acc[i], kEpiWarps / 2);
     }
@@ -96,15 +224,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
     tmem_relinquish();
   }
   if (!g.a_is_new) pdl_wait();  // alone in its call: every input may come from the kernel before
-  const int wpairs = cdiv(g.n, 256);
+  const int wp = cdiv(g.n, 256);  // blocks of 256 weight rows
   const int wtiles = cdiv(g.n, 128);
-  if (RAGGED) build_groups<kPairRows>(g, groups);
+  if (RAGGED) build_pair_groups(g, groups, wp);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers exist before either signals
   tc_fence_after();
   if (threadIdx.x == 0) pdl_launch_dependents();
   const uint32_t tmem = *s_tmem;
-  const int n_units = (RAGGED ? groups.tiles[g.groups] : g.groups * cdiv(g.m, kPairRows)) * wpairs;
+  const int n_units = RAGGED ? groups.units[g.groups] : g.groups * units_of(g.m, wp);
   const int u0 = blockIdx.x >> 1, du = gridDim.x >> 1;
 
   if (warp < 4) {
@@ -115,35 +243,57 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       // third of what DRAM's latency takes.
       uint32_t i = 0;
       bool ok = true;
-      int pu = u0, ps = 0, prow = 0;
-      auto weight_row = [&](const Unit& U) {
-        return (int)warp_uniform(U.group) * g.n + (2 * (int)warp_uniform(U.wtile) + (int)rank) * 128;
+      PairUnit ahead{};
+      int pu = u0, ps = 0;
+      auto known = [&](int u) {
+        PairUnit U = pair_unit<RAGGED>(g, groups, wp, u, rank);
+        U.group = (int)warp_uniform(U.group), U.wt = (int)warp_uniform(U.wt);
+        U.first = (int)warp_uniform(U.first), U.rows = (int)warp_uniform(U.rows);
+        return U;
+      };
+      // f(place in the stage's weights, first weight row) of the CTA's boxes.  Block b of 128 rows is N of the
+      // stage's accumulator b.
+      auto each_box = [&](const PairUnit& U, auto f) {
+        const int base = U.group * g.n;
+        if (U.wide && U.wt >= wp) return;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (!U.wide && b != (int)rank) continue;  // the other CTA's
+          if constexpr (H == kGated) {
+            f(b * kWStage, base + U.wt * 128 + b * 64);
+            f(b * kWStage + kWStage / 2, base + g.n / 2 + U.wt * 128 + b * 64);
+          } else {
+            f(b * kWStage, base + U.wt * 256 + b * 128);
+          }
+        }
       };
       auto prefetch = [&]() {
         if (pu >= n_units) return;
-        if (ps == 0) prow = weight_row(get_unit<kPairRows, RAGGED>(g, groups, wpairs, pu));
-        if (elect_one()) tma_prefetch_2d(&p.tmap_w, ps * 128, prow);
+        if (ps == 0) ahead = known(pu);
+        if (elect_one()) each_box(ahead, [&](int, int row) { tma_prefetch_2d(&p.tmap_w, ps * 128, row); });
         __syncwarp();
         if (++ps == p.kb) ps = 0, pu += du;
       };
       for (int j = 0; j < kPrefetch; ++j) prefetch();
       if (g.a_is_new) pdl_wait();
       for (int u = u0; u < n_units && ok; u += du) {
-        const Unit U = get_unit<kPairRows, RAGGED>(g, groups, wpairs, u);
-        const int rows = min(max((int)warp_uniform(U.rows) - 128 * (int)rank, 0), 128);
-        const int first = (int)warp_uniform(U.first) + 128 * (int)rank;
-        const int wrow = weight_row(U);
-        const int boxes = cdiv(rows, kPairBox);
+        const PairUnit U = known(u);
+        const int boxes = cdiv(U.rows, kPairBox);
+        const uint32_t bytes = (U.wide && U.wt >= wp ? 0 : kPairWStage) + boxes * kPairBox * 128;
         for (int s = 0; s < p.kb; ++s, ++i) {
           const uint32_t slot = i % kPairSlots;
           ok = __all_sync(0xffffffffu, wait(&empty[slot], ((i / kPairSlots) & 1) ^ 1, ab, 131));
           if (!ok) break;
           if (elect_one()) {
-            mbar_arrive_expect_tx(&full[slot], kPairWStage + boxes * kPairBox * 128);
-            tma_load_2d_both(smem + slot * kPairWStage + rank * kWStage, &p.tmap_w, s * 128, wrow, &full[slot]);
-            if (boxes > 0) tma_load_2d(s_a + slot * kPairAStage, &p.tmap_a, s * 128, first, &full[slot]);
+            mbar_arrive_expect_tx(&full[slot], bytes);
+            uint8_t* sw = smem + slot * kPairWStage;
+            each_box(U, [&](int at, int row) {
+              if (U.wide) tma_load_2d(sw + at, &p.tmap_w, s * 128, row, &full[slot]);
+              else tma_load_2d_both(sw + at, &p.tmap_w, s * 128, row, &full[slot]);
+            });
+            if (boxes > 0) tma_load_2d(s_a + slot * kPairAStage, &p.tmap_a, s * 128, U.first, &full[slot]);
             if (boxes > 1)
-              tma_load_2d(s_a + slot * kPairAStage + kPairBox * 128, &p.tmap_a, s * 128, first + kPairBox, &full[slot]);
+              tma_load_2d(s_a + slot * kPairAStage + kPairBox * 128, &p.tmap_a, s * 128, U.first + kPairBox, &full[slot]);
           }
           __syncwarp();
           prefetch();
@@ -208,21 +358,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       uint32_t i = 0, n = 0;
       bool ok = true;
       for (int u = u0; u < n_units && ok; u += du, ++n) {
-        const Unit U = get_unit<kPairRows, RAGGED>(g, groups, wpairs, u);
+        const PairUnit U = pair_unit<RAGGED>(g, groups, wp, u, rank);
         const uint32_t b = n % kAhead;
         ok = __all_sync(0xffffffffu, wait(&empty_unit[b], ((n / kAhead) & 1) ^ 1, ab, 135));
         if (!ok) break;
         if (lane == 0) {
-          s_unit[b] = make_int4(U.group, U.wtile, U.first, U.rows);
+          s_unit[b] = make_int4(U.group, U.wt, U.first, U.rows);
           mbar_arrive(&full_unit[b]);
         }
         __syncwarp();
-        const float* sa[4];  // rows lane, lane + 32, ...
+        const float* sa[4];  // rows lane, lane + 32, ... (a unit without rows here: its first CTA's)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          sa[j] = p.a_scales + (int64_t)(U.first + min(128 * (int)rank + 32 * j + lane, U.rows - 1)) * p.kb;
-        const float* sw0 = p.w_scales + ((int64_t)U.group * wtiles + 2 * U.wtile) * p.kb;
-        const float* sw1 = 2 * U.wtile + 1 < wtiles ? sw0 + p.kb : sw0;
+          sa[j] = p.a_scales + (int64_t)(U.rows > 0 ? U.first + min(32 * j + lane, U.rows - 1) : 0) * p.kb;
+        // of the accumulators' weight rows; gated: of the gate rows and of the up rows
+        const int t0 = min(H == kGated ? U.wt : 2 * U.wt, wtiles - 1);
+        const int t1 = min(H == kGated ? U.wt + wtiles / 2 : t0 + 1, wtiles - 1);
+        const float* sw0 = p.w_scales + ((int64_t)U.group * wtiles + t0) * p.kb;
+        const float* sw1 = p.w_scales + ((int64_t)U.group * wtiles + t1) * p.kb;
         // four stages at a time, loaded eight stages ahead
         float4 next[2][4], w[2];
         auto load = [&](int s, int d) {
@@ -251,28 +404,28 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
             }
         }
       }
-      if (RAGGED && !g.out_rows) clear_tail<32>(g, groups.first[g.groups], lane);
+      if (H == kPlain && RAGGED && !g.out_rows) clear_tail<32>(g, groups.first[g.groups], lane);
     }
   } else {
     // ------------------------------------------- promotion and epilogue
     if (g.a_is_new) pdl_wait();  // (the output's last readers)
     const int q4 = warp & 3, half = (warp - 4) >> 2;
-    const int r = 128 * (int)rank + 32 * q4 + lane;
+    const int r = 32 * q4 + lane;
     const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + 128 * half;
     uint64_t* mine_acc = full_acc + half;  // this warp's two accumulators: 2 apart
     uint64_t* done = empty_acc + half;
     uint8_t* stage = smem + kPairOffStage + (warp - 4) * kOutTile;
     const float4* scales = reinterpret_cast<const float4*>(s_scale);
-    uint32_t i = 0, n = 0, quad = 0;
+    uint32_t i = 0, n = 0, quad = 0, done_units = 0;
     bool ok = true;
     for (int u = u0; u < n_units && ok; u += du, ++n) {
       ok = __all_sync(0xffffffffu,  wait(&full_unit[n % kAhead], (n / kAhead) & 1, ab, 136));
       if (!ok) break;
-      const int4 U = s_unit[n % kAhead];  // group, weight unit, first row, rows
+      const int4 U = s_unit[n % kAhead];  // group, block of weights, first row, rows
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty_unit[n % kAhead]);
-      const int col = U.y * 256 + 128 * half;
-      if (r - lane >= U.w || col >= g.n) {  // nothing of this warp's
+      const int col = U.y * 256 + 128 * half;  // (of the sums)
+      if (32 * q4 >= U.w || (H != kGated && col >= g.n)) {  // nothing of this warp's
         for (int s = 0; s < p.kb && ok; ++s, ++i) {
           if ((s & 3) == 0) {
             ok = __all_sync(0xffffffffu,  wait(&full_scale[quad & 1], (quad >> 1) & 1, ab, 138));
@@ -291,19 +444,24 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       bool seen = false;  // the block's accumulator was seen complete during the block before
       // (one way out of the loop: with a second the compiler copies the sums every time round; once a
       // wait has run out, the others return at once and nothing is stored)
-      float4 four = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 four = make_float4(0.f, 0.f, 0.f, 0.f), up = four;
       for (int s = 0; s < p.kb; ++s, ++i) {
         if ((s & 3) == 0) {
           ok = __all_sync(0xffffffffu, wait(&full_scale[quad & 1], (quad >> 1) & 1, ab, 138)) && ok;
-          four = scales[(quad & 1) * (kScaleQuad / 4) + 32 * q4 + lane];
-          const float4 w = scales[(quad & 1) * (kScaleQuad / 4) + 128 + half];
+          four = scales[(quad & 1) * (kScaleQuad / 4) + r];
+          const float4 w = scales[(quad & 1) * (kScaleQuad / 4) + 128 + (H == kGated ? 0 : half)];
+          if constexpr (H == kGated) {
+            const float4 v = scales[(quad & 1) * (kScaleQuad / 4) + 129];
+            up = make_float4(four.x * v.x, four.y * v.y, four.z * v.z, four.w * v.w);
+          }
           four = make_float4(four.x * w.x, four.y * w.y, four.z * w.z, four.w * w.w);
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty_scale[quad & 1]);
           ++quad;
         }
-        const float scale = four.x;
+        const float scale = four.x, scale_up = H == kGated ? up.x : scale;
         four = make_float4(four.y, four.z, four.w, 0.f);
+        if constexpr (H == kGated) up = make_float4(up.y, up.z, up.w, 0.f);
         if (!seen) ok = __all_sync(0xffffffffu, wait(&mine_acc[2 * (i & 1)], (i >> 1) & 1, ab, 134)) && ok;
         tc_fence_after();
         const uint32_t at = taddr + 256 * (i & 1);
@@ -320,12 +478,45 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
             look = mbar_test(&mine_acc[2 * (~i & 1)], ((i + 1) >> 1) & 1);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) fma2(acc[8 * c + e], t[2 * e], t[2 * e + 1], scale);
+          for (int e = 0; e < 8; ++e) fma2(acc[8 * c + e], t[2 * e], t[2 * e + 1], c < 4 ? scale : scale_up);
         }
         seen = __all_sync(0xffffffffu, look);
       }
       if (!ok) break;
-      if (OUT < 2 && g.vec) {
+      if constexpr (H != kPlain) {
+        // h in place of the sums, its block's scale (gated: with the warp of the other 64 columns), codes
+        constexpr int kCols = H == kGated ? 32 : 64;  // pairs of columns of this warp
+        uint32_t a = 0;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          if constexpr (H == kGated) {
+            acc[c] = gated2(acc[c], acc[32 + c], p.q.q.glu);
+          } else {
+            const float x = fp4q::max_nan(acc[c].x, 0.f), y = fp4q::max_nan(acc[c].y, 0.f);
+            acc[c] = make_float2(x * x, y * y);
+          }
+          a = max(a, max(__float_as_uint(acc[c].x) & 0x7fffffffu, __float_as_uint(acc[c].y) & 0x7fffffffu));
+        }
+        if constexpr (H == kGated) {
+          uint32_t* most = reinterpret_cast<uint32_t*>(smem + kPairOffStage) + (done_units & 1) * 256;
+          most[half * 128 + r] = a;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&both_halves[q4]);
+          ok = __all_sync(0xffffffffu, wait(&both_halves[q4], done_units & 1, ab, 139));
+          if (!ok) break;
+          a = max(a, most[(half ^ 1) * 128 + r]);
+          ++done_units;
+        }
+        const float s = fp8q::block_scale<false>(a);
+        if (to >= 0) {
+          const int width = H == kGated ? g.n / 2 : g.n;
+          const int at = H == kGated ? 128 * U.y + 64 * half : col;
+          uint4* codes = reinterpret_cast<uint4*>(p.q.q.codes + (int64_t)to * width + at);
+#pragma unroll
+          for (int c = 0; c < kCols / 8; ++c) codes[c] = fp8q::encode8<false>(Sixteen{acc + 8 * c}, s);
+          if (H != kGated || half == 0) p.q.scales[(int64_t)to * (width / 128) + at / 128] = s;
+        }
+      } else if (OUT < 2 && g.vec) {
         // Through shared memory.  Full tiles leave from there as boxes of 32 rows x 64, under the next
         // unit: stores of all SMs at once take 4000 cycles to drain, and what the warp does next
         // queues behind them.  Others (rows by an index, the end of a group) as 256 bytes of two
@@ -342,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&p.tmap_out, col, U.z + r, stage);
-            if (col + 64 < g.n) tma_store_2d(&p.tmap_out, col + 64, U.z + r, stage + kOutTile / 2);
+            tma_store_2d(&p.tmap_out, col, U.z + 32 * q4, stage);
+            if (col + 64 < g.n) tma_store_2d(&p.tmap_out, col + 64, U.z + 32 * q4, stage + kOutTile / 2);
             bulk_commit();
           }
         } else {
@@ -377,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int OUT, bool RAGGED>
+template <int OUT, bool RAGGED, int H>
 cudaError_t launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t stream) {
-  auto kern = fp8_pair_kernel<OUT, RAGGED>;
+  auto kern = fp8_pair_kernel<OUT, RAGGED, H>;
   const size_t smem = pair_smem(RAGGED);
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -403,7 +594,14 @@ cudaError_t launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t stream) 
 }  // namespace fp8
 
 cudaError_t launch_fp8_gemm_pair(const Fp8GemmParams& p, int pairs, cudaStream_t stream) {
-  return fp8::with_out(p, [&](auto out, auto ragged) { return fp8::launch_pair<out.value, ragged.value>(p, pairs, stream); });
+  return fp8::with_out(
+      p, [&](auto out, auto ragged) { return fp8::launch_pair<out.value, ragged.value, fp8::kPlain>(p, pairs, stream); });
+}
+
+// The first product of a layer: p.q takes h (codes, scales, glu).
+cudaError_t launch_fp8_gemm_h(const Fp8GemmParams& p, bool gated, int pairs, cudaStream_t stream) {
+  return gated ? fp8::launch_pair<0, true, fp8::kGated>(p, pairs, stream)
+               : fp8::launch_pair<0, true, fp8::kRelu2>(p, pairs, stream);
 }
 
 }  // namespace b4
