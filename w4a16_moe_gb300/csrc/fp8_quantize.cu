@@ -22,7 +22,8 @@ using namespace fp8q;
 namespace {
 
 constexpr int kThreads8 = 128;
-constexpr int kBlockThreads = 256;  // of a 128 x 128 block: four chunks a thread
+constexpr int kBlockThreads = 512;  // of a 128 x 128 block: two chunks a thread
+constexpr int kBlockChunks = 1024 / kBlockThreads, kBlockStep = kBlockThreads / 8, kBlockResident = 2;
 
 // What the codes stand for, in x's type.
 template <typename T>
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads8) fp8_quantize_kernel(const __grid_co
 
 // A scale per 128 x 128: a block of threads takes one.
 template <typename T, bool ACT, bool POW2>
-__global__ void __launch_bounds__(kBlockThreads) fp8_quantize_block_kernel(const __grid_constant__ Fp8QuantParams p) {
+__global__ void __launch_bounds__(kBlockThreads, kBlockResident) fp8_quantize_block_kernel(const __grid_constant__ Fp8QuantParams p) {
   __shared__ uint32_t s_max[kBlockThreads / 32];
   pdl_wait();
   pdl_launch_dependents();
@@ -111,16 +112,16 @@ __global__ void __launch_bounds__(kBlockThreads) fp8_quantize_block_kernel(const
   const int r0 = (int)(gb - group * row_blocks) * kFp8Block + (threadIdx.x >> 3);
   const int chunk = 8 * kb + (threadIdx.x & 7);
   const bool in = 16 * chunk < q.k;
-  Chunk<T, ACT> h[4];
+  Chunk<T, ACT> h[kBlockChunks];
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 32 * i;
+  for (int i = 0; i < kBlockChunks; ++i) {
+    const int r = r0 + kBlockStep * i;
     if (in && r < q.m) h[i].get(q, reinterpret_cast<const T*>(q.x) + (group * q.m + r) * q.x_stride, chunk);
     else h[i].zero();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a = max(a, h[i].amax());
+  for (int i = 0; i < kBlockChunks; ++i) a = max(a, h[i].amax());
   a = __reduce_max_sync(0xffffffffu, a);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = a;
   __syncthreads();
@@ -129,8 +130,8 @@ __global__ void __launch_bounds__(kBlockThreads) fp8_quantize_block_kernel(const
   const float s = block_scale<POW2>(a);
   if (threadIdx.x == 0) p.scales[blockIdx.x] = s;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 32 * i;
+  for (int i = 0; i < kBlockChunks; ++i) {
+    const int r = r0 + kBlockStep * i;
     if (in && r < q.m) {
       const int64_t row = group * q.m + r;
       const uint4 w = encode8<POW2>(h[i], s);
