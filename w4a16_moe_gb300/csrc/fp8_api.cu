@@ -116,14 +116,14 @@ Fp8QuantParams quant_params(const b4_fp8_config* c, const void* x, const int32_t
 
 // Activation rows of a unit: 32 or 128 (fp8_gemm.cuh, one SM a unit of 128 outputs), 256
 // (fp8_gemm_pair.cu, a pair of SMs, 256 outputs).  By the rows, of ragged groups their mean.
-// Measured in us at 32 / 128 / 256: N = K = 4096, m = 64 10.2 / 13.4 / 17.7, 128 13.3 / 13.9 / 19.7, 256 23.2 / 14.3 /
-// 18.9, 512 42.3 / 14.6 / 20.2, 1024 71 / 25.7 / 21.1; 64 groups, N = 2816, K = 2048, mean 6 62.9 / 64.2 / 89, 16 63.9 / 65.1 /
-// 89, 96 181 / 70.6 / 98, 128 230 / 93.4 / 99, 192 331 / 125 / 103; 28 groups, N = K = 2880, mean 32 56.6 / 48.1 / 64, 64 85.9 /
-// 49.4 / 65.
+// Measured in us at 32 / 128 / 256: N = K = 4096, m = 64 9.6 / 13.4 / 17.7, 128 12.4 / 14.1 / 19.7, 256 21.3 / 14.3 /
+// 18.9, 512 38.8 / 14.8 / 20.2, 1024 66 / 25.7 / 21.1; 64 groups, N = 2816, K = 2048, mean 6 61.4 / 64.4 / -, 16 62.3 / 65.1 /
+// -, 96 168 / 70.5 / 90.2, 128 214 / 93.8 / 90.8, 192 - / 125 / 106, with popularities spread by e^N(0, 1) 64 124 / 73.0 /
+// 77.1, 96 164 / 84.9 / 84.0, 192 - / 125 / 109; 28 groups, N = K = 2880, mean 32 54.7 / 48.0 / -, 64 80.0 / 49.2 / 62.9.
 int unit_rows(const b4_fp8_config* c, bool ragged) {
   if (ragged) {
     const int64_t per = c->m / c->num_groups;
-    return per <= 16 ? 32 : per <= 128 ? 128 : 256;
+    return per <= 16 ? 32 : per <= 104 ? 128 : 256;
   }
   return c->m <= 128 ? 32 : c->m <= 512 ? 128 : 256;
 }
@@ -136,7 +136,8 @@ int64_t most_units(const b4_fp8_config* c, bool ragged, int rows) {
   return tok * cdiv(c->n, rows == 256 ? 256 : 128);
 }
 
-// CTAs that share a unit along K where the units are fewer than the SMs.
+// CTAs that share a unit along K where the units are fewer than the SMs: each keeps three stages
+// (of 128 K) or more, and the first has room for the others' partial sums.
 int k_splits(const b4_fp8_config* c, int64_t units, int sms) {
   const int stages = cdiv(c->k, kFp8Block);
   const int rows = c->m < 32 ? c->m : 32;

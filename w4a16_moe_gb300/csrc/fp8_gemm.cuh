@@ -13,8 +13,8 @@
 // memory; up to ROWS of them live, the others multiply whatever lies behind them in shared
 // memory and are not read), 128 weight rows on N: a lane's scale is one register for all of
 // its columns, and the 128 weight rows share theirs.  Roles of the twelve warps: 0 copies,
-// 1 matrix instructions, 2 and 3 scales (both factors' product, ahead of the promoting warps,
-// which a load would hold up) and zeros in rows of a ragged output past the last group, 4 to
+// 1 (and 3) matrix instructions, 2 (or 3 too) scales (both factors' product, ahead of the promoting
+// warps, which a load would hold up) and zeros in rows of a ragged output past the last group, 4 to
 // 11 promotion and output, 32 lanes x 64 columns each.  As the second kernel of a call, it
 // fills its ring with weights while the quantiser still runs.
 //
@@ -24,6 +24,10 @@
 // SPLIT: where the units are fewer than the SMs, a cluster of 2 to 8 CTAs shares a unit along
 // K.  The partial sums go to the first CTA's shared memory as asynchronous stores that count
 // on its barrier, and it adds them in rank order, so the result does not depend on timing.
+//
+// Measured: 64 groups of 6 rows, N = 2816, K = 2048 61.4 us (372 MB, 6.1 TB/s), of 96 rows 70.5 us (5.9 TB/s); one row, N = K = 4096
+// 7.6 us, direct 7.7; eight groups of one row, N = 1536, K = 4096 (50 MB) direct 13.5 us: 96 CTAs of a unit each,
+// whose 32 stages follow one another.
 //
 // Every wait is bounded (ptx.cuh).
 #pragma once
@@ -62,7 +66,9 @@ struct Cfg {
   static constexpr int kNumBars = 2 * kSlots + 2 * kAccs + 3;
   static constexpr size_t misc = bars + 8 * (kNumBars + 1);
   static constexpr size_t total(bool ragged) { return misc + 16 + (ragged ? sizeof(Groups) : 0); }
-  static_assert(kSlots >= 3 && kWStage * kSlots >= 128 * 128, "shared memory budget");
+  static constexpr int kPromoters = ROWS / 16;  // warps that have rows: two a quarter
+  static constexpr int kIssuers = ROWS == 32 ? 2 : 1, kScalers = 3 - kIssuers;  // of warps 1 to 3
+  static_assert(kSlots >= kAccs && kWStage * kSlots >= 128 * 128, "shared memory budget");
 };
 
 // DIRECT: rows first .. first + rows of the operand, quantised by 256 threads: codes of the
@@ -147,9 +153,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     }
     for (int i = 0; i < kAccs; ++i) {
       mbar_init(&full_acc[i], DIRECT ? 1 : 2);
-      mbar_init(&empty_acc[i], kEpiWarps);
+      mbar_init(&empty_acc[i], C::kPromoters);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, C::kIssuers);
     mbar_init(part_bar, 1);
     mbar_init(own_bar, kEpiWarps);
     fence_mbar_init();
@@ -225,31 +231,35 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || (warp == 3 && C::kIssuers == 2)) {
     // ---------------------------------------------- matrix instructions
+    // Units of 32 rows: warp 1 issues the even stages, warp 3 the odd ones, since one warp takes some
+    // 600 cycles for a stage, more than DRAM takes to bring it.  (With 128 rows scales take that
+    // long too, and need the warp more: 64 groups of 96 rows 70 us, 92 the other way.)
+    const int w = C::kIssuers == 2 ? warp >> 1 : 0;
     const uint32_t w_desc = desc_lo(smem_u32(s_w)), a_desc = desc_lo(smem_u32(s_a));
     constexpr uint32_t idesc = idesc_fp8(128, 128);
-    uint32_t i = 0;
-    bool ok = u0 < n_units, seen = false;
-    if (DIRECT && ok) ok = __all_sync(0xffffffffu, wait(own_bar, 0, ab, 129));
-    for (int u = u0; u < n_units && ok; u += du) {
-      for (int s = s_beg; s < s_end; ++s, ++i) {
-        const uint32_t slot = i % NS, acc = i % kAccs;
-        ok = __all_sync(0xffffffffu, wait(&empty_acc[acc], ((i / kAccs) & 1) ^ 1, ab, 122));
-        if (ok && !seen) ok = __all_sync(0xffffffffu, wait(&full[slot], (i / NS) & 1, ab, 123));
-        if (!ok) break;
-        tc_fence_after();
-        const bool look = mbar_test(&full[(i + 1) % NS], ((i + 1) / NS) & 1);
-        if (elect_one()) {
-          const uint32_t wd = w_desc + slot * (kWStage / 16);
-          const uint32_t ad = a_desc + (DIRECT ? (s - s_beg) * (kFp8DirectTile * 128 / 16) : slot * (C::kAStage / 16));
+    const int stages = s_end - s_beg;
+    const int total = u0 < n_units ? (SPLIT || DIRECT ? 1 : (n_units - 1 - u0) / du + 1) * stages : 0;
+    bool ok = true;
+    if (DIRECT && total > 0) ok = __all_sync(0xffffffffu, wait(own_bar, 0, ab, 129));
+    for (int i = w; i < total && ok; i += C::kIssuers) {
+      const uint32_t slot = i % NS, acc = i % kAccs;
+      // (the accumulator first: with it the stages kAccs back have run, so that the slot's barrier is not
+      // two phases behind, where it would look complete)
+      ok = __all_sync(0xffffffffu, wait(&empty_acc[acc], ((i / kAccs) & 1) ^ 1, ab, 122));
+      ok = ok && __all_sync(0xffffffffu, wait(&full[slot], (i / NS) & 1, ab, 123));
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t wd = w_desc + slot * (kWStage / 16);
+        const uint32_t ad = a_desc + (DIRECT ? i * (kFp8DirectTile * 128 / 16) : slot * (C::kAStage / 16));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_fp8<1>(tmem + acc * 128, ad + 2 * j, wd + 2 * j, idesc, j > 0);
-          mma_commit(&full_acc[acc]);
-          mma_commit(&empty[slot]);
-        }
-        seen = __all_sync(0xffffffffu, look);
+        for (int j = 0; j < 4; ++j) mma_fp8<1>(tmem + acc * 128, ad + 2 * j, wd + 2 * j, idesc, j > 0);
+        mma_commit(&full_acc[acc]);
+        mma_commit(&empty[slot]);
       }
+      __syncwarp();
     }
     // drain: every instruction issued has completed
     if (elect_one()) mma_commit(drain);
@@ -261,13 +271,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     // ---- scales, stages by turns; rows of a ragged output past the last group are zero
     if (g.a_is_new) pdl_wait();
     if constexpr (!DIRECT) {
+      constexpr int kTurn = C::kScalers;
       uint32_t i0 = 0;  // stages of the units before
       bool ok = true;
       for (int u = u0; u < n_units && ok; u += du, i0 += s_end - s_beg) {
         const Unit U = get_unit<ROWS, RAGGED>(g, groups, wtiles, u);
         const float* sw = p.w_scales + ((int64_t)U.group * wtiles + U.wtile) * p.kb;
         constexpr int kPer = ROWS / 32;
-        constexpr int kDeep = 4;  // stages of this warp loaded ahead
+        constexpr int kDeep = 8 / kTurn;  // stages of this warp loaded ahead
         float v[kDeep][kPer];
         auto load = [&](int s, float (&to)[kPer]) {
           const float f = s < s_end ? __ldg(sw + s) : 0.f;
@@ -277,10 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             to[j] = s < s_end && r < U.rows ? f * p.a_scales[(int64_t)(U.first + r) * p.kb + s] : 0.f;
           }
         };
-        // the stages whose number (all units') is this warp's parity
-        int s = s_beg + (int)((i0 + warp) & 1);
+        // the stages whose number (all units') leaves this warp's turn
+        int s = s_beg + (kTurn == 2 ? (int)((i0 + warp) & 1) : 0);
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d) load(s + 2 * d, v[d]);
+        for (int d = 0; d < kDeep; ++d) load(s + kTurn * d, v[d]);
         while (s < s_end && ok) {
 #pragma unroll
           for (int d = 0; d < kDeep; ++d) {
@@ -294,15 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 for (int j = 0; j < kPer; ++j) s_scale[(i % kScaleRing) * ROWS + 32 * j + lane] = v[d][j];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full_acc[i % kAccs]);
-                load(s + 2 * kDeep, v[d]);
+                load(s + kTurn * kDeep, v[d]);
               }
-              s += 2;
+              s += kTurn;
             }
           }
         }
       }
     }
-    if (RAGGED && !g.out_rows) clear_tail(g, groups.first[g.groups], threadIdx.x - 64);
+    if (RAGGED && !g.out_rows) clear_tail<32 * C::kScalers>(g, groups.first[g.groups], threadIdx.x - 64);
   } else {
     // ------------------------------------------- promotion and output
     if (g.a_is_new) pdl_wait();
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     uint8_t* stage = smem + C::stage + (warp - 4) * kStagePiece;
     uint32_t i = 0;
     bool ok = true;
-    for (int u = u0; u < n_units && ok; u += du) {
+    for (int u = u0; u < n_units && ok && 32 * q4 < ROWS; u += du) {
       const Unit U = get_unit<ROWS, RAGGED>(g, groups, wtiles, u);
       if (32 * q4 >= U.rows) {  // no row of this warp's
         for (int s = s_beg; s < s_end && ok; ++s, ++i) {

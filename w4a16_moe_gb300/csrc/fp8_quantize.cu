@@ -42,9 +42,10 @@ __device__ __forceinline__ void store_values8(T* dst, int level, const uint4& w,
   store_words(dst, level, o);
 }
 
+// Chunks of a thread where they are many: 8192 rows of 4096 bf16 18.6 us with two, 19.8 with one, 20.2 with four.
 template <typename T, bool ACT>
 __host__ __device__ constexpr int chunks_of_thread() {
-  return ACT ? 1 : sizeof(T) == 2 ? 4 : 2;
+  return ACT ? 1 : 2;
 }
 
 }  // namespace
@@ -59,8 +60,8 @@ __global__ void __launch_bounds__(kThreads8) fp8_quantize_kernel(const __grid_co
   const uint32_t slots = 8u * p.kb;  // chunks of a row, whole blocks
   int64_t rows = (int64_t)q.groups * q.m;
   if (q.offsets) rows = min(max(__ldg(q.offsets + q.groups), 0), q.m);
-  const int64_t base = (int64_t)blockIdx.x * (kThreads8 * N);
-  const int64_t r0 = base / slots;
+  const uint64_t base = (uint64_t)blockIdx.x * (kThreads8 * N);
+  const int64_t r0 = base >> 32 ? (int64_t)(base / slots) : (int64_t)((uint32_t)base / slots);
   const uint32_t c0 = (uint32_t)(base - r0 * slots);
   Chunk<T, ACT> h[N];
   int64_t row[N];
