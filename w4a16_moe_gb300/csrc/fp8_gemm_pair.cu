@@ -26,7 +26,12 @@
 // products' issue is shared by two: what those warps looked up or issued themselves held up
 // the chain.
 //
-// Measured: N = K = 4096, 4096 rows 65 us (2.1 PFLOP/s), 8192 x 8192 x 4096 218 us (2.5 PFLOP/s); 64 groups of 192
+// What else counts, each step measured at 4096 rows of N = K = 4096 or 64 groups of 192 rows, N = 2816, K = 2048: stores of outputs
+// by the warps themselves 70.6, through shared memory 67.4, as TMA boxes 65.8; four stages in the ring
+// instead of three where no boxes are staged 104.4 -> 103.3; scales of the next unit looked up under the
+// last stages of this one 112 -> 106; the copying warp's loop without decisions 72.3 -> 65.8.
+//
+// Measured: N = K = 4096, 4096 rows 64 us (2.1 PFLOP/s), 8192 x 8192 x 4096 213 us (2.6 PFLOP/s); 64 groups of 192
 // rows, N = 2816, K = 2048 103 us.
 
 #include "fp8_mma.cuh"
@@ -39,22 +44,29 @@ cudaError_t ensure_smem_limit(const void* func, size_t bytes);
 namespace fp8 {
 
 constexpr int kPairRows = 256;
-constexpr int kPairSlots = 3;
 constexpr int kPairBox = 64;                    // activation rows of a box
 constexpr int kPairAStage = 128 * 128;
-constexpr int kOutTile = 2 * 32 * 128;          // staged outputs of a warp: 32 rows of two times 64, 128-byte swizzle
 constexpr int kPairWStage = 2 * kWStage;        // both blocks of weight rows
-constexpr size_t kPairOffA = (size_t)kPairSlots * kPairWStage;
-constexpr size_t kPairOffStage = kPairOffA + (size_t)kPairSlots * kPairAStage;
-constexpr size_t kPairOffBars = kPairOffStage + kEpiWarps * kOutTile;
+constexpr int kOutTile = 2 * 32 * 128;          // staged outputs of a warp: 32 rows of two times 64, 128-byte swizzle
 constexpr int kPrefetch = 10;                   // stages of weights asked into L2 ahead of their copies
 constexpr int kAhead = 4;                       // units looked up ahead of the promoting warps
-constexpr int kPairBars = 2 * kPairSlots + 8 + 1 + 2 * kAhead + 4 + 4;
-constexpr size_t kPairOffUnits = (kPairOffBars + 8 * kPairBars + 15) / 16 * 16;
 constexpr int kScaleQuad = 130 * 4;             // scales of four stages: 128 rows, two blocks of weights; two of these
-constexpr size_t kPairOffScales = kPairOffUnits + 16 * kAhead;
-constexpr size_t kPairOffMisc = kPairOffScales + 2 * kScaleQuad * sizeof(float);
-constexpr size_t pair_smem(bool ragged) { return kPairOffMisc + 16 + (ragged ? 2 * sizeof(int) * (kMaxGroups + 1) + sizeof(int) * kThreads / 32 : 0); }
+
+// BOXES: outputs leave as boxes from 64 KB of staging, which costs the ring a fourth stage.
+template <bool BOXES>
+struct PairCfg {
+  static constexpr int kSlots = BOXES ? 3 : 4;
+  static constexpr int kBars = 2 * kSlots + 8 + 1 + 2 * kAhead + 4 + 4;
+  static constexpr size_t a = (size_t)kSlots * kPairWStage;
+  static constexpr size_t stage = a + (size_t)kSlots * kPairAStage;
+  static constexpr size_t bars = stage + kEpiWarps * (BOXES ? kOutTile : kStagePiece);
+  static constexpr size_t units = (bars + 8 * kBars + 15) / 16 * 16;
+  static constexpr size_t scales = units + 16 * kAhead;
+  static constexpr size_t misc = scales + 2 * kScaleQuad * sizeof(float);
+  static constexpr size_t total(bool ragged) {
+    return misc + 16 + (ragged ? 2 * sizeof(int) * (kMaxGroups + 1) + sizeof(int) * kThreads / 32 : 0);
+  }
+};
 
 enum PairH : int { kPlain = 0, kGated = 1, kRelu2 = 2 };
 
@@ -173,12 +185,14 @@ struct Sixteen {
 };
 
 // OUT: 0 bf16, 1 f16, 2 f32 outputs; H: kPlain, or h as the next product's operand.
-template <int OUT, bool RAGGED, int H>
+template <int OUT, bool RAGGED, int H, bool BOXES>
 __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_constant__ Fp8GemmParams p) {
+  using C = PairCfg<BOXES>;
+  constexpr int kPairSlots = C::kSlots;
   extern __shared__ __align__(1024) uint8_t smem[];
-  PairGroups& groups = *reinterpret_cast<PairGroups*>(smem + kPairOffMisc + 16);  // ragged only
-  uint8_t* s_a = smem + kPairOffA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairOffBars);
+  PairGroups& groups = *reinterpret_cast<PairGroups*>(smem + C::misc + 16);  // ragged only
+  uint8_t* s_a = smem + C::a;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::bars);
   uint64_t* empty = full + kPairSlots;                                // the products of both CTAs are through with the slot
   uint64_t* full_acc = empty + kPairSlots;
   uint64_t* empty_acc = full_acc + 4;
@@ -188,10 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   uint64_t* full_scale = empty_unit + kAhead;
   uint64_t* empty_scale = full_scale + 2;
   uint64_t* both_halves = empty_scale + 2;                            // gated: a quarter's two warps have their maxima
-  int4* s_unit = reinterpret_cast<int4*>(smem + kPairOffUnits);       // group, weight unit, first row, rows
-  float* s_scale = reinterpret_cast<float*>(smem + kPairOffScales);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kPairOffMisc);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kPairOffMisc + 4);
+  int4* s_unit = reinterpret_cast<int4*>(smem + C::units);       // group, weight unit, first row, rows
+  float* s_scale = reinterpret_cast<float*>(smem + C::scales);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::misc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const Fp4GemmParams& g = p.g;
@@ -243,57 +257,65 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       // third of what DRAM's latency takes.
       uint32_t i = 0;
       bool ok = true;
-      PairUnit ahead{};
-      int pu = u0, ps = 0;
-      auto known = [&](int u) {
-        PairUnit U = pair_unit<RAGGED>(g, groups, wp, u, rank);
-        U.group = (int)warp_uniform(U.group), U.wt = (int)warp_uniform(U.wt);
-        U.first = (int)warp_uniform(U.first), U.rows = (int)warp_uniform(U.rows);
-        return U;
+      // A CTA's boxes of weights in a stage: of block b of 128 rows (N of accumulator b) for both CTAs, b its
+      // rank, or of wide units both blocks for itself; gated, a block is 64 gate rows and their up rows.
+      struct Boxes {
+        int row, first, rows;
+        bool wide, none;
       };
-      // f(place in the stage's weights, first weight row) of the CTA's boxes.  Block b of 128 rows is N of the
-      // stage's accumulator b.
-      auto each_box = [&](const PairUnit& U, auto f) {
-        const int base = U.group * g.n;
-        if (U.wide && U.wt >= wp) return;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (!U.wide && b != (int)rank) continue;  // the other CTA's
-          if constexpr (H == kGated) {
-            f(b * kWStage, base + U.wt * 128 + b * 64);
-            f(b * kWStage + kWStage / 2, base + g.n / 2 + U.wt * 128 + b * 64);
-          } else {
-            f(b * kWStage, base + U.wt * 256 + b * 128);
+      auto boxes_of = [&](int u) {
+        const PairUnit U = pair_unit<RAGGED>(g, groups, wp, u, rank);
+        Boxes B;
+        B.wide = U.wide;
+        B.none = U.wide && U.wt >= wp;
+        B.row = (int)warp_uniform(U.group * g.n + U.wt * (H == kGated ? 128 : 256) + (U.wide ? 0 : (int)rank * (H == kGated ? 64 : 128)));
+        B.first = (int)warp_uniform(U.first);
+        B.rows = (int)warp_uniform(U.rows);
+        return B;
+      };
+      Boxes ahead{};
+      int pu = u0, ps = 0;
+      auto prefetch = [&]() {
+        if (!RAGGED || pu >= n_units) return;
+        if (ps == 0) ahead = boxes_of(pu);
+        if (!ahead.none && elect_one()) {
+          tma_prefetch_2d(&p.tmap_w, ps * 128, ahead.row);
+          if (H == kGated) tma_prefetch_2d(&p.tmap_w, ps * 128, ahead.row + g.n / 2);
+          if (ahead.wide) {
+            tma_prefetch_2d(&p.tmap_w, ps * 128, ahead.row + (H == kGated ? 64 : 128));
+            if (H == kGated) tma_prefetch_2d(&p.tmap_w, ps * 128, ahead.row + g.n / 2 + 64);
           }
         }
-      };
-      auto prefetch = [&]() {
-        if (pu >= n_units) return;
-        if (ps == 0) ahead = known(pu);
-        if (elect_one()) each_box(ahead, [&](int, int row) { tma_prefetch_2d(&p.tmap_w, ps * 128, row); });
         __syncwarp();
         if (++ps == p.kb) ps = 0, pu += du;
       };
       for (int j = 0; j < kPrefetch; ++j) prefetch();
       if (g.a_is_new) pdl_wait();
       for (int u = u0; u < n_units && ok; u += du) {
-        const PairUnit U = known(u);
-        const int boxes = cdiv(U.rows, kPairBox);
-        const uint32_t bytes = (U.wide && U.wt >= wp ? 0 : kPairWStage) + boxes * kPairBox * 128;
+        const Boxes B = boxes_of(u);
+        const uint32_t bytes = (B.none ? 0 : kPairWStage) + cdiv(B.rows, kPairBox) * kPairBox * 128;
+        uint8_t* sw0 = smem + (B.wide ? 0 : rank * kWStage);
         for (int s = 0; s < p.kb; ++s, ++i) {
           const uint32_t slot = i % kPairSlots;
           ok = __all_sync(0xffffffffu, wait(&empty[slot], ((i / kPairSlots) & 1) ^ 1, ab, 131));
           if (!ok) break;
           if (elect_one()) {
             mbar_arrive_expect_tx(&full[slot], bytes);
-            uint8_t* sw = smem + slot * kPairWStage;
-            each_box(U, [&](int at, int row) {
-              if (U.wide) tma_load_2d(sw + at, &p.tmap_w, s * 128, row, &full[slot]);
-              else tma_load_2d_both(sw + at, &p.tmap_w, s * 128, row, &full[slot]);
-            });
-            if (boxes > 0) tma_load_2d(s_a + slot * kPairAStage, &p.tmap_a, s * 128, U.first, &full[slot]);
-            if (boxes > 1)
-              tma_load_2d(s_a + slot * kPairAStage + kPairBox * 128, &p.tmap_a, s * 128, U.first + kPairBox, &full[slot]);
+            uint8_t* sw = sw0 + slot * kPairWStage;
+            if (!B.wide) {
+              tma_load_2d_both(sw, &p.tmap_w, s * 128, B.row, &full[slot]);
+              if (H == kGated) tma_load_2d_both(sw + kWStage / 2, &p.tmap_w, s * 128, B.row + g.n / 2, &full[slot]);
+            } else if (!B.none) {
+              tma_load_2d(sw, &p.tmap_w, s * 128, B.row, &full[slot]);
+              tma_load_2d(sw + kWStage, &p.tmap_w, s * 128, B.row + (H == kGated ? 64 : 128), &full[slot]);
+              if (H == kGated) {
+                tma_load_2d(sw + kWStage / 2, &p.tmap_w, s * 128, B.row + g.n / 2, &full[slot]);
+                tma_load_2d(sw + kWStage * 3 / 2, &p.tmap_w, s * 128, B.row + g.n / 2 + 64, &full[slot]);
+              }
+            }
+            if (B.rows > 0) tma_load_2d(s_a + slot * kPairAStage, &p.tmap_a, s * 128, B.first, &full[slot]);
+            if (B.rows > kPairBox)
+              tma_load_2d(s_a + slot * kPairAStage + kPairBox * 128, &p.tmap_a, s * 128, B.first + kPairBox, &full[slot]);
           }
           __syncwarp();
           prefetch();
@@ -355,54 +377,57 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       // --- units and scales for the promoting warps, ahead of them (their registers are all taken, and
       // what they look up themselves holds up their sums); rows past the last group are zero
       if (g.a_is_new) pdl_wait();
-      uint32_t i = 0, n = 0;
+      // Four stages of a unit at a time, looked up eight stages ahead of their turn, into the next
+      // unit too: a load from L2 takes a microsecond and more under the operands' traffic.
+      const float *sa[4], *sw;  // of rows lane, lane + 32, ..; lanes 0 and 1: of the accumulators' weight rows
+      int lu = u0, ls = 0;      // looked up next
+      uint32_t n = 0;
       bool ok = true;
-      for (int u = u0; u < n_units && ok; u += du, ++n) {
-        const PairUnit U = pair_unit<RAGGED>(g, groups, wp, u, rank);
+      auto enter = [&]() {  // unit lu: told to the promoters, its scales found
+        const PairUnit U = pair_unit<RAGGED>(g, groups, wp, lu, rank);
         const uint32_t b = n % kAhead;
-        ok = __all_sync(0xffffffffu, wait(&empty_unit[b], ((n / kAhead) & 1) ^ 1, ab, 135));
-        if (!ok) break;
-        if (lane == 0) {
+        ok = ok && __all_sync(0xffffffffu, wait(&empty_unit[b], ((n / kAhead) & 1) ^ 1, ab, 135));
+        if (ok && lane == 0) {
           s_unit[b] = make_int4(U.group, U.wt, U.first, U.rows);
           mbar_arrive(&full_unit[b]);
         }
         __syncwarp();
-        const float* sa[4];  // rows lane, lane + 32, ... (a unit without rows here: its first CTA's)
+        ++n;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j)  // (a CTA without rows in the unit: any)
           sa[j] = p.a_scales + (int64_t)(U.rows > 0 ? U.first + min(32 * j + lane, U.rows - 1) : 0) * p.kb;
-        // of the accumulators' weight rows; gated: of the gate rows and of the up rows
-        const int t0 = min(H == kGated ? U.wt : 2 * U.wt, wtiles - 1);
-        const int t1 = min(H == kGated ? U.wt + wtiles / 2 : t0 + 1, wtiles - 1);
-        const float* sw0 = p.w_scales + ((int64_t)U.group * wtiles + t0) * p.kb;
-        const float* sw1 = p.w_scales + ((int64_t)U.group * wtiles + t1) * p.kb;
-        // four stages at a time, loaded eight stages ahead
-        float4 next[2][4], w[2];
-        auto load = [&](int s, int d) {
-          if (lane < 2) w[d] = load_scales(lane == 0 ? sw0 : sw1, s, p.kb, p.w_vec);
+        // gated: the gate rows' and the up rows'
+        const int t = H == kGated ? U.wt + (lane & 1) * (wtiles / 2) : 2 * U.wt + (lane & 1);
+        sw = p.w_scales + ((int64_t)U.group * wtiles + min(t, wtiles - 1)) * p.kb;
+      };
+      float4 next[2][4], w[2];
+      auto look_up = [&](int d) {
+        if (lu >= n_units) return;
+        if (ls == 0) enter();
+        w[d] = load_scales(sw, ls, p.kb, p.w_vec);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) next[d][j] = load_scales(sa[j], s, p.kb, p.a_vec);
-        };
-        load(0, 0);
-        load(4, 1);
-        for (int s = 0; s < p.kb && ok; s += 8) {
+        for (int j = 0; j < 4; ++j) next[d][j] = load_scales(sa[j], ls, p.kb, p.a_vec);
+        ls += 4;
+        if (ls >= p.kb) ls = 0, lu += du;
+      };
+      look_up(0);
+      look_up(1);
+      const int quads = u0 < n_units ? ((n_units - 1 - u0) / du + 1) * cdiv(p.kb, 4) : 0;
+      for (int i = 0; i < quads && ok; i += 2) {
 #pragma unroll
-          for (int d = 0; d < 2; ++d)
-            if (s + 4 * d < p.kb && ok) {
-              const uint32_t q = i & 1;
-              ok = __all_sync(0xffffffffu, wait(&empty_scale[q], ((i >> 1) & 1) ^ 1, ab, 137));
-              if (ok) {
-                float4* to = reinterpret_cast<float4*>(s_scale + q * kScaleQuad) + lane;
+        for (int d = 0; d < 2; ++d)
+          if (i + d < quads && ok) {
+            ok = __all_sync(0xffffffffu, wait(&empty_scale[d], ((i >> 1) & 1) ^ 1, ab, 137));
+            if (ok) {
+              float4* to = reinterpret_cast<float4*>(s_scale + d * kScaleQuad) + lane;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) to[32 * j] = next[d][j];
-                if (lane < 2) to[128] = w[d];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full_scale[q]);
-                load(s + 4 * d + 8, d);
-              }
-              ++i;
+              for (int j = 0; j < 4; ++j) to[32 * j] = next[d][j];
+              if (lane < 2) to[128] = w[d];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&full_scale[d]);
+              look_up(d);
             }
-        }
+          }
       }
       if (H == kPlain && RAGGED && !g.out_rows) clear_tail<32>(g, groups.first[g.groups], lane);
     }
@@ -414,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
     const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + 128 * half;
     uint64_t* mine_acc = full_acc + half;  // this warp's two accumulators: 2 apart
     uint64_t* done = empty_acc + half;
-    uint8_t* stage = smem + kPairOffStage + (warp - 4) * kOutTile;
+    uint8_t* stage = smem + C::stage + (warp - 4) * (BOXES ? kOutTile : kStagePiece);
     const float4* scales = reinterpret_cast<const float4*>(s_scale);
     uint32_t i = 0, n = 0, quad = 0, done_units = 0;
     bool ok = true;
@@ -498,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
           a = max(a, max(__float_as_uint(acc[c].x) & 0x7fffffffu, __float_as_uint(acc[c].y) & 0x7fffffffu));
         }
         if constexpr (H == kGated) {
-          uint32_t* most = reinterpret_cast<uint32_t*>(smem + kPairOffStage) + (done_units & 1) * 256;
+          uint32_t* most = reinterpret_cast<uint32_t*>(smem + C::stage) + (done_units & 1) * 256;
           most[half * 128 + r] = a;
           __syncwarp();
           if (lane == 0) mbar_arrive(&both_halves[q4]);
@@ -516,12 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
           for (int c = 0; c < kCols / 8; ++c) codes[c] = fp8q::encode8<false>(Sixteen{acc + 8 * c}, s);
           if (H != kGated || half == 0) p.q.scales[(int64_t)to * (width / 128) + at / 128] = s;
         }
-      } else if (OUT < 2 && g.vec) {
+      } else if constexpr (BOXES) {
         // Through shared memory.  Full tiles leave from there as boxes of 32 rows x 64, under the next
         // unit: stores of all SMs at once take 4000 cycles to drain, and what the warp does next
-        // queues behind them.  Others (rows by an index, the end of a group) as 256 bytes of two
-        // rows a store.
-        const bool boxes = p.out_boxes && (__all_sync(0xffffffffu, to >= 0) || (!RAGGED && g.groups == 1));
+        // queues behind them.  Others (the end of a group) as 256 bytes of two rows a store.
+        const bool boxes = __all_sync(0xffffffffu, to >= 0) || (!RAGGED && g.groups == 1);
         if (lane == 0) bulk_wait_read();
         __syncwarp();
 #pragma unroll
@@ -561,17 +585,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
     }
   }
 
-  if (warp >= 4 && lane == 0) bulk_wait();  // the boxes have left
+  if (BOXES && warp >= 4 && lane == 0) bulk_wait();  // the boxes have left
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the pair's copies, products or signals may touch it
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int OUT, bool RAGGED, int H>
+template <int OUT, bool RAGGED, int H, bool BOXES>
 cudaError_t launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t stream) {
-  auto kern = fp8_pair_kernel<OUT, RAGGED, H>;
-  const size_t smem = pair_smem(RAGGED);
+  auto kern = fp8_pair_kernel<OUT, RAGGED, H, BOXES>;
+  const size_t smem = PairCfg<BOXES>::total(RAGGED);
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -594,14 +618,18 @@ cudaError_t launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t stream) 
 }  // namespace fp8
 
 cudaError_t launch_fp8_gemm_pair(const Fp8GemmParams& p, int pairs, cudaStream_t stream) {
-  return fp8::with_out(
-      p, [&](auto out, auto ragged) { return fp8::launch_pair<out.value, ragged.value, fp8::kPlain>(p, pairs, stream); });
+  return fp8::with_out(p, [&](auto out, auto ragged) {
+    constexpr int O = out.value;
+    constexpr bool G = ragged.value;
+    return p.out_boxes ? fp8::launch_pair<O & 1, G, fp8::kPlain, true>(p, pairs, stream)
+                       : fp8::launch_pair<O, G, fp8::kPlain, false>(p, pairs, stream);
+  });
 }
 
 // The first product of a layer: p.q takes h (codes, scales, glu).
 cudaError_t launch_fp8_gemm_h(const Fp8GemmParams& p, bool gated, int pairs, cudaStream_t stream) {
-  return gated ? fp8::launch_pair<0, true, fp8::kGated>(p, pairs, stream)
-               : fp8::launch_pair<0, true, fp8::kRelu2>(p, pairs, stream);
+  return gated ? fp8::launch_pair<0, true, fp8::kGated, false>(p, pairs, stream)
+               : fp8::launch_pair<0, true, fp8::kRelu2, false>(p, pairs, stream);
 }
 
 }  // namespace b4
