@@ -6,7 +6,9 @@
  * SiLU-SwiGLU, clamped swiglu or ReLU^2 epilogue, and a grouped FC2 GEMM whose store folds in
  * the top-k weighted sum, plus a separate small-m decode path.  It is the
  * layer described by flashinfer PR #4255, "feat(moe): sync SM12x W4A16 fused
- * MoE family to b12x HEAD" (Description), restated for GB300.
+ * MoE family to b12x HEAD" (Description), restated for GB300.  Beside it, without a
+ * counterpart there: the choice of experts from router logits, products of FP4 and of
+ * FP8 operands, and the layer with 4-bit and with 8-bit activations.
  *
  * Conventions for every entry point
  * ---------------------------------
@@ -590,7 +592,8 @@ b4_status b4_fp8_matmul(const b4_fp8_config* cfg, const uint8_t* a_codes, const 
                         uint32_t* device_status, b4_stream_t stream);
 
 /* b4_fp8_quantize of x into the workspace, then b4_fp8_matmul: 2 launches, the second set up
- * under the first.  num_groups is 1 unless offsets is given.
+ * under the first, or 1 where at most 8 rows are quantised by the product's own kernel (the
+ * same bits).  num_groups is 1 unless offsets is given.
  * workspace: >= b4_fp8_linear_workspace_bytes(cfg), 256-byte aligned; holds the status word
  * that b4_check_status reads. */
 size_t b4_fp8_linear_workspace_bytes(const b4_fp8_config* cfg);
@@ -599,12 +602,14 @@ b4_status b4_fp8_linear(const b4_fp8_config* cfg, const void* x, const int32_t* 
                         void* workspace, size_t workspace_bytes, b4_stream_t stream);
 
 /* The fused MoE layer with 8-bit weights and activations: route packing, x rows gathered and
- * quantised, grouped FC1 (fp32 out), activation and quantisation, grouped FC2 stored in route
- * order (bf16), and the weighted sum of each token's valid routes in fp32 with one rounding.
+ * quantised, grouped FC1, activation and quantisation of its fp32 sums, grouped FC2 stored in
+ * route order (rounded to bf16), and the weighted sum of each token's valid routes in fp32 with
+ * one more rounding.
  * cfg, routing and activations as b4_fused_moe (cfg->format and cfg->path are not read; hidden
  * and inter multiples of 16); weights as quantised operands: w13 [E_l][2 I or I][H] with gate
  * rows first and s13 [E_l][ceil(rows / 128)][ceil(H / 128)], w2 [E_l][H][I] and s2 likewise.
- * 6 launches. */
+ * 6 launches; 5 where FC1's own kernel leaves h quantised (experts of many rows, inter a
+ * multiple of 128); fewer for up to 8 routes. */
 size_t b4_fused_moe_fp8_workspace_bytes(const b4_moe_config* cfg, int32_t activation);
 b4_status b4_fused_moe_fp8(const b4_moe_config* cfg, const uint16_t* x, const uint8_t* w13, const float* s13,
                            const uint8_t* w2, const float* s2, const int32_t* topk_ids, const float* topk_weights,

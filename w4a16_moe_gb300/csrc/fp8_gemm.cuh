@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         const uint32_t wd = w_desc + slot * (kWStage / 16);
         const uint32_t ad = a_desc + (DIRECT ? i * (kFp8DirectTile * 128 / 16) : slot * (C::kAStage / 16));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_fp8<1>(tmem + acc * 128, ad + 2 * j, wd + 2 * j, idesc, j > 0);
+        for (int j = 0; j < 4; ++j) mma_fp8(tmem + acc * 128, ad + 2 * j, wd + 2 * j, idesc, j > 0);
         mma_commit(&full_acc[acc]);
         mma_commit(&empty[slot]);
       }

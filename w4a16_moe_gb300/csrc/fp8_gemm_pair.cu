@@ -5,34 +5,33 @@
 // rows.  Both need all of the weight rows: each CTA loads a block of 128 of them and multicasts
 // it to both, so an SM asks L2 for 32 KB a stage of 128 K and takes in 48 KB, for 512 cycles
 // of products (measured with copies alone: 480 cycles a stage on all SMs, 756 without
-// sharing).
+// sharing).  The rows that are left of a group, 128 or fewer, make wide units: both CTAs take
+// them, each with 256 weight rows of its own and without sharing.
 //
-// The rows that are left of a group, 128 or fewer, make wide units: both CTAs take them, each
-// with 256 weight rows of its own and without sharing.
-//
-// H: the product is the first of a layer (b4_fused_moe_fp8).  A unit's sums become h, 128 columns of a
-// gated activation (its weight rows are 128 gate rows and the 128 up rows that go with them, 64 of each
-// in an accumulator, so that a lane holds both of a column) or 256 of ReLU^2, and h leaves quantised,
-// codes and scales as b4_fp8_quantize writes them: it never goes to memory in 32 bits.
+// H: the product is the first of a layer (b4_fused_moe_fp8).  A unit's sums become h, 128
+// columns of a gated activation (its weight rows are 128 gate rows and the 128 up rows that go
+// with them, 64 of each in an accumulator, so that a lane holds both of a column) or 256 of
+// ReLU^2, and h leaves quantised, codes and scales as b4_fp8_quantize writes them: it never
+// goes to memory in 32 bits.
 //
 // A stage is one block of K.  It has two accumulators of 128 columns, one for each block of 128
 // weight rows, twice: while the tensor core fills one of each pair, four warps read the other,
 // 32 lanes x 128 columns each, and add it to fp32 registers times the row's scale and the
-// weights'.  What is in tensor memory, 512 columns, takes a chain of steps to renew: 256 cycles
-// of products, 270 until a waiting warp has seen them done, 500 of promotion (of which 350 are
-// the loads and multiply-adds of two warps a scheduler), 200 until the next products issue; that
-// chain, 760 to 830 cycles for two stages' worth of one half, is what bounds the kernel, not
-// the 512 cycles of products.  Scales come through shared memory from a warp of their own, and the
-// products' issue is shared by two: what those warps looked up or issued themselves held up
-// the chain.
+// weights'.  Tensor memory, 512 columns, is renewed by a chain of steps: 256 cycles of
+// products, 270 until a waiting warp has seen them done, 500 of promotion (of which 350 are
+// the loads and multiply-adds of two warps a scheduler), 200 until the next products issue.
+// That chain, 760 to 830 cycles a stage, bounds the kernel, not the 512 cycles of products.
+// Scales come through shared memory from warps of their own, and two warps share the
+// products' issue: what these looked up or issued for themselves held up the chain.
 //
-// What else counts, each step measured at 4096 rows of N = K = 4096 or 64 groups of 192 rows, N = 2816, K = 2048: stores of outputs
-// by the warps themselves 70.6, through shared memory 67.4, as TMA boxes 65.8; four stages in the ring
-// instead of three where no boxes are staged 104.4 -> 103.3; scales of the next unit looked up under the
-// last stages of this one 112 -> 106; the copying warp's loop without decisions 72.3 -> 65.8.
+// What else counts.  4096 rows of N = K = 4096: outputs stored by the warps from registers
+// 70.6 us, through shared memory 67.4, as TMA boxes 65.8; the copying warp's loop with
+// decisions in it 72.3, without 65.8.  64 groups of 192 rows, N = 2816, K = 2048: scales of a
+// unit looked up at its start 112, under the last stages of the one before 106; three stages
+// in the ring 104.4, four where no boxes are staged 103.3.
 //
-// Measured: N = K = 4096, 4096 rows 64 us (2.1 PFLOP/s), 8192 x 8192 x 4096 213 us (2.6 PFLOP/s); 64 groups of 192
-// rows, N = 2816, K = 2048 103 us.
+// Measured: N = K = 4096, 4096 rows 64 us (2.1 PFLOP/s), 8192 x 8192 x 4096 213 us (2.6
+// PFLOP/s); 64 groups of 192 rows, N = 2816, K = 2048 103 us.
 
 #include "fp8_mma.cuh"
 #include "fp8_quant.cuh"
@@ -351,14 +350,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
         const uint32_t wd = w_desc + slot * (kPairWStage / 16), ad = a_desc + slot * (kPairAStage / 16);
         if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_fp8<1>(d, ad + 2 * j, wd + 2 * j, idesc, j > 0);
+          for (int j = 0; j < 4; ++j) mma_fp8(d, ad + 2 * j, wd + 2 * j, idesc, j > 0);
           mma_commit(&full_acc[2 * w]);
         }
         if (!__all_sync(0xffffffffu, look) && !__all_sync(0xffffffffu, wait(&empty_acc[2 * w + 1], acc_phase, ab, 132))) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_fp8<1>(d + 128, ad + 2 * j, wd + kWStage / 16 + 2 * j, idesc, j > 0);
+          for (int j = 0; j < 4; ++j) mma_fp8(d + 128, ad + 2 * j, wd + kWStage / 16 + 2 * j, idesc, j > 0);
           mma_commit(&full_acc[2 * w + 1]);
           mma_commit_both(&empty[slot]);
         }

@@ -14,18 +14,13 @@ using namespace fp4;
 __device__ __forceinline__ constexpr uint32_t idesc_fp8(uint32_t m, uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
-// D (+)= A B^T, both operands in shared memory with the 128-byte swizzle; CG CTAs of a pair.
-template <int CG>
+// D (+)= A B^T, both operands in shared memory with the 128-byte swizzle.
 __device__ __forceinline__ void mma_fp8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-#define FP8_MMA(group)                                                                                               \
-  asm volatile(                                                                                                      \
-      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, " \
-      "%5};\n\ttcgen05.mma.cta_group::" group ".kind::f8f6f4 [%0], x, y, %3, p;\n\t}" ::"r"(d),                     \
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHiSw128)                                                 \
-      : "memory")
-  if constexpr (CG == 1) FP8_MMA("1");
-  else FP8_MMA("2");
-#undef FP8_MMA
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, "
+      "%5};\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHiSw128)
+      : "memory");
 }
 // A box into the same place of both CTAs' shared memory, each CTA's barrier counting its copy.
 __device__ __forceinline__ void tma_load_2d_both(void* dst, const CUtensorMap* tm, int c0, int r0, uint64_t* bar) {
