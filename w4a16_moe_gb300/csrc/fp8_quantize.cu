@@ -6,19 +6,20 @@
 //   c = e4m3(h / s), nearest even of the quotient in fp32; a block with an infinity or a
 //       NaN has the scale NaN
 //
-// A thread takes 16 consecutive elements: a 32-byte load (two of fp32) and a 16-byte store
-// of codes; eight neighbouring threads are a block of 128 and join their maxima by three
-// shuffles.  The quotient is h y + h z in one fused multiply-add, y an approximate reciprocal of
-// s and z what it lacks: to 46 bits before its rounding, two operations an element.
+// A thread takes pieces of 16 consecutive elements, one, two or four of a block of 128: a
+// 32-byte load (two of fp32) and a 16-byte store of codes each; the block's threads are
+// neighbours and join their maxima by shuffles.  The quotient is h y + h z in one fused
+// multiply-add, y an approximate reciprocal of s and z what it lacks: to 46 bits before its
+// rounding, two operations an element.
 //
 // Bound by DRAM where x comes from there; gathered rows, which L2 holds, by the issue of
 // instructions.  A 128 x 128 block is read once and stays in the registers of 512 threads
 // between its maximum and its codes (with 256 threads 145 us for the second line below).
 //
-// Measured, codes, scales and values: 8192 rows of 4096 bf16 25.5 us (169 MB, 6.6 TB/s); 16 fp32
-// matrices of 2816 x 2048 127 us (830 MB, 6.5 TB/s).
+// Measured: 8192 rows of 4096 bf16 16.8 us (6.0 TB/s), with values too 26.4 (6.4 TB/s); 12288 gathered rows
+// of 2048 10.4; 16 fp32 matrices of 2816 x 2048, values too, 127 us (6.5 TB/s).
 
-#include <algorithm>
+#include <type_traits>
 
 #include "fp8_quant.cuh"
 
@@ -49,59 +50,54 @@ __device__ __forceinline__ void store_values8(T* dst, int level, const uint4& w,
   store_words(dst, level, o);
 }
 
-// Chunks of a thread where they are many: 8192 rows of 4096 bf16 18.6 us with two, 19.8 with one, 20.2 with four.
-template <typename T, bool ACT>
-__host__ __device__ constexpr int chunks_of_thread() {
-  return ACT ? 1 : 2;
-}
-
 }  // namespace
 
-// A scale per row and 128 columns.
+// A scale per row and 128 columns: 8 / N threads take a block, N chunks each, and share its scale.
 template <typename T, bool ACT, bool POW2, int N>
 __global__ void __launch_bounds__(kThreads8) fp8_quantize_kernel(const __grid_constant__ Fp8QuantParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const Fp4QuantParams& q = p.q;
   if (q.status && blockIdx.x == 0 && threadIdx.x < 2) q.status[threadIdx.x] = 0;
-  const uint32_t slots = 8u * p.kb;  // chunks of a row, whole blocks
+  constexpr int kLanes = 8 / N;                // of a block
+  const uint32_t slots = kLanes * p.kb;        // threads of a row
   int64_t rows = (int64_t)q.groups * q.m;
   if (q.offsets) rows = min(max(__ldg(q.offsets + q.groups), 0), q.m);
-  const uint64_t base = (uint64_t)blockIdx.x * (kThreads8 * N);
-  const int64_t r0 = base >> 32 ? (int64_t)(base / slots) : (int64_t)((uint32_t)base / slots);
-  const uint32_t c0 = (uint32_t)(base - r0 * slots);
+  const uint64_t base = (uint64_t)blockIdx.x * kThreads8;
+  int64_t row = base >> 32 ? (int64_t)(base / slots) : (int64_t)((uint32_t)base / slots);
+  uint32_t j = (uint32_t)(base - row * slots) + threadIdx.x;
+  while (j >= slots) j -= slots, ++row;  // (seldom more than twice: cheaper than a division)
+  const uint32_t block = j / kLanes;
+  const int chunk = (int)(8 * block + j % kLanes);  // and every kLanes-th of the block's from there
+  const bool live = row < rows;
+  int64_t src = row;
+  if (q.rows && live) {
+    const int r = __ldg(q.rows + row);
+    src = r < 0 ? -1 : r / q.row_div;
+    if (q.x_rows > 0 && src >= q.x_rows) src = -1;
+  }
   Chunk<T, ACT> h[N];
-  int64_t row[N];
-  int chunk[N];
-  bool live[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const uint32_t j = c0 + i * kThreads8 + threadIdx.x;
-    row[i] = r0 + j / slots;
-    chunk[i] = (int)(j % slots);
-    live[i] = row[i] < rows;
-    int64_t src = row[i];
-    if (q.rows && live[i]) {
-      const int r = __ldg(q.rows + row[i]);
-      src = r < 0 ? -1 : r / q.row_div;
-      if (q.x_rows > 0 && src >= q.x_rows) src = -1;
-    }
-    if (live[i] && src >= 0 && 16 * chunk[i] < q.k)
-      h[i].get(q, reinterpret_cast<const T*>(q.x) + src * q.x_stride, chunk[i]);
+    if (live && src >= 0 && 16 * (chunk + kLanes * i) < q.k)
+      h[i].get(q, reinterpret_cast<const T*>(q.x) + src * q.x_stride, chunk + kLanes * i);
     else h[i].zero();
   }
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) a = max(a, h[i].amax());
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+  const float s = block_scale<POW2>(a);
+  if (!live) return;
+  if (j % kLanes == 0) p.scales[row * p.kb + block] = s;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    uint32_t a = h[i].amax();
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float s = block_scale<POW2>(a);
-    if (!live[i]) continue;
-    if ((chunk[i] & 7) == 0) p.scales[row[i] * p.kb + (chunk[i] >> 3)] = s;
-    if (16 * chunk[i] < q.k) {
+    const int c = chunk + kLanes * i;
+    if (16 * c < q.k) {
       const uint4 w = encode8<POW2>(h[i], s);
-      *reinterpret_cast<uint4*>(q.codes + row[i] * q.ld + 16 * chunk[i]) = w;
-      if (q.values) store_values8(reinterpret_cast<T*>(q.values) + row[i] * q.k + 16 * chunk[i], q.values_vec, w, s);
+      *reinterpret_cast<uint4*>(q.codes + row * q.ld + 16 * c) = w;
+      if (q.values) store_values8(reinterpret_cast<T*>(q.values) + row * q.k + 16 * c, q.values_vec, w, s);
     }
   }
 }
@@ -172,9 +168,19 @@ cudaError_t quantize8(const Fp8QuantParams& p, int block_rows, int sms, cudaStre
     return launch8(fp8_quantize_block_kernel<T, ACT, POW2>, (int64_t)q.groups * cdiv(q.m, kFp8Block) * p.kb, kBlockThreads,
                    stream, p);
   const int64_t chunks = (q.offsets ? q.m : (int64_t)q.groups * q.m) * p.kb * 8;
-  constexpr int N = chunks_of_thread<T, ACT>();
-  if (chunks <= (int64_t)sms * 512) return launch8(fp8_quantize_kernel<T, ACT, POW2, 1>, (chunks + kThreads8 - 1) / kThreads8, kThreads8, stream, p);
-  return launch8(fp8_quantize_kernel<T, ACT, POW2, N>, (chunks + kThreads8 * N - 1) / (kThreads8 * N), kThreads8, stream, p);
+  auto run = [&](auto n) {
+    constexpr int N = n.value;
+    return launch8(fp8_quantize_kernel<T, ACT, POW2, N>, (chunks / N + kThreads8 - 1) / kThreads8, kThreads8, stream, p);
+  };
+  // Chunks of a thread: more share a block's scale and a row's index among more elements, but leave
+  // fewer threads to hide latencies.  In us with 1 / 2 / 4: 16-bit x, 512 rows of 4096 - / 2.5 / 2.8, 2036
+  // gathered rows of 2880 - / 4.0 / 5.0, 12288 of 2048 14.6 / 11.4 / 10.4, 8192 rows of 4096 19.4 / 17.1 / 16.8; fp32
+  // - / 27.2 / 33.7; behind SwiGLU, 12288 rows of 1408 fp32 24.1 / 25.1 / 29.6.
+  if constexpr (!ACT) {
+    if (sizeof(T) == 2 && chunks > (int64_t)sms * 2560) return run(std::integral_constant<int, sizeof(T) == 2 ? 4 : 2>{});
+    if (chunks > (int64_t)sms * 512) return run(std::integral_constant<int, 2>{});
+  }
+  return run(std::integral_constant<int, 1>{});
 }
 
 template <typename T>
