@@ -2,7 +2,9 @@
 
 A thin Python binding over the C ABI of ``libb4moe.so`` (``include/b4moe.h``):
 argument marshalling only -- every step of the layer runs in the library's
-CUDA kernels.  Tensors are torch CUDA tensors (torch serves as the device
+CUDA kernels.  Beside the layer stand the choice of experts (``route_topk``),
+the products of FP4 and FP8 operands (``fp4_*``, ``fp8_*``) and the layers of
+these (``fused_moe_a4``, ``fused_moe_fp8``).  Tensors are torch CUDA tensors (torch serves as the device
 allocator and stream provider); their data pointers are handed to the C
 entry points as plain addresses.
 
