@@ -25,7 +25,7 @@
 // K.  The partial sums go to the first CTA's shared memory as asynchronous stores that count
 // on its barrier, and it adds them in rank order, so the result does not depend on timing.
 //
-// Measured: 64 groups of 6 rows, N = 2816, K = 2048 61.4 us (372 MB, 6.1 TB/s), of 96 rows 70.5 us (5.9 TB/s); one row, N = K = 4096
+// Measured: 64 groups of 6 rows, N = 2816, K = 2048 60.7 us (372 MB, 6.1 TB/s), of 96 rows 70 us (5.9 TB/s); one row, N = K = 4096
 // 7.6 us, direct 7.7; eight groups of one row, N = 1536, K = 4096 (50 MB) direct 13.5 us: 96 CTAs of a unit each,
 // whose 32 stages follow one another.
 //
@@ -271,45 +271,57 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     // ---- scales, stages by turns; rows of a ragged output past the last group are zero
     if (g.a_is_new) pdl_wait();
     if constexpr (!DIRECT) {
-      constexpr int kTurn = C::kScalers;
-      uint32_t i0 = 0;  // stages of the units before
-      bool ok = true;
-      for (int u = u0; u < n_units && ok; u += du, i0 += s_end - s_beg) {
-        const Unit U = get_unit<ROWS, RAGGED>(g, groups, wtiles, u);
-        const float* sw = p.w_scales + ((int64_t)U.group * wtiles + U.wtile) * p.kb;
-        constexpr int kPer = ROWS / 32;
-        constexpr int kDeep = 8 / kTurn;  // stages of this warp loaded ahead
-        float v[kDeep][kPer];
-        auto load = [&](int s, float (&to)[kPer]) {
-          const float f = s < s_end ? __ldg(sw + s) : 0.f;
+      // Looked up kDeep stages of this warp ahead of their turn, into the next unit too: a load from L2
+      // takes a microsecond and more under the weights' traffic (64 groups of 6 rows, N = 2048, K = 1408
+      // 34.0 us with each unit for itself, 32.8).  No deeper: in a layer, whose kernels follow one another, a
+      // launch fetches its code anew (8 deep, twice unrolled: 64 tokens, 6 of 64 experts 118 us, 111 so).
+      constexpr int kTurn = C::kScalers, kPer = ROWS / 32;
+      constexpr int kDeep = 4;
+      const int stages = s_end - s_beg;
+      const int total = u0 < n_units ? (SPLIT ? 1 : (n_units - 1 - u0) / du + 1) * stages : 0;
+      const int i0 = kTurn == 2 ? warp & 1 : 0;
+      const float *sw = p.w_scales, *sa[kPer];  // of unit lu, its rows lane, lane + 32, ..
+      bool live[kPer];
+      int lu = u0 - du, ls = s_beg + i0 + stages;  // looked up next (the first: stage i0 of the first unit)
+      float f[kDeep], v[kDeep][kPer];
+      auto look_up = [&](int d) {
+        while (ls >= s_end) {
+          ls -= stages;
+          lu += du;
+          if (ls >= s_end) continue;
+          if (lu >= n_units) return;
+          const Unit U = get_unit<ROWS, RAGGED>(g, groups, wtiles, lu);
+          sw = p.w_scales + ((int64_t)U.group * wtiles + U.wtile) * p.kb;
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
-            const int r = 32 * j + lane;
-            to[j] = s < s_end && r < U.rows ? f * p.a_scales[(int64_t)(U.first + r) * p.kb + s] : 0.f;
+            live[j] = 32 * j + lane < U.rows;
+            sa[j] = p.a_scales + (int64_t)(U.first + (live[j] ? 32 * j + lane : 0)) * p.kb;
           }
-        };
-        // the stages whose number (all units') leaves this warp's turn
-        int s = s_beg + (kTurn == 2 ? (int)((i0 + warp) & 1) : 0);
+        }
+        if (lu >= n_units) return;
+        f[d] = __ldg(sw + ls);
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d) load(s + kTurn * d, v[d]);
-        while (s < s_end && ok) {
+        for (int j = 0; j < kPer; ++j) v[d][j] = live[j] ? sa[j][ls] : 0.f;
+        ls += kTurn;
+      };
+      bool ok = true;
+      // (the first turn only looks up: one copy of the code, which a launch has to fetch)
+      for (int base = i0 - kTurn * kDeep; base < total && ok; base += kTurn * kDeep) {
 #pragma unroll
-          for (int d = 0; d < kDeep; ++d) {
-            if (s < s_end && ok) {
-              const uint32_t i = i0 + s - s_beg;
-              // the products before the last on this accumulator are complete: so they were issued, after the
-              // promoters had let go of the stage before that, whose scales lie where this stage's go
-              if (i >= kAccs) ok = __all_sync(0xffffffffu, wait(&full_acc[i % kAccs], ((i / kAccs) & 1) ^ 1, ab, 127));
-              if (ok) {
+        for (int d = 0; d < kDeep; ++d) {
+          const int i = base + kTurn * d;
+          if (i >= total || !ok) continue;
+          if (i >= 0) {
+            // the products before the last on this accumulator are complete: so they were issued, after the
+            // promoters had let go of the stage before that, whose scales lie where this stage's go
+            if (i >= kAccs) ok = __all_sync(0xffffffffu, wait(&full_acc[i % kAccs], ((i / kAccs) & 1) ^ 1, ab, 127));
+            if (!ok) continue;
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) s_scale[(i % kScaleRing) * ROWS + 32 * j + lane] = v[d][j];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full_acc[i % kAccs]);
-                load(s + kTurn * kDeep, v[d]);
-              }
-              s += kTurn;
-            }
+            for (int j = 0; j < kPer; ++j) s_scale[(i % kScaleRing) * ROWS + 32 * j + lane] = f[d] * v[d][j];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full_acc[i % kAccs]);
           }
+          look_up(d);
         }
       }
     }
@@ -345,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
         continue;
       }
-      const int to = output_row(g, U.first + r, r < U.rows);
+      const int entry = output_entry(g, U.first + r, r < U.rows);
       float2 acc[32];
 #pragma unroll
       for (int c = 0; c < 32; ++c) acc[c] = make_float2(0.f, 0.f);
@@ -396,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             }
           }
       }
-      store_rows<OUT>(g, to, U.wtile * 128 + 64 * half, acc, stage, lane);
+      store_rows<OUT>(g, output_row(g, entry), U.wtile * 128 + 64 * half, acc, stage, lane);
     }
   }
 

@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
         }
         continue;
       }
-      const int to = output_row(g, U.z + r, r < U.w);
+      const int entry = output_entry(g, U.z + r, r < U.w);
       float2 acc[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
         seen = __all_sync(0xffffffffu, look);
       }
       if (!ok) break;
+      const int to = output_row(g, entry);
       if constexpr (H != kPlain) {
         // h in place of the sums, its block's scale (gated: with the warp of the other 64 columns), codes
         constexpr int kCols = H == kGated ? 32 : 64;  // pairs of columns of this warp

@@ -112,12 +112,13 @@ __device__ __forceinline__ void store_rows(const Fp4GemmParams& g, int to, int n
   }
 }
 
-// Output row of operand row `at`, -1 where it is dropped.
-__device__ __forceinline__ int output_row(const Fp4GemmParams& g, int at, bool live) {
-  if (!live) return -1;
-  if (!g.out_rows) return at;
-  const int to = __ldg(g.out_rows + at);
-  return to < g.out_rows_end ? to : -1;
+// The entry of operand row `at` in out_rows, read before its sums are made and looked at after (a load
+// takes a microsecond and more under the operands' traffic), and its output row, -1 where it is dropped.
+__device__ __forceinline__ int output_entry(const Fp4GemmParams& g, int at, bool live) {
+  return !live ? -1 : g.out_rows ? __ldg(g.out_rows + at) : at;
+}
+__device__ __forceinline__ int output_row(const Fp4GemmParams& g, int entry) {
+  return entry < g.out_rows_end ? entry : -1;
 }
 
 // Calls f with the output's type and whether the rows are grouped as compile-time values.
