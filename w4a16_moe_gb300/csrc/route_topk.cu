@@ -17,12 +17,14 @@
 // a token to another expert.  Without a bias the logits' own order decides (scores are
 // monotone).  With one, where neighbours in the order are closer than fp32's error, the
 // chosen and the next are compared again in 64 bits, a lane each; where the last group taken
-// and the first left are, or a third comes close, the row is done again in 64 bits.
+// and the first left are, the groups about that line are, from the experts that may be their
+// largest (softmax, whose scores need the row's sum: the whole row); where a third expert comes
+// close, the row is done again in 64 bits.
 //
-// Bound by latency for few tokens (one launch: 2.2 us for 1 token of 128 experts) and by the issue
-// of instructions for many: 16384 tokens of 256 experts in 8 groups, sigmoid with a bias, bf16
-// 23 us (8.4 MB of logits, read once), of which the rows done again in 64 bits are 6 to 10: they
-// are few, and each holds its warp for as long as it takes.
+// Bound by latency for few tokens (one launch: 2.3 us for 1 token of 128 experts) and by the
+// issue of instructions for many: 16384 tokens of 256 experts in 8 groups, sigmoid with a bias,
+// bf16 20 us (8.4 MB of logits, read once).  A row done again as a whole holds its warp for 5 us,
+// which the last ones show: with close groups done so too it was 27.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -230,6 +232,22 @@ __device__ __forceinline__ bool close_(float a, float b, float terms, float most
   return a - b <= terms * (0x1p-20f * most + 0x1p-23f * fabsf(a));
 }
 
+// Of sigmoid scores in 64 bits, the largest two among a lane's experts in `mask`.
+template <typename T>
+__device__ __noinline__ double2 top2_64(const RouteParams& p, const T* row, int first, uint32_t mask) {
+  double a = -INFINITY, b = -INFINITY;
+  while (__any_sync(kAll, mask != 0)) {
+    if (mask) {
+      const int e = first + __ffs(mask) - 1;
+      mask &= mask - 1;
+      const double v = sigmoid((double)logit(row, e)) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
+      b = fmax(b, fmin(a, v));
+      a = fmax(a, v);
+    }
+  }
+  return make_double2(a, b);
+}
+
 // A lane's experts, sorted: keys descending, equal ones by index.  (An odd-even merge network.)
 template <int V>
 __device__ __forceinline__ void sort_keys(int (&key)[V], int (&pos)[V]) {
@@ -307,12 +325,38 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const __grid_constant__
   if (p.groups > 1) {
     merge_top2(a, b, p.lanes_log2);
     const float value = group < p.groups ? group_value(a, b, p.group_top) : -INFINITY;
-    const int rank = group_rank(p, value, group);
+    int rank = group_rank(p, value, group);
     if (scores && p.top_groups < p.groups) {
       const uint32_t in = __ballot_sync(kAll, rank == p.top_groups - 1 && group < p.groups);
       const uint32_t out = __ballot_sync(kAll, rank == p.top_groups && group < p.groups);
       const float last = __shfl_sync(kAll, value, __ffs(in) - 1), next = __shfl_sync(kAll, value, __ffs(out) - 1);
-      again = next > -INFINITY && close_(last, next, 4.f, inv);
+      const bool open = next > -INFINITY && close_(last, next, 4.f, inv);
+      again = open && p.softmax;
+      if (open && !p.softmax) {
+        // The groups about the line in 64 bits, from the experts that may be their largest (softmax needs
+        // the row's sum for it: the whole row).  One above the others by more than fp32's error is among
+        // the kept whatever their order, and likewise below.
+        const bool near = group < p.groups && value > -INFINITY && close_(fmaxf(value, next), fminf(value, last), 4.f, inv);
+        const float least = p.group_top == 2 && b > -INFINITY ? b : a;
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float k = value_of(key[i]), c = p.bias ? k : sigmoid_order(k);
+          if (near && i < count && k > -INFINITY && (c >= least || close_(least, c, 2.f, inv))) mask |= 1u << i;
+        }
+        double2 t = top2_64(p, row, first, mask);
+        merge_top2(t.x, t.y, p.lanes_log2);
+        const double exact = group_value(t.x, t.y, p.group_top);
+        const uint32_t nears = __ballot_sync(kAll, near);
+        rank = 0;
+        for (int g = 0; g < p.groups; ++g) {
+          const int from = g << p.lanes_log2;
+          const float v = __shfl_sync(kAll, value, from);
+          const double v64 = __shfl_sync(kAll, exact, from);
+          const bool both = near && (nears >> from & 1);
+          rank += (both ? v64 > exact : v > value) || ((both ? v64 == exact : v == value) && g < group);
+        }
+      }
     }
     if (rank >= p.top_groups || group >= p.groups) {
 #pragma unroll
