@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 
   if (warp == 0) {
     // ----------------------------------------------------------- copies
-    uint32_t i = 0, issued = 0;
+    uint32_t i = 0;
     bool ok = u0 < n_units;
     // while the kernel before still writes the activations: weights first, for as much
     // of the ring as the first unit fills
@@ -218,16 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
         __syncwarp();
         --early;
-        ++issued;
       }
     }
     if (ab.raised() && lane == 0) {
-      // let copies already issued land before the CTA's shared memory goes away
-      const uint32_t n = issued < (uint32_t)NS ? issued : (uint32_t)NS;
-      for (uint32_t j = issued - n; j < issued; ++j) {
-        const unsigned long long t0 = globaltimer();
-        while (!mbar_try_wait(&full[j % NS], (j / NS) & 1) && globaltimer() - t0 < kWaitLimitNs) {
-        }
+      // copies already issued land before the shared memory goes away: give them a fixed time
+      const unsigned long long t0 = globaltimer();
+      while (globaltimer() - t0 < 2000000ull) {
       }
     }
     __syncwarp();
