@@ -67,7 +67,8 @@ def route_row(z, bias, top_k, score, renorm=True, scale=1.0, groups=1, top_group
         if renorm:
             if score == "sigmoid" and v.max() < 1e-200:  # the ratios of what underflows
                 v = np.exp(z[order] - z[order].max())
-            v = v / v.sum()
+            # (of a softmax that is the softmax over the chosen, also where all of theirs are 0)
+            v = scores(z[order], score) if score == "softmax" else v / v.sum()
         w[: len(order)] = v * scale
     return ids, w
 

@@ -170,3 +170,27 @@ def test_graph_and_side_stream(b4):
     torch.cuda.synchronize()
     want = R.route(z.double().cpu().numpy(), b.double().cpu().numpy(), 8, "sigmoid")
     assert np.array_equal(ids.cpu().numpy(), want[0]) and not torch.equal(ids, first[0])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,k,groups,top_groups", [(256, 8, 8, 4), (320, 6, 10, 3), (32, 4, 32, 7), (96, 5, 16, 2), (1024, 8, 4, 1)])
+def test_groups_that_fp32_does_not_separate(b4, score, e, k, groups, top_groups):
+    """Every group holds the same logits in another order, each a few ulps off: the groups' order is that of the 64-bit values;
+    some rows have groups of excluded experts, of one that counts, or equal ones."""
+    g = torch.Generator().manual_seed(31)
+    per, m = e // groups, 40
+    z = torch.randn(m, 1, per, generator=g).repeat(1, groups, 1)
+    z = torch.gather(z, 2, torch.rand(m, groups, per, generator=g).argsort(-1))
+    z = (z * (1 + torch.randint(-3, 4, z.shape, generator=g) * 2.0**-23)).to(F32)
+    z[5, : groups // 2] = float("-inf")
+    z[6, :, 1:] = float("nan")
+    z[7] = z[7, :1]
+    z[8, 1, 0] = float("inf")
+    z = z.reshape(m, e)
+    some = torch.full((e,), 0.25)
+    some[e // 3] = float("-inf")
+    first = some.clone()
+    first[e // 2] = float("inf")
+    for bias in (None, some, first):
+        for group_top in (1, 2):
+            _compare(b4, z, bias, k, score, groups=groups, top_groups=top_groups, group_top=group_top)

@@ -23,7 +23,7 @@
 //
 // Bound by latency for few tokens (one launch: 2.3 us for 1 token of 128 experts) and by the
 // issue of instructions for many: 16384 tokens of 256 experts in 8 groups, sigmoid with a bias,
-// bf16 20 us (8.4 MB of logits, read once).  A row done again as a whole holds its warp for 5 us,
+// bf16 21 us (8.4 MB of logits, read once).  A row done again as a whole holds its warp for 5 us,
 // which the last ones show: with close groups done so too it was 27.
 
 #include <cuda_bf16.h>
@@ -393,7 +393,21 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const __grid_constant__
       const float zn = __shfl_down_sync(kAll, zm, 1), bn = __shfl_down_sync(kAll, bm, 1);
       const float ze = extra >= 0 ? logit(row, extra) : 0.f, be = extra >= 0 ? __ldg(p.bias + extra) : 0.f;
       const bool last_lane = lane == p.top_k - 1;
-      tie = tie && !(zm == (last_lane ? ze : zn) && bm == (last_lane ? be : bn));
+      const bool same = zm == (last_lane ? ze : zn) && bm == (last_lane ? be : bn);
+      const bool at_end = last_lane && tie && same;
+      tie = tie && !same;
+      if (__any_sync(kAll, at_end)) {
+        // behind a true tie of the last chosen with the first left another may stand who is close, and not equal
+        const float zl = __shfl_sync(kAll, zm, p.top_k - 1), bl = __shfl_sync(kAll, bm, p.top_k - 1);
+        const float cl = value_of(__shfl_sync(kAll, its_key, p.top_k - 1));
+        bool other = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (key[i] > kNone && close_(cl, value_of(key[i]), 2.f, inv))
+            other = other || logit(row, first + pos[i]) != zl || __ldg(p.bias + first + pos[i]) != bl;
+        const bool any_other = __any_sync(kAll, other);  // (every lane votes)
+        tie = tie || (any_other && last_lane);
+      }
     }
     if (__any_sync(kAll, tie)) {
       // one more, and who stands behind it; then, unless that one may belong among them too, only
