@@ -1,0 +1,59 @@
+"""GPU tests of the routing operator (b4_route_topk) where a lane holds many experts and where fp32 errs the most.
+
+Against the float64 oracle, ids equal; weights within the tolerance that test_gpu_route_topk.py derives.
+"""
+
+import pytest
+import torch
+
+from oracle import router as R
+from test_gpu_route_topk import BF, F32, HF, _compare, _z, b4  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# more than 32 experts a lane: a group has the power of two of lanes that fits (17 groups: one), and up to 60 experts
+WIDE = [  # experts, groups, top_k, top_groups
+    (561, 17, 8, 4), (645, 5, 6, 2), (771, 3, 8, 1), (720, 9, 8, 3), (960, 6, 32, 2), (1020, 17, 9, 17), (1023, 31, 8, 9),
+    (720, 5, 4, 5), (960, 20, 8, 7), (1000, 10, 8, 3), (1023, 3, 8, 2), (1023, 11, 32, 1),
+]
+
+
+@pytest.mark.parametrize("e,groups,k,top_groups", WIDE)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_more_experts_than_32_a_lane(b4, e, groups, k, top_groups, score, bias):  # noqa: F811
+    b = torch.randn(e, generator=torch.Generator().manual_seed(9)) * 0.1 if bias else None
+    for dtype in (BF, HF, F32):
+        z = _z(5, e, e + k, dtype)
+        z[1, : e // 2] = float("-inf")
+        z[2, e // 3:] = float("nan")
+        for group_top in (1, 2):
+            for renorm, scale in ((True, 2.5), (False, 1.0)):
+                _compare(b4, z, b, k, score, renorm=renorm, scale=scale, groups=groups, top_groups=top_groups, group_top=group_top)
+
+
+@pytest.mark.parametrize("e,groups,k,top_groups", WIDE)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_close_scores_of_more_experts_than_32_a_lane(b4, e, groups, k, top_groups, score):  # noqa: F811
+    """Every c one value but for rounding, and groups of the same logits in another order, a few ulps off."""
+    z = _z(1, e, 21, F32)
+    b = torch.from_numpy((0.75 - R.scores(z.double().numpy()[0], score)).astype("float32"))
+    g = torch.Generator().manual_seed(31)
+    per = e // groups
+    same = torch.randn(6, 1, per, generator=g).repeat(1, groups, 1)
+    same = torch.gather(same, 2, torch.rand(6, groups, per, generator=g).argsort(-1))
+    same = (same * (1 + torch.randint(-3, 4, same.shape, generator=g) * 2.0**-23)).to(F32).reshape(6, e)
+    for group_top in (1, 2):
+        _compare(b4, z.repeat(2, 1), b, k, score, groups=groups, top_groups=top_groups, group_top=group_top)
+        for bias in (None, torch.full((e,), 0.25)):
+            _compare(b4, same, bias, k, score, groups=groups, top_groups=top_groups, group_top=group_top)
+
+
+def test_the_last_expert_of_a_lane(b4):  # noqa: F811
+    """Each expert in turn is the only one that counts, or the largest."""
+    for e, groups in ((561, 17), (720, 9), (1020, 17)):
+        z = torch.full((e, e), -3.0)
+        z.fill_diagonal_(3.0)
+        for kw in (dict(groups=groups, top_groups=1), dict(groups=groups, top_groups=2, group_top=2)):
+            _compare(b4, z[::7], None, 1, "softmax", **kw)
+            _compare(b4, z[::7], torch.zeros(e), 1, "sigmoid", **kw)
