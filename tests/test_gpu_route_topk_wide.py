@@ -57,3 +57,59 @@ def test_the_last_expert_of_a_lane(b4):  # noqa: F811
         for kw in (dict(groups=groups, top_groups=1), dict(groups=groups, top_groups=2, group_top=2)):
             _compare(b4, z[::7], None, 1, "softmax", **kw)
             _compare(b4, z[::7], torch.zeros(e), 1, "sigmoid", **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,groups,k,top_groups", [(64, 8, 8, 4), (256, 8, 8, 4), (160, 5, 6, 2), (720, 9, 8, 3)])
+@pytest.mark.parametrize("size", [100.0, 3000.0])
+def test_groups_whose_largest_cancel(b4, score, e, groups, k, top_groups, size):  # noqa: F811
+    """A group's two largest far from zero and of opposite sign: their sum is small, the roundings of each are not.
+
+    Sums of groups differ by some 1e-6, an fp32 of the size of 100 is rounded by up to 4e-6, of 3000 by 1.2e-4."""
+    g = torch.Generator().manual_seed(41)
+    per, m = e // groups, 60
+    z = torch.randn(1, 1, per, generator=g) + torch.randn(m, groups, per, generator=g) * 1e-5
+    bias = torch.full((groups, per), -4 * size)
+    bias[:, 1], bias[:, 2] = size, -size
+    _compare(b4, z.reshape(m, e), bias.reshape(e), k, score, groups=groups, top_groups=top_groups, group_top=2)
+    # one group alone is far from zero: its sum's error counts against the others' small ones, above and below them
+    for shift in (-1e-6, 0.0, 1e-6):
+        bias = torch.full((groups, per), -4 * size)
+        bias[:, 1], bias[:, 2] = 0.5, -0.5
+        bias[1, 1], bias[1, 2] = size, -size
+        zs = z.clone()
+        zs[:, 1] += shift
+        _compare(b4, zs.reshape(m, e), bias.reshape(e), k, score, groups=groups, top_groups=top_groups, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_of_the_largest_and_lowest_biases(b4, score):  # noqa: F811
+    """Sums past fp32's range, groups masked by the type's lowest value or by -inf, infinite groups."""
+    top, inf = torch.finfo(F32).max, float("inf")
+    z = _z(9, 64, 43, F32)
+    for case in range(6):
+        bias = torch.randn(8, 8, generator=torch.Generator().manual_seed(44)) * 0.1
+        if case == 0:
+            bias[5] = bias[2] = top
+            bias[5, 3:] = top / 2
+            bias[2, 1:] = 0.75 * top
+        elif case == 1:
+            bias[:6] = -top
+            bias[0] = -inf
+            bias[3, 0] = -0.5 * top
+        elif case == 2:
+            bias[[1, 4, 6]] = inf
+            bias[4, 1:] = -top
+            bias[2, 2:4] = top
+        elif case == 3:
+            bias[:] = -top
+            bias[::2] = -inf
+        elif case == 4:
+            bias[:, 1:] = -inf
+            bias[3:, 0] = -top
+        else:
+            bias[:] = -inf
+            bias[6, 1] = bias[7, 1] = -top
+        for kw in (dict(groups=8, top_groups=2), dict(groups=8, top_groups=4), dict(groups=4, top_groups=3)):
+            for group_top in (1, 2):
+                _compare(b4, z, bias.reshape(64), 8, score, group_top=group_top, **kw)

@@ -18,8 +18,8 @@
 // than fp32 resolves about once in a thousand tokens, and another order there would send
 // a token to another expert.  Without a bias the logits' own order decides (scores are
 // monotone).  With one, where neighbours in the order are closer than fp32's error, the
-// chosen and the next are compared again in 64 bits, a lane each; where the last group taken
-// and the first left are, the groups about that line are, from the experts that may be their
+// chosen and the next are compared again in 64 bits, a lane each; where groups taken and
+// groups left may stand the other way round, these are, from the experts that may be their
 // largest (softmax, whose scores need the row's sum: the whole row); where a third expert comes
 // close, the row is done again in 64 bits.
 //
@@ -32,6 +32,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -242,6 +243,18 @@ __device__ __forceinline__ bool close_(float a, float b, float terms, float most
   return a - b <= terms * (0x1p-20f * most + 0x1p-23f * fabsf(a));
 }
 
+// Where a group's real value lies, from its fp32 one and its largest two: twice what they can be off by.  Each of
+// the two is off by 2^-21 of `most` and 2^-24 of itself, the sum by 2^-24 more: far more than of the sum, where
+// they cancel.  (a is the larger; sums past fp32's range are not infinite.)
+struct Range {
+  float low, high;
+};
+__device__ __forceinline__ Range group_range(float value, float a, float b, int group_top, float most) {
+  const float off = 0x1p-19f * most + 0x1p-22f * fabsf(a) + (group_top == 2 && b > -INFINITY ? 0x1p-22f * fabsf(b) : 0.f);
+  if (fabsf(value) < INFINITY) return Range{value - off, value + off};
+  return Range{value > 0.f && a < INFINITY ? FLT_MAX : value, value < 0.f && a > -INFINITY ? -FLT_MAX : value};
+}
+
 // Of sigmoid scores in 64 bits, the largest two among a lane's experts in `mask`.
 template <typename T, typename M>
 __device__ __noinline__ double2 top2_64(const RouteParams& p, const T* row, int first, M mask) {
@@ -337,16 +350,15 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const __grid_constant__
     const float value = group < p.groups ? group_value(a, b, p.group_top) : -INFINITY;
     int rank = group_rank(p, value, group);
     if (scores && p.top_groups < p.groups) {
-      const uint32_t in = __ballot_sync(kAll, rank == p.top_groups - 1 && group < p.groups);
-      const uint32_t out = __ballot_sync(kAll, rank == p.top_groups && group < p.groups);
-      const float last = __shfl_sync(kAll, value, __ffs(in) - 1), next = __shfl_sync(kAll, value, __ffs(out) - 1);
-      const bool open = next > -INFINITY && close_(last, next, 4.f, inv);
+      const bool kept = group < p.groups && rank < p.top_groups, left = group < p.groups && rank >= p.top_groups;
+      const Range r = group_range(value, a, b, p.group_top, inv);
+      const float least_kept = -warp_max(kept ? -r.low : -INFINITY), most_left = warp_max(left ? r.high : -INFINITY);
+      const bool open = most_left > -INFINITY && most_left >= least_kept;
       again = open && p.softmax;
       if (open && !p.softmax) {
         // The groups about the line in 64 bits, from the experts that may be their largest (softmax needs
-        // the row's sum for it: the whole row).  One above the others by more than fp32's error is among
-        // the kept whatever their order, and likewise below.
-        const bool near = group < p.groups && value > -INFINITY && close_(fmaxf(value, next), fminf(value, last), 4.f, inv);
+        // the row's sum for it: the whole row).  The others stay on the side where they are.
+        const bool near = kept ? r.low <= most_left : left && r.high >= least_kept;
         const float least = p.group_top == 2 && b > -INFINITY ? b : a;
         Mask<V> mask = 0;
 #pragma unroll
@@ -357,15 +369,14 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const __grid_constant__
         double2 t = top2_64(p, row, first, mask);
         merge_top2(t.x, t.y, p.lanes_log2);
         const double exact = group_value(t.x, t.y, p.group_top);
-        const uint32_t nears = __ballot_sync(kAll, near);
-        rank = 0;
+        const uint32_t nears = __ballot_sync(kAll, near), keeps = __ballot_sync(kAll, kept);
+        int before = 0;
         for (int g = 0; g < p.groups; ++g) {
           const int from = g << p.lanes_log2;
-          const float v = __shfl_sync(kAll, value, from);
-          const double v64 = __shfl_sync(kAll, exact, from);
-          const bool both = near && (nears >> from & 1);
-          rank += (both ? v64 > exact : v > value) || ((both ? v64 == exact : v == value) && g < group);
+          const double v = __shfl_sync(kAll, exact, from);
+          before += nears >> from & 1 ? v > exact || (v == exact && g < group) : (int)(keeps >> from & 1);
         }
+        if (near) rank = before;
       }
     }
     if (rank >= p.top_groups || group >= p.groups) {
