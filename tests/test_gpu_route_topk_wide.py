@@ -113,3 +113,24 @@ def test_groups_of_the_largest_and_lowest_biases(b4, score):  # noqa: F811
         for kw in (dict(groups=8, top_groups=2), dict(groups=8, top_groups=4), dict(groups=4, top_groups=3)):
             for group_top in (1, 2):
                 _compare(b4, z, bias.reshape(64), 8, score, group_top=group_top, **kw)
+
+
+@pytest.mark.parametrize("e,groups,v", [(1024, 1, 32), (960, 6, 40), (1020, 17, 60)])
+def test_softmax_of_one_large_and_many_small(b4, e, groups, v):  # noqa: F811
+    """Exponentials just over half a unit of the largest's last place: added one by one, each is rounded up to a whole one.
+
+    The largest's score has the bias -1, so that c is what its score lacks of 1, some 2e-6; another expert's bias alone lies
+    1e-8 below the exact c."""
+    z = torch.full((1, e), -60.0, dtype=F32)
+    step = e // groups if groups == 17 else -(-(e // groups) // (4 if groups == 6 else 32))  # experts of a lane
+    z[0, :v] = -16.635  # e^z = 1.0005 2^-24
+    z[0, 0] = 0.0
+    for lane in (1, 2, 4, 8, 16):
+        if lane * step < e:
+            z[0, lane * step] = -16.635
+    s = R.scores(z.double().numpy()[0], "softmax")
+    bias = torch.full((e,), -2.0, dtype=F32)
+    bias[0] = -1.0
+    for shift in (-1e-8, 1e-8):
+        bias[e - 1] = float(s[0] - 1.0 + shift)
+        _compare(b4, z, bias, 2, "softmax", groups=groups, top_groups=groups)

@@ -234,18 +234,22 @@ __device__ __noinline__ int choose64(const RouteParams& p, const T* row, int lan
   return chosen;
 }
 
-// Whether two values of the order may stand the other way round: the sum of what their
-// fp32 forms can be off by.  A score is at most `most` (1, or the largest of a softmax) and off by
-// 2^-21 of that (its exponential 2^-22 and an argument off by 2^-24 |z|, which a score of at
-// most e^-|z| makes small; the sum of exponentials and the quotient another three roundings);
-// the sum with the bias adds 2^-24 of itself.
+// Whether two values of the order may stand the other way round: twice what their fp32 forms
+// can be off by, the biases' part, and the scores' part once.  A score is at most `most` (1, or the largest of a
+// softmax) and off by 6 2^-24 of that for itself (its exponential 2^-22, an argument off by 2^-23 |z|,
+// which a score of at most e^-|z| makes small, and a product); what a softmax's scores share, the sum of
+// exponentials with 11 roundings at most (by halves in a lane, then five shuffles; one by one 31 small ones
+// beside a large one could all be rounded up) and the quotient, moves two of them apart by 15 2^-24 of
+// their difference.  So 27 2^-24 in all, taken as 32; the sum with the bias adds 2^-24 of itself.
 __device__ __forceinline__ bool close_(float a, float b, float terms, float most) {
   return a - b <= terms * (0x1p-20f * most + 0x1p-23f * fabsf(a));
 }
 
-// Where a group's real value lies, from its fp32 one and its largest two: twice what they can be off by.  Each of
-// the two is off by 2^-21 of `most` and 2^-24 of itself, the sum by 2^-24 more: far more than of the sum, where
-// they cancel.  (a is the larger; sums past fp32's range are not infinite.)
+// Where a group's real value lies, from its fp32 one and its largest two: twice what the biases' part can be off by.  Each of
+// the two is off by 6 2^-24 of `most` and by 2^-24 of itself, and what a softmax's scores share moves two
+// groups apart by 30 2^-24 (see close_): 27 2^-24 a group, taken as 32, once.  The sum adds 2^-24 of
+// itself, which is far less than of the two where they cancel.  (a is the larger; sums past fp32's range are not
+// infinite.)
 struct Range {
   float low, high;
 };
@@ -318,10 +322,14 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 1; i < V; ++i) t = fmaxf(t, z[i]);
     top = warp_max(t);
-    float sum = 0.f;
+    float e[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += z[i] > -INFINITY ? exp_below(z[i], top) : 0.f;
-    inv = 1.f / warp_sum(sum);
+    for (int i = 0; i < V; ++i) e[i] = z[i] > -INFINITY ? exp_below(z[i], top) : 0.f;
+#pragma unroll
+    for (int o = V / 2; o > 0; o /= 2)  // (by halves: see close_)
+#pragma unroll
+      for (int i = 0; i < o; ++i) e[i] += e[i + o];
+    inv = 1.f / warp_sum(e[0]);
   }
   int key[V], pos[V];
   float a = -INFINITY, b = -INFINITY;
