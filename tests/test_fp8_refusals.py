@@ -1,0 +1,82 @@
+"""What the binding of the routing and FP8 operators refuses, operand by operand (CPU).
+
+The library is replaced by a recorder, so that a call that is let through is seen and nothing runs.
+"""
+
+import pytest
+import torch
+
+BF, F32, U8, I32, E4M3 = torch.bfloat16, torch.float32, torch.uint8, torch.int32, torch.float8_e4m3fn
+
+
+@pytest.fixture
+def b4(monkeypatch):
+    import __graft_entry__
+
+    __graft_entry__._build_module().build()
+    import w4a16_moe_gb300 as mod
+
+    calls = []
+
+    class Recorder:
+        def __getattr__(self, name):
+            return lambda *args: calls.append(name) or 0
+
+    monkeypatch.setattr(mod, "_lib", Recorder())
+    monkeypatch.setattr(mod, "_launch_stream", lambda stream, t, name: 0)
+    mod.calls = calls
+    yield mod
+    del mod.calls
+
+
+def _entries(b4):
+    """Entry point -> (call, its tensors by name)."""
+    m, k, n, kb, top = 4, 272, 200, 3, 2
+    q, blocks, p, r = (b4.Fp8Config(m=m, k=k), b4.Fp8Config(m=n, k=k, x_dtype=F32, block_rows=128), b4.Fp8Config(m=m, k=k, n=n),
+                       b4.RouterConfig(m, 16, top))
+    layer = b4.MoEConfig(m, top, 8, 8, 272, 144)
+
+    def z(*shape, dtype=F32):
+        return torch.zeros(*shape, dtype=dtype)
+
+    w = dict(w_codes=z(1, n, k, dtype=E4M3), w_scales=z(1, 2, kb))
+    return {
+        "route_topk": (lambda **t: b4.route_topk(r, **t), dict(logits=z(m, 16, dtype=BF), topk_ids=z(m, top, dtype=I32),
+                       topk_weights=z(m, top), bias=z(16), num_tokens=z(1, dtype=I32))),
+        "fp8_quantize": (lambda **t: b4.fp8_quantize(q, **t), dict(x=z(m, k, dtype=BF), codes=z(m, k, dtype=E4M3), scales=z(m, kb),
+                         values=z(m, k, dtype=BF), rows=z(m, dtype=I32), offsets=z(2, dtype=I32))),
+        "fp8_quantize blocks": (lambda **t: b4.fp8_quantize(blocks, **t), dict(x=z(n, k), codes=z(n, k, dtype=U8), scales=z(2, kb),
+                                values=z(n, k))),
+        "fp8_matmul": (lambda **t: b4.fp8_matmul(p, **t), dict(a_codes=z(m, k, dtype=E4M3), a_scales=z(m, kb), **w, out=z(m, n, dtype=BF),
+                       offsets=z(2, dtype=I32), out_rows=z(m, dtype=I32), device_status=z(2, dtype=I32))),
+        "fp8_linear": (lambda **t: b4.fp8_linear(p, **t), dict(x=z(m, k, dtype=BF), **w, out=z(m, n, dtype=BF), workspace=z(9, dtype=U8),
+                       rows=z(m, dtype=I32), offsets=z(2, dtype=I32), out_rows=z(m, dtype=I32))),
+        "fused_moe_fp8": (lambda **t: b4.fused_moe_fp8(layer, activation=b4.SILU, **t),
+                          dict(x=z(m, 272, dtype=BF), w13=z(8, 288, 272, dtype=E4M3), s13=z(8, 3, 3), w2=z(8, 272, 144, dtype=U8),
+                               s2=z(8, 3, 2), topk_ids=z(m, top, dtype=I32), topk_weights=z(m, top), out=z(m, 272, dtype=BF),
+                               workspace=z(9, dtype=U8))),
+    }
+
+
+ROWS = [("route_topk", "topk_ids"), ("route_topk", "topk_weights"), ("fp8_quantize", "codes"), ("fp8_quantize", "scales"),
+        ("fp8_quantize", "values"), ("fp8_quantize blocks", "codes"), ("fp8_quantize blocks", "scales"),
+        ("fp8_quantize blocks", "values"), ("fp8_matmul", "a_codes"), ("fp8_matmul", "a_scales"), ("fp8_matmul", "w_codes"),
+        ("fp8_matmul", "w_scales"), ("fp8_linear", "w_codes"), ("fp8_linear", "w_scales"), ("fused_moe_fp8", "x"),
+        ("fused_moe_fp8", "out"), ("fused_moe_fp8", "w13"), ("fused_moe_fp8", "s13"), ("fused_moe_fp8", "w2"),
+        ("fused_moe_fp8", "s2"), ("fused_moe_fp8", "topk_ids"), ("fused_moe_fp8", "topk_weights")]
+
+
+@pytest.mark.parametrize("entry,name", ROWS)
+def test_rows_longer_than_the_configs_are_refused(b4, entry, name):
+    """A contiguous tensor of longer rows would be read or written at another pitch; one of more rows is fine."""
+    call, tensors = _entries(b4)[entry]
+    call(**tensors)
+    assert len(b4.calls) == 1
+    t = tensors[name]
+    wide = torch.zeros(*t.shape[:-1], t.shape[-1] + 16, dtype=t.dtype)
+    with pytest.raises(ValueError, match=rf"^{name} has rows of {t.shape[-1] + 16} "):
+        call(**{**tensors, name: wide})
+    assert len(b4.calls) == 1
+    call(**{**tensors, name: torch.zeros(t.shape[0] + 1, *t.shape[1:], dtype=t.dtype)})
+    call(**{**tensors, name: torch.zeros(t.numel() + 5, dtype=t.dtype)})
+    assert len(b4.calls) == 3

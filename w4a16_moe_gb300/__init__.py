@@ -803,11 +803,16 @@ def route_topk(cfg: RouterConfig, logits, topk_ids, topk_weights, bias=None, num
         _check(st)
 
 
-def _route_out(t, dtype, cfg, name):
-    p = _fp4_buffer(t, dtype, cfg.routes, name)
-    if p is not None and t.numel() != cfg.routes and _wider(t, cfg.top_k):
-        raise ValueError(f"{name} has rows of {t.shape[-1]} elements, the config rows of {cfg.top_k}")
+def _rows_buffer(t, dtype, n, pitch, name, what="elements"):
+    """Address of a contiguous tensor of at least n elements in rows of ``pitch`` (None stays None)."""
+    p = _fp4_buffer(t, dtype, n, name)
+    if p is not None and t.numel() != n and _wider(t, pitch):
+        raise ValueError(f"{name} has rows of {t.shape[-1]} {what}, the config rows of {pitch}")
     return p
+
+
+def _route_out(t, dtype, cfg, name):
+    return _rows_buffer(t, dtype, cfg.routes, cfg.top_k, name)
 
 
 # ------------------------------------------------------- FP8 operators
@@ -849,13 +854,14 @@ class Fp8Config:
         return self._operands[ragged][0]
 
 
-def _fp8_codes(t, n, name):
-    """Address of a contiguous tensor of at least n E4M3 codes, as torch's type or as bytes (None stays None)."""
-    if isinstance(t, _Tensor) and (t.dtype is E4M3 or t.dtype is _U8) and t.numel() >= n and t.is_contiguous():
-        return t.data_ptr()
-    if isinstance(t, _Tensor) and t.dtype is E4M3:
-        t = t.view(_U8)
-    return _fp4_buffer(t, _U8, n, name)
+def _fp8_codes(t, n, k, name):
+    """Address of a contiguous tensor of at least n E4M3 codes in rows of k, as torch's type or as bytes (None stays
+    None)."""
+    return _rows_buffer(t, E4M3 if isinstance(t, _Tensor) and t.dtype is E4M3 else _U8, n, k, name, "codes")
+
+
+def _fp8_scales(t, n, kb, name):
+    return _rows_buffer(t, _F32, n, kb, name, "scales")
 
 
 def _fp8_weights(cfg, w_codes, w_scales):
@@ -867,12 +873,7 @@ def _fp8_weight(codes, scales, sizes, name, scales_name):
     """Addresses of quantised matrices and of their scales: sizes are their codes, scales, codes of a row, scales of a
     row."""
     n, ns, k, kb = sizes
-    cp, sp = _fp8_codes(codes, n, name), _fp4_buffer(scales, _F32, ns, scales_name)
-    if cp is not None and codes.numel() != n and _wider(codes, k):
-        raise ValueError(f"{name} has rows of {codes.shape[-1]} codes, the config rows of {k}")
-    if sp is not None and scales.numel() != ns and _wider(scales, kb):
-        raise ValueError(f"{scales_name} has rows of {scales.shape[-1]} scales, the config rows of {kb}")
-    return cp, sp
+    return _fp8_codes(codes, n, k, name), _fp8_scales(scales, ns, kb, scales_name)
 
 
 def _fp8_sizes(e, n, k):
@@ -910,8 +911,8 @@ def fp8_quantize(cfg: Fp8Config, x, codes, scales, values=None, rows=None, offse
     st = _lib.b4_fp8_quantize(
         _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _fp4_buffer(rows, _I32, n, "rows"),
         _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None,
-        _fp8_codes(codes, n_codes, "codes"), _fp4_buffer(scales, _F32, n_scales, "scales"),
-        values if values is None else _fp4_buffer(values, cfg.x_dtype, n_codes, "values"), handle)
+        _fp8_codes(codes, n_codes, cfg.k, "codes"), _fp8_scales(scales, n_scales, cfg.blocks, "scales"),
+        values if values is None else _rows_buffer(values, cfg.x_dtype, n_codes, cfg.k, "values"), handle)
     if st:
         _check(st)
 
@@ -923,7 +924,7 @@ def fp8_matmul(cfg: Fp8Config, a_codes, a_scales, w_codes, w_scales, out, offset
     handle = _launch_stream(stream, a_codes, "a_codes")
     wp, sp = _fp8_weights(cfg, w_codes, w_scales)
     st = _lib.b4_fp8_matmul(
-        cfg._ref, _fp8_codes(a_codes, n_codes, "a_codes"), _fp4_buffer(a_scales, _F32, n_scales, "a_scales"),
+        cfg._ref, _fp8_codes(a_codes, n_codes, cfg.k, "a_codes"), _fp8_scales(a_scales, n_scales, cfg.blocks, "a_scales"),
         wp, sp, offsets if offsets is None else _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets"),
         out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, n, "out_rows"), _fp4_out(cfg, out, n),
         device_status if device_status is None else _fp4_buffer(device_status, _I32, 2, "device_status"),
@@ -973,21 +974,18 @@ def fused_moe_fp8(cfg: MoEConfig, x, w13, s13, w2, s2, topk_ids, topk_weights, a
     bf16 is written in full.  The config's format and path are not read."""
     e, m, h, i = cfg.num_local_experts, cfg.m, cfg.hidden, cfg.inter
     rows, routes = m * h, m * cfg.top_k
-    xp, op = _fp4_buffer(x, torch.bfloat16, rows, "x"), _fp4_buffer(out, torch.bfloat16, rows, "out")
+    xp, op = _rows_buffer(x, torch.bfloat16, rows, h, "x"), _rows_buffer(out, torch.bfloat16, rows, h, "out")
     sizes13, sizes2 = _fp8_layer_sizes(e, h, i, activation)
     w13p, s13p = _fp8_weight(w13, s13, sizes13, "w13", "s13")
     w2p, s2p = _fp8_weight(w2, s2, sizes2, "w2", "s2")
-    idp = _fp4_buffer(topk_ids, _I32, routes, "topk_ids")
-    wtp = _fp4_buffer(topk_weights, _F32, routes, "topk_weights")
+    idp = _rows_buffer(topk_ids, _I32, routes, cfg.top_k, "topk_ids")
+    wtp = _rows_buffer(topk_weights, _F32, routes, cfg.top_k, "topk_weights")
     _need(workspace, _U8, "workspace")
     if None in (xp, op, w13p, s13p, w2p, s2p, idp, wtp):
         for t, name in ((x, "x"), (out, "out"), (topk_ids, "topk_ids"), (topk_weights, "topk_weights"), (w13, "w13"),
                         (s13, "s13"), (w2, "w2"), (s2, "s2")):
             if t is None:
                 raise TypeError(f"{name} must be a torch tensor")
-    for t, name in ((x, "x"), (out, "out")):
-        if t.numel() != rows and _wider(t, h):
-            raise ValueError(f"{name} has rows of {t.shape[-1]} elements, the config rows of {h}")
     handle = _launch_stream(stream, x, "x")
     c = cfg._c()
     st = _lib.b4_fused_moe_fp8(ctypes.byref(c), xp, w13p, s13p, w2p, s2p, idp, wtp, int(activation), op,
