@@ -23,7 +23,7 @@ def b4(monkeypatch):
             return lambda *args: calls.append(name) or 0
 
     monkeypatch.setattr(mod, "_lib", Recorder())
-    monkeypatch.setattr(mod, "_launch_stream", lambda stream, t, name: 0)
+    monkeypatch.setattr(mod, "_launch_stream", lambda stream, t, name: (0, t.get_device()))
     mod.calls = calls
     yield mod
     del mod.calls
@@ -80,3 +80,51 @@ def test_rows_longer_than_the_configs_are_refused(b4, entry, name):
     call(**{**tensors, name: torch.zeros(t.shape[0] + 1, *t.shape[1:], dtype=t.dtype)})
     call(**{**tensors, name: torch.zeros(t.numel() + 5, dtype=t.dtype)})
     assert len(b4.calls) == 3
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor of another device."""
+
+    def get_device(self):
+        return 1
+
+
+PLACES = [(entry, name) for entry, names in {
+    "route_topk": "topk_ids topk_weights bias num_tokens", "fp8_quantize": "codes scales values rows offsets",
+    "fp8_matmul": "a_scales w_codes w_scales out offsets out_rows device_status",
+    "fp8_linear": "w_codes w_scales out workspace rows offsets out_rows",
+    "fused_moe_fp8": "w13 s13 w2 s2 topk_ids topk_weights out workspace"}.items() for name in names.split()]
+
+
+@pytest.mark.parametrize("entry,name", PLACES)
+def test_tensors_of_another_device_are_refused(b4, entry, name):
+    """Each but the first, whose device is the call's."""
+    call, tensors = _entries(b4)[entry]
+    with pytest.raises(ValueError, match=rf"^{name} is on "):
+        call(**{**tensors, name: tensors[name].as_subclass(Elsewhere)})
+    first = next(iter(tensors))
+    with pytest.raises(ValueError, match=" is on "):  # the other way round: it alone is there
+        call(**{**tensors, first: tensors[first].as_subclass(Elsewhere)})
+    assert not b4.calls
+    call(**tensors)
+    assert len(b4.calls) == 1
+
+
+def test_an_expert_map_of_another_device_is_refused(b4):
+    _, tensors = _entries(b4)["fused_moe_fp8"]
+    em = torch.zeros(8, dtype=I32)
+    for t, what in ((em.as_subclass(Elsewhere), "expert_map is on "), (em[:7], "expert_map needs 8")):
+        with pytest.raises(ValueError, match=what):
+            b4.fused_moe_fp8(b4.MoEConfig(4, 2, 8, 8, 272, 144, expert_map=t), activation=b4.SILU, **tensors)
+    b4.fused_moe_fp8(b4.MoEConfig(4, 2, 8, 8, 272, 144, expert_map=em), activation=b4.SILU, **tensors)
+    assert len(b4.calls) == 1
+
+
+@pytest.mark.parametrize("entry,name", [("route_topk", "logits"), ("fp8_quantize", "x"), ("fp8_linear", "out"),
+                                        ("fp8_matmul", "out"), ("fused_moe_fp8", "w13"), ("fused_moe_fp8", "topk_ids")])
+def test_a_missing_tensor_is_named(b4, monkeypatch, entry, name):
+    call, tensors = _entries(b4)[entry]
+    if name == next(iter(tensors)):
+        monkeypatch.undo()
+    with pytest.raises(TypeError, match=f"{name} must be a torch tensor"):
+        call(**{**tensors, name: None})

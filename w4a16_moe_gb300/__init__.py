@@ -770,25 +770,44 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 
 
 def _launch_stream(stream, t, name):
-    """Handle of ``stream``, or of the current stream.  The kernels run on the current device: a tensor of another is
-    refused."""
-    index = t.get_device()
-    if index < 0 or not t.is_cuda:
+    """(handle of ``stream``, or of the current stream; device of the call).  The kernels run on the current device: a
+    tensor of another is refused."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
-    if index != _current_device():
+    if device != _current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
     if stream is not None:
-        return stream.cuda_stream
-    return _stream(None) if _raw_stream is None else _raw_stream(index)
+        return stream.cuda_stream, device
+    return (_stream(None) if _raw_stream is None else _raw_stream(device)), device
+
+
+def _buffer(t, dtype, n, name, device, pitch=0, what="elements"):
+    """Address of a contiguous tensor of at least n elements on the call's device, in rows of ``pitch`` (0: any).  None
+    stays None."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        have = t.numel()
+        if have == n or (have > n and not (pitch and _wider(t, pitch))):
+            return t.data_ptr()
+    if t is None:
+        return None
+    _need(t, dtype, name)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on device {device}")
+    if t.numel() < n:
+        raise ValueError(f"{name} needs {n} elements, got {t.numel()}")
+    raise ValueError(f"{name} has rows of {t.shape[-1]} {what}, the config rows of {pitch}")
 
 
 def route_topk(cfg: RouterConfig, logits, topk_ids, topk_weights, bias=None, num_tokens=None, stream=None):
     """Enqueue the choice of experts (``b4_route_topk``): ``topk_ids`` [m, top_k] int32 and ``topk_weights`` [m, top_k]
     fp32 are written in full.  ``bias`` [num_experts] fp32 is added to the scores for the choice alone; rows from
     ``num_tokens`` (a device int32) on get ids of -1, which the layers drop."""
-    if logits.dtype is not cfg.dtype:
+    if isinstance(logits, _Tensor) and logits.dtype is not cfg.dtype:
         raise TypeError(f"logits must be {cfg.dtype}, got {logits.dtype}")
-    handle = _launch_stream(stream, logits, "logits")
+    handle, device = _launch_stream(stream, logits, "logits")
     shape = logits.shape
     if shape != cfg._shape or not logits.is_contiguous():
         if len(shape) != 2 or shape[0] < cfg.m or shape[1] < cfg.num_experts:
@@ -796,23 +815,16 @@ def route_topk(cfg: RouterConfig, logits, topk_ids, topk_weights, bias=None, num
         if cfg.m and (logits.stride(1) != 1 or (shape[0] > 1 and logits.stride(0) != cfg.stride)):
             raise ValueError(f"logits rows must be contiguous and {cfg.stride} elements apart (stride)")
     st = _lib.b4_route_topk(
-        cfg._ref, logits.data_ptr(), bias if bias is None else _fp4_buffer(bias, _F32, cfg.num_experts, "bias"),
-        num_tokens if num_tokens is None else _fp4_buffer(num_tokens, _I32, 1, "num_tokens"),
-        _route_out(topk_ids, _I32, cfg, "topk_ids"), _route_out(topk_weights, _F32, cfg, "topk_weights"), handle)
+        cfg._ref, logits.data_ptr(), bias if bias is None else _buffer(bias, _F32, cfg.num_experts, "bias", device),
+        num_tokens if num_tokens is None else _buffer(num_tokens, _I32, 1, "num_tokens", device),
+        _route_out(topk_ids, _I32, cfg, "topk_ids", device), _route_out(topk_weights, _F32, cfg, "topk_weights", device),
+        handle)
     if st:
         _check(st)
 
 
-def _rows_buffer(t, dtype, n, pitch, name, what="elements"):
-    """Address of a contiguous tensor of at least n elements in rows of ``pitch`` (None stays None)."""
-    p = _fp4_buffer(t, dtype, n, name)
-    if p is not None and t.numel() != n and _wider(t, pitch):
-        raise ValueError(f"{name} has rows of {t.shape[-1]} {what}, the config rows of {pitch}")
-    return p
-
-
-def _route_out(t, dtype, cfg, name):
-    return _rows_buffer(t, dtype, cfg.routes, cfg.top_k, name)
+def _route_out(t, dtype, cfg, name, device=-1):
+    return _buffer(t, dtype, cfg.routes, name, device, cfg.top_k)
 
 
 # ------------------------------------------------------- FP8 operators
@@ -854,26 +866,34 @@ class Fp8Config:
         return self._operands[ragged][0]
 
 
-def _fp8_codes(t, n, k, name):
+def _fp8_codes(t, n, k, name, device):
     """Address of a contiguous tensor of at least n E4M3 codes in rows of k, as torch's type or as bytes (None stays
     None)."""
-    return _rows_buffer(t, E4M3 if isinstance(t, _Tensor) and t.dtype is E4M3 else _U8, n, k, name, "codes")
+    return _buffer(t, E4M3 if isinstance(t, _Tensor) and t.dtype is E4M3 else _U8, n, name, device, k, "codes")
 
 
-def _fp8_scales(t, n, kb, name):
-    return _rows_buffer(t, _F32, n, kb, name, "scales")
+def _fp8_scales(t, n, kb, name, device):
+    return _buffer(t, _F32, n, name, device, kb, "scales")
 
 
-def _fp8_weights(cfg, w_codes, w_scales):
+def _fp8_weights(cfg, w_codes, w_scales, device=-1):
     """Addresses of the config's weight matrices and of their scales."""
-    return _fp8_weight(w_codes, w_scales, cfg._weights, "w_codes", "w_scales")
+    return _fp8_weight(w_codes, w_scales, cfg._weights, "w_codes", "w_scales", device)
 
 
-def _fp8_weight(codes, scales, sizes, name, scales_name):
+def _fp8_weight(codes, scales, sizes, name, scales_name, device):
     """Addresses of quantised matrices and of their scales: sizes are their codes, scales, codes of a row, scales of a
     row."""
     n, ns, k, kb = sizes
-    return _fp8_codes(codes, n, k, name), _fp8_scales(scales, ns, kb, scales_name)
+    return _fp8_codes(codes, n, k, name, device), _fp8_scales(scales, ns, kb, scales_name, device)
+
+
+def _fp8_out(cfg, out, rows, device):
+    if not isinstance(out, _Tensor):
+        raise TypeError("out must be a torch tensor")
+    if out.get_device() != device:
+        raise ValueError(f"out is on {out.device}, the call's other tensors on device {device}")
+    return _fp4_out(cfg, out, rows)
 
 
 def _fp8_sizes(e, n, k):
@@ -907,12 +927,12 @@ def fp8_quantize(cfg: Fp8Config, x, codes, scales, values=None, rows=None, offse
     config's elements.  ``rows`` gathers from x's rows (entries that name none give zero rows)."""
     ragged = offsets is not None
     n, n_codes, n_scales = cfg._operands[ragged]
-    handle = _launch_stream(stream, x, "x")
+    handle, device = _launch_stream(stream, x, "x")
     st = _lib.b4_fp8_quantize(
-        _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _fp4_buffer(rows, _I32, n, "rows"),
-        _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None,
-        _fp8_codes(codes, n_codes, cfg.k, "codes"), _fp8_scales(scales, n_scales, cfg.blocks, "scales"),
-        values if values is None else _rows_buffer(values, cfg.x_dtype, n_codes, cfg.k, "values"), handle)
+        _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _buffer(rows, _I32, n, "rows", device),
+        _buffer(offsets, _I32, cfg.num_groups + 1, "offsets", device) if ragged else None,
+        _fp8_codes(codes, n_codes, cfg.k, "codes", device), _fp8_scales(scales, n_scales, cfg.blocks, "scales", device),
+        values if values is None else _buffer(values, cfg.x_dtype, n_codes, "values", device, cfg.k), handle)
     if st:
         _check(st)
 
@@ -921,14 +941,14 @@ def fp8_matmul(cfg: Fp8Config, a_codes, a_scales, w_codes, w_scales, out, offset
                device_status=None, stream=None):
     """Enqueue the product of two quantised operands (``b4_fp8_matmul``)."""
     n, n_codes, n_scales = cfg._operands[offsets is not None]
-    handle = _launch_stream(stream, a_codes, "a_codes")
-    wp, sp = _fp8_weights(cfg, w_codes, w_scales)
+    handle, device = _launch_stream(stream, a_codes, "a_codes")
+    wp, sp = _fp8_weights(cfg, w_codes, w_scales, device)
     st = _lib.b4_fp8_matmul(
-        cfg._ref, _fp8_codes(a_codes, n_codes, cfg.k, "a_codes"), _fp8_scales(a_scales, n_scales, cfg.blocks, "a_scales"),
-        wp, sp, offsets if offsets is None else _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets"),
-        out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, n, "out_rows"), _fp4_out(cfg, out, n),
-        device_status if device_status is None else _fp4_buffer(device_status, _I32, 2, "device_status"),
-        handle)
+        cfg._ref, _fp8_codes(a_codes, n_codes, cfg.k, "a_codes", device),
+        _fp8_scales(a_scales, n_scales, cfg.blocks, "a_scales", device), wp, sp,
+        offsets if offsets is None else _buffer(offsets, _I32, cfg.num_groups + 1, "offsets", device),
+        out_rows if out_rows is None else _buffer(out_rows, _I32, n, "out_rows", device), _fp8_out(cfg, out, n, device),
+        device_status if device_status is None else _buffer(device_status, _I32, 2, "device_status", device), handle)
     if st:
         _check(st)
 
@@ -949,13 +969,13 @@ def fp8_linear(cfg: Fp8Config, x, w_codes, w_scales, out, workspace, rows=None, 
     """
     m = cfg.m
     ragged = offsets is not None
-    handle = _launch_stream(stream, x, "x")
-    wp, sp = _fp8_weights(cfg, w_codes, w_scales)
+    handle, device = _launch_stream(stream, x, "x")
+    wp, sp = _fp8_weights(cfg, w_codes, w_scales, device)
     st = _lib.b4_fp8_linear(
-        _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _fp4_buffer(rows, _I32, m, "rows"),
-        _fp4_buffer(offsets, _I32, cfg.num_groups + 1, "offsets") if ragged else None, wp, sp,
-        out_rows if out_rows is None else _fp4_buffer(out_rows, _I32, m, "out_rows"), _fp4_out(cfg, out, m),
-        _fp4_buffer(workspace, _U8, 0, "workspace"), workspace.numel(), handle)
+        _fp8_x(cfg, x, rows, ragged), x.data_ptr(), rows if rows is None else _buffer(rows, _I32, m, "rows", device),
+        _buffer(offsets, _I32, cfg.num_groups + 1, "offsets", device) if ragged else None, wp, sp,
+        out_rows if out_rows is None else _buffer(out_rows, _I32, m, "out_rows", device), _fp8_out(cfg, out, m, device),
+        _buffer(workspace, _U8, 0, "workspace", device), workspace.numel(), handle)
     if st:
         _check(st)
 
@@ -974,22 +994,24 @@ def fused_moe_fp8(cfg: MoEConfig, x, w13, s13, w2, s2, topk_ids, topk_weights, a
     bf16 is written in full.  The config's format and path are not read."""
     e, m, h, i = cfg.num_local_experts, cfg.m, cfg.hidden, cfg.inter
     rows, routes = m * h, m * cfg.top_k
-    xp, op = _rows_buffer(x, torch.bfloat16, rows, h, "x"), _rows_buffer(out, torch.bfloat16, rows, h, "out")
+    handle, device = _launch_stream(stream, x, "x")
+    xp, op = _buffer(x, torch.bfloat16, rows, "x", device, h), _buffer(out, torch.bfloat16, rows, "out", device, h)
     sizes13, sizes2 = _fp8_layer_sizes(e, h, i, activation)
-    w13p, s13p = _fp8_weight(w13, s13, sizes13, "w13", "s13")
-    w2p, s2p = _fp8_weight(w2, s2, sizes2, "w2", "s2")
-    idp = _rows_buffer(topk_ids, _I32, routes, cfg.top_k, "topk_ids")
-    wtp = _rows_buffer(topk_weights, _F32, routes, cfg.top_k, "topk_weights")
-    _need(workspace, _U8, "workspace")
-    if None in (xp, op, w13p, s13p, w2p, s2p, idp, wtp):
-        for t, name in ((x, "x"), (out, "out"), (topk_ids, "topk_ids"), (topk_weights, "topk_weights"), (w13, "w13"),
-                        (s13, "s13"), (w2, "w2"), (s2, "s2")):
+    w13p, s13p = _fp8_weight(w13, s13, sizes13, "w13", "s13", device)
+    w2p, s2p = _fp8_weight(w2, s2, sizes2, "w2", "s2", device)
+    idp = _buffer(topk_ids, _I32, routes, "topk_ids", device, cfg.top_k)
+    wtp = _buffer(topk_weights, _F32, routes, "topk_weights", device, cfg.top_k)
+    wsp = _buffer(workspace, _U8, 0, "workspace", device)
+    if None in (op, w13p, s13p, w2p, s2p, idp, wtp, wsp):
+        for t, name in ((out, "out"), (topk_ids, "topk_ids"), (topk_weights, "topk_weights"), (w13, "w13"), (s13, "s13"),
+                        (w2, "w2"), (s2, "s2"), (workspace, "workspace")):
             if t is None:
                 raise TypeError(f"{name} must be a torch tensor")
-    handle = _launch_stream(stream, x, "x")
     c = cfg._c()
-    st = _lib.b4_fused_moe_fp8(ctypes.byref(c), xp, w13p, s13p, w2p, s2p, idp, wtp, int(activation), op,
-                               workspace.data_ptr(), workspace.numel(), handle)
+    if cfg.expert_map is not None:
+        _buffer(cfg.expert_map, _I32, cfg.num_global_experts, "expert_map", device)
+    st = _lib.b4_fused_moe_fp8(ctypes.byref(c), xp, w13p, s13p, w2p, s2p, idp, wtp, int(activation), op, wsp,
+                               workspace.numel(), handle)
     if st:
         _check(st)
 
