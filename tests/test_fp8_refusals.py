@@ -3,6 +3,10 @@
 The library is replaced by a recorder, so that a call that is let through is seen and nothing runs.
 """
 
+import glob
+import os
+import re
+
 import pytest
 import torch
 
@@ -128,3 +132,13 @@ def test_a_missing_tensor_is_named(b4, monkeypatch, entry, name):
         monkeypatch.undo()
     with pytest.raises(TypeError, match=f"{name} must be a torch tensor"):
         call(**{**tensors, name: None})
+
+
+def test_no_copy_is_multicast():
+    """A copy into several CTAs may only read this GPU's memory, which the address of an operand does not tell."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "w4a16_moe_gb300", "csrc")
+    files = glob.glob(os.path.join(csrc, "*.cu*"))
+    assert files
+    for f in files:
+        text = re.sub(r'"\s*"', "", open(f).read())  # (an instruction may be several literals)
+        assert not re.search(r"cp\.async\.bulk[^;]*multicast", text), f

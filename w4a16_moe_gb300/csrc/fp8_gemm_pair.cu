@@ -2,11 +2,12 @@
 // form for many rows.  The formula is that of fp8_gemm.cuh.
 //
 // A pair takes units of 256 activation rows x 256 weight rows, each CTA 128 of the activation
-// rows.  Both need all of the weight rows: each CTA loads a block of 128 of them and multicasts
-// it to both, so an SM asks L2 for 32 KB a stage of 128 K and takes in 48 KB, for 512 cycles
-// of products (measured with copies alone: 480 cycles a stage on all SMs, 756 without
-// sharing).  The rows that are left of a group, 128 or fewer, make wide units: both CTAs take
-// them, each with 256 weight rows of its own and without sharing.
+// rows and all of the weight rows, which it loads for itself: 48 KB a stage of 128 K, for 512
+// cycles of products (copies alone take 756 cycles a stage on all SMs, less than the chain
+// below).  The rows that are left of a group, 128 or fewer, make wide units: both CTAs take
+// them, each with 256 weight rows of its own.  The two share no memory; they are a cluster so
+// that they run side by side and meet each other's weights in L2 (64 groups of 192 rows, N =
+// 2816, K = 2048 104.9 us, 106.0 as CTAs by themselves).
 //
 // H: the product is the first of a layer (b4_fused_moe_fp8).  A unit's sums become h, 128
 // columns of a gated activation (its weight rows are 128 gate rows and the 128 up rows that go
@@ -30,8 +31,8 @@
 // unit looked up at its start 112, under the last stages of the one before 106; three stages
 // in the ring 104.4, four where no boxes are staged 103.3.
 //
-// Measured: N = K = 4096, 4096 rows 64 us (2.1 PFLOP/s), 8192 x 8192 x 4096 213 us (2.6
-// PFLOP/s); 64 groups of 192 rows, N = 2816, K = 2048 103 us.
+// Measured: N = K = 4096, 4096 rows 63 us (2.2 PFLOP/s), 8192 x 8192 x 4096 215 us (2.5
+// PFLOP/s); 64 groups of 192 rows, N = 2816, K = 2048 105 us.
 
 #include "fp8_mma.cuh"
 #include "fp8_quant.cuh"
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   PairGroups& groups = *reinterpret_cast<PairGroups*>(smem + C::misc + 16);  // ragged only
   uint8_t* s_a = smem + C::a;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::bars);
-  uint64_t* empty = full + kPairSlots;                                // the products of both CTAs are through with the slot
+  uint64_t* empty = full + kPairSlots;                                // the products are through with the slot
   uint64_t* full_acc = empty + kPairSlots;
   uint64_t* empty_acc = full_acc + 4;
   uint64_t* drain = empty_acc + 4;
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = blockIdx.x & 1;
   const Fp4GemmParams& g = p.g;
   const Abort ab{g.status, s_abort};
 
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
     *s_abort = 0;
     for (int i = 0; i < kPairSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 2);
+      mbar_init(&empty[i], 1);
     }
     mbar_init(drain, 2);
     for (int i = 0; i < 4; ++i) {
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   const int wtiles = cdiv(g.n, 128);
   if (RAGGED) build_pair_groups(g, groups, wp);
   tc_fence_before();
-  cluster_sync();  // both CTAs' barriers exist before either signals
+  __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0) pdl_launch_dependents();
   const uint32_t tmem = *s_tmem;
@@ -256,8 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       // third of what DRAM's latency takes.
       uint32_t i = 0;
       bool ok = true;
-      // A CTA's boxes of weights in a stage: of block b of 128 rows (N of accumulator b) for both CTAs, b its
-      // rank, or of wide units both blocks for itself; gated, a block is 64 gate rows and their up rows.
+      // A unit's boxes of weights in a stage: both blocks of 128 rows; gated, a block is 64 gate rows and their up
+      // rows.  The CTAs of a tall unit ask one block each into L2.
+      constexpr int kBox = H == kGated ? 64 : 128;
       struct Boxes {
         int row, first, rows;
         bool wide, none;
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
         Boxes B;
         B.wide = U.wide;
         B.none = U.wide && U.wt >= wp;
-        B.row = (int)warp_uniform(U.group * g.n + U.wt * (H == kGated ? 128 : 256) + (U.wide ? 0 : (int)rank * (H == kGated ? 64 : 128)));
+        B.row = (int)warp_uniform(U.group * g.n + U.wt * 2 * kBox);
         B.first = (int)warp_uniform(U.first);
         B.rows = (int)warp_uniform(U.rows);
         return B;
@@ -278,11 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
         if (!RAGGED || pu >= n_units) return;
         if (ps == 0) ahead = boxes_of(pu);
         if (!ahead.none && elect_one()) {
-          tma_prefetch_2d(&p.tmap_w, ps * 128, ahead.row);
-          if (H == kGated) tma_prefetch_2d(&p.tmap_w, ps * 128, ahead.row + g.n / 2);
+          const int row = ahead.row + (ahead.wide ? 0 : (int)rank * kBox);
+          tma_prefetch_2d(&p.tmap_w, ps * 128, row);
+          if (H == kGated) tma_prefetch_2d(&p.tmap_w, ps * 128, row + g.n / 2);
           if (ahead.wide) {
-            tma_prefetch_2d(&p.tmap_w, ps * 128, ahead.row + (H == kGated ? 64 : 128));
-            if (H == kGated) tma_prefetch_2d(&p.tmap_w, ps * 128, ahead.row + g.n / 2 + 64);
+            tma_prefetch_2d(&p.tmap_w, ps * 128, row + kBox);
+            if (H == kGated) tma_prefetch_2d(&p.tmap_w, ps * 128, row + g.n / 2 + kBox);
           }
         }
         __syncwarp();
@@ -293,23 +296,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       for (int u = u0; u < n_units && ok; u += du) {
         const Boxes B = boxes_of(u);
         const uint32_t bytes = (B.none ? 0 : kPairWStage) + cdiv(B.rows, kPairBox) * kPairBox * 128;
-        uint8_t* sw0 = smem + (B.wide ? 0 : rank * kWStage);
         for (int s = 0; s < p.kb; ++s, ++i) {
           const uint32_t slot = i % kPairSlots;
           ok = __all_sync(0xffffffffu, wait(&empty[slot], ((i / kPairSlots) & 1) ^ 1, ab, 131));
           if (!ok) break;
           if (elect_one()) {
             mbar_arrive_expect_tx(&full[slot], bytes);
-            uint8_t* sw = sw0 + slot * kPairWStage;
-            if (!B.wide) {
-              tma_load_2d_both(sw, &p.tmap_w, s * 128, B.row, &full[slot]);
-              if (H == kGated) tma_load_2d_both(sw + kWStage / 2, &p.tmap_w, s * 128, B.row + g.n / 2, &full[slot]);
-            } else if (!B.none) {
+            uint8_t* sw = smem + slot * kPairWStage;
+            if (!B.none) {
               tma_load_2d(sw, &p.tmap_w, s * 128, B.row, &full[slot]);
-              tma_load_2d(sw + kWStage, &p.tmap_w, s * 128, B.row + (H == kGated ? 64 : 128), &full[slot]);
+              tma_load_2d(sw + kWStage, &p.tmap_w, s * 128, B.row + kBox, &full[slot]);
               if (H == kGated) {
                 tma_load_2d(sw + kWStage / 2, &p.tmap_w, s * 128, B.row + g.n / 2, &full[slot]);
-                tma_load_2d(sw + kWStage * 3 / 2, &p.tmap_w, s * 128, B.row + g.n / 2 + 64, &full[slot]);
+                tma_load_2d(sw + kWStage * 3 / 2, &p.tmap_w, s * 128, B.row + g.n / 2 + kBox, &full[slot]);
               }
             }
             if (B.rows > 0) tma_load_2d(s_a + slot * kPairAStage, &p.tmap_a, s * 128, B.first, &full[slot]);
@@ -321,8 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
         }
       }
       if (ab.raised() && lane == 0) {
-        // copies already issued, the other CTA's too, land before the shared memory goes away:
-        // give them a fixed time
+        // copies already issued land before the shared memory goes away: give them a fixed time
         const unsigned long long t0 = globaltimer();
         while (globaltimer() - t0 < 2000000ull) {
         }
@@ -359,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
 #pragma unroll
           for (int j = 0; j < 4; ++j) mma_fp8(d + 128, ad + 2 * j, wd + kWStage / 16 + 2 * j, idesc, j > 0);
           mma_commit(&full_acc[2 * w + 1]);
-          mma_commit_both(&empty[slot]);
+          mma_commit(&empty[slot]);
         }
         __syncwarp();
         slot += 2;
@@ -587,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
 
   if (BOXES && warp >= 4 && lane == 0) bulk_wait();  // the boxes have left
   tc_fence_before();
-  cluster_sync();  // neither CTA leaves while the pair's copies, products or signals may touch it
+  __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
@@ -604,12 +602,12 @@ cudaError_t launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t stream) 
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p);

@@ -22,22 +22,6 @@ __device__ __forceinline__ void mma_fp8(uint32_t d, uint32_t a, uint32_t b, uint
       "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHiSw128)
       : "memory");
 }
-// A box into the same place of both CTAs' shared memory, each CTA's barrier counting its copy.
-__device__ __forceinline__ void tma_load_2d_both(void* dst, const CUtensorMap* tm, int c0, int r0, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
-      "%3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(tm), "r"(c0), "r"(r0), "r"(smem_u32(bar)), "h"((uint16_t)3)
-      : "memory");
-}
-// Arrive once on `bar` in both CTAs when every instruction this thread issued so far completes.
-__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
