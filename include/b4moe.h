@@ -502,13 +502,14 @@ b4_status b4_fused_moe_a4(const b4_moe_config* cfg, const uint16_t* x, const uin
  * sum of its two largest (group_top = 2; of what it has), and the experts of the
  * top_groups best groups stay.  The ids are the top_k experts of largest c in
  * descending order; the weights are s, over their sum where renormalised, times scale.
- * Ties, of groups too, go to the lowest index.  The order is that of the real numbers:
- * where fp32 does not separate two of them the row is done again in 64 bits.
+ * Ties, of groups too, go to the lowest index.  The order is that of the real numbers, as
+ * far as 64 bits hold them: where fp32 does not separate two, they are compared again.
  * (Renormalised softmax weights are the softmax over the chosen logits.)
  *
- * An expert whose logit or bias is NaN or -inf is never chosen and adds nothing; where
- * fewer than top_k can be, the rest of the row is id -1 with weight 0, which the layers
- * drop.  A logit of +inf counts as the limit: softmax shares 1 among those.  A bias of
+ * An expert whose logit or bias is NaN or -inf is never chosen and does not count for its
+ * group; by its logit it adds nothing to the softmax either, a bias leaves it in there.
+ * Where fewer than top_k can be chosen, the rest of the row is id -1 with weight 0, which
+ * the layers drop.  A logit of +inf counts as the limit: softmax shares 1 among those.  A bias of
  * +inf puts its expert first. */
 typedef enum b4_score { B4_SCORE_SOFTMAX = 0, B4_SCORE_SIGMOID = 1 } b4_score;
 
@@ -573,7 +574,8 @@ typedef struct b4_fp8_config {
  * The quotient is a product with a reciprocal known to 46 bits, rounded once to fp32; the
  * gated activations as in b4_fp4_quantize.  A block with a NaN or an infinity has the scale
  * NaN and codes NaN.  rows (or NULL) gathers: a negative entry gives a zero row (scales 1).
- * values (or NULL) receives scale * e4m3(code) in x's type, [rows][k].  Rows of a ragged
+ * values (or NULL) receives scale * e4m3(code) rounded to x's type, [rows][k] (infinite where it
+ * passes the type's range: POW2 codes of its largest numbers).  Rows of a ragged
  * operand past offsets[num_groups] are not written.  block_rows = 128 takes neither rows nor
  * offsets.  1 launch; m = 0 launches nothing. */
 b4_status b4_fp8_quantize(const b4_fp8_config* cfg, const void* x, const int32_t* rows, const int32_t* offsets,
@@ -581,7 +583,8 @@ b4_status b4_fp8_quantize(const b4_fp8_config* cfg, const void* x, const int32_t
 
 /* out[t][n] = sum over blocks b of s_a[t][b] s_w[e][n / 128][b] sum_{k in b} a[t][k] w[e][n][k] for
  * the rows t of group e: the tensor cores multiply and add the codes of a block in fp32, the
- * scaled blocks are added in fp32 in order of k, and the result is rounded once.
+ * scaled blocks are added in fp32 in order of k, and the result is rounded once.  s_a s_w is
+ * formed in fp32: below 2^-126 it loses bits, past 2^128 it is infinite (times 0: NaN).
  *
  * a_codes, a_scales  quantised activations, [rows][k] and [rows][ceil(k / 128)].
  * w_codes       [num_groups][n][k], w_scales [num_groups][ceil(n / 128)][ceil(k / 128)].

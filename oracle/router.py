@@ -5,7 +5,8 @@ TEST INFRASTRUCTURE ONLY (see ``oracle/__init__.py``).
 The pages take ids and weights as inputs; what is fixed here:
 
 * s = softmax(z) or sigmoid(z), c = s + bias, without a bias the order of z;
-* a NaN or -inf in a logit or a bias takes the expert out altogether;
+* a NaN or -inf in a logit takes the expert out altogether, in a bias out of the
+  choice and its group's value (the softmax has its logit still);
 * groups of neighbouring experts count with the sum of their ``group_top``
   largest c (of what they have; by z where that is one score without a bias);
   the ``top_groups`` best stay;

@@ -134,3 +134,15 @@ def test_softmax_of_one_large_and_many_small(b4, e, groups, v):  # noqa: F811
     for shift in (-1e-8, 1e-8):
         bias[e - 1] = float(s[0] - 1.0 + shift)
         _compare(b4, z, bias, 2, "softmax", groups=groups, top_groups=groups)
+
+
+def test_experts_out_by_their_bias_stay_in_the_softmax(b4):  # noqa: F811
+    """Without renormalisation the weights show what the softmax's sum is made of."""
+    z = _z(6, 64, 45, F32)
+    z[1, 5] = z[2, 9] = float("-inf")
+    z[3, 40:] = float("nan")
+    bias = torch.randn(64, generator=torch.Generator().manual_seed(46)) * 0.1
+    bias[[5, 30]] = float("-inf")
+    bias[[7, 41]] = float("nan")
+    for kw in (dict(), dict(groups=4, top_groups=2), dict(groups=4, top_groups=2, group_top=2)):
+        _compare(b4, z, bias, 8, "softmax", renorm=False, scale=1.5, **kw)

@@ -345,6 +345,8 @@ b4_status moe_plan(const b4_moe_config* cfg, int32_t activation, MoeFp8* M) {
   M->sorted = take(sizeof(int32_t) * (size_t)r_cap);
   M->quant = take(L1.total > L2.total ? L1.total : L2.total);  // x's rows, then h's
   M->fc1 = take(sizeof(float) * (size_t)r_cap * n1);
+  // FC2's output of a route, rounded to bf16 before the weighted sum: 2^-9 of it, where each code of its operands
+  // is rounded by 2^-4; in 32 bits the rows that pass through memory here would be twice as many bytes
   M->y = take(sizeof(uint16_t) * (size_t)r_cap * cfg->hidden);
   M->total = off;
   return B4_OK;
