@@ -151,10 +151,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* t
       : "memory");
 }
 
-// Ask a box into L2.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* tm, int c0, int r0) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tm), "r"(c0), "r"(r0) : "memory");
-}
 // A box from shared memory to (column c0, row r0) of a matrix, what lies outside of it left out;
 // in groups of the issuing thread.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, int c0, int r0, const void* src) {

@@ -116,10 +116,11 @@ Fp8QuantParams quant_params(const b4_fp8_config* c, const void* x, const int32_t
 
 // Activation rows of a unit: 32 or 128 (fp8_gemm.cuh, one SM a unit of 128 outputs), 256
 // (fp8_gemm_pair.cu, a pair of SMs, 256 outputs).  By the rows, of ragged groups their mean.
-// Measured in us at 32 / 128 / 256: N = K = 4096, m = 64 9.6 / 13.4 / 17.7, 128 12.4 / 14.1 / 19.7, 256 21.3 / 14.3 /
-// 18.9, 512 38.8 / 14.8 / 20.2, 1024 66 / 25.7 / 21.1; 64 groups, N = 2816, K = 2048, mean 6 61.4 / 64.4 / -, 16 62.3 / 65.1 /
-// -, 96 168 / 70.5 / 90.2, 128 214 / 93.8 / 90.8, 192 - / 125 / 106, with popularities spread by e^N(0, 1) 64 124 / 73.0 /
-// 77.1, 96 164 / 84.9 / 84.0, 192 - / 125 / 109; 28 groups, N = K = 2880, mean 32 54.7 / 48.0 / -, 64 80.0 / 49.2 / 62.9.
+// Measured in us at 32 / 128 / 256: N = K = 4096, m = 64 9.5 / 13.4 / 18.0, 128 12.7 / 13.9 / 19.0, 256 21.3 / 14.1 /
+// 19.1, 512 38.8 / 14.5 / 19.5, 1024 66 / 25.5 / 19.9; 64 groups, N = 2816, K = 2048, mean 6 61.4 / 64.4 / -, 16 62.3 / 65.1 /
+// -, 96 168 / 69.4 / 73.8, 128 214 / 91.5 / 83.9, 192 - / 123 / 99.5, with popularities spread by e^N(0, 1) 64 124 / 71.1 /
+// 69.1, 96 164 / 83.4 / 76.7, 192 - / 123 / 99.6; 28 groups, N = K = 2880, mean 32 54.7 / 47.3 / 50.9, 64 80.0 / 48.2 / 52.3,
+// 96 - / 49.5 / 54.0, 128 - / 62.9 / 61.6.
 int unit_rows(const b4_fp8_config* c, bool ragged) {
   if (ragged) {
     const int64_t per = c->m / c->num_groups;

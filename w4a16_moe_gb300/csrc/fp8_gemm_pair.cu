@@ -29,10 +29,11 @@
 // 70.6 us, through shared memory 67.4, as TMA boxes 65.8; the copying warp's loop with
 // decisions in it 72.3, without 65.8.  64 groups of 192 rows, N = 2816, K = 2048: scales of a
 // unit looked up at its start 112, under the last stages of the one before 106; three stages
-// in the ring 104.4, four where no boxes are staged 103.3.
+// in the ring 104.4, four where no boxes are staged 103.3; weights asked into L2 ahead of their
+// copies 103, not 99.5.
 //
-// Measured: N = K = 4096, 4096 rows 63 us (2.2 PFLOP/s), 8192 x 8192 x 4096 215 us (2.5
-// PFLOP/s); 64 groups of 192 rows, N = 2816, K = 2048 105 us.
+// Measured: N = K = 4096, 4096 rows 63 us (2.2 PFLOP/s), 8192 x 8192 x 4096 215 us (2.6
+// PFLOP/s); 64 groups of 192 rows, N = 2816, K = 2048 99.5 us.
 
 #include "fp8_mma.cuh"
 #include "fp8_quant.cuh"
@@ -48,7 +49,6 @@ constexpr int kPairBox = 64;                    // activation rows of a box
 constexpr int kPairAStage = 128 * 128;
 constexpr int kPairWStage = 2 * kWStage;        // both blocks of weight rows
 constexpr int kOutTile = 2 * 32 * 128;          // staged outputs of a warp: 32 rows of two times 64, 128-byte swizzle
-constexpr int kPrefetch = 10;                   // stages of weights asked into L2 ahead of their copies
 constexpr int kAhead = 4;                       // units looked up ahead of the promoting warps
 constexpr int kScaleQuad = 130 * 4;             // scales of four stages: 128 rows, two blocks of weights; two of these
 
@@ -252,71 +252,39 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   if (warp < 4) {
     if (warp == 0) {
       // --------------------------------------------------------- copies
-      // Weights are asked into L2 kPrefetch stages ahead of their copies (across units, and
-      // from the start, under the quantiser): the ring alone has 48 KB of them on their way, a
-      // third of what DRAM's latency takes.
+      // (None are asked into L2 ahead: what the SMs have in flight is enough for DRAM, and more is fetched twice.
+      // 128 groups of 128 rows, N = 4096, K = 1536 173 us with ten stages ahead, 172 with one, 165 so; the layer of
+      // E128 H4096 I1536, 2048 tokens 585, 543, 536.)
       uint32_t i = 0;
       bool ok = true;
-      // A unit's boxes of weights in a stage: both blocks of 128 rows; gated, a block is 64 gate rows and their up
-      // rows.  The CTAs of a tall unit ask one block each into L2.
+      // A unit's boxes of weights in a stage: both blocks of 128 rows; gated, a block is 64 gate rows and their up rows.
       constexpr int kBox = H == kGated ? 64 : 128;
-      struct Boxes {
-        int row, first, rows;
-        bool wide, none;
-      };
-      auto boxes_of = [&](int u) {
-        const PairUnit U = pair_unit<RAGGED>(g, groups, wp, u, rank);
-        Boxes B;
-        B.wide = U.wide;
-        B.none = U.wide && U.wt >= wp;
-        B.row = (int)warp_uniform(U.group * g.n + U.wt * 2 * kBox);
-        B.first = (int)warp_uniform(U.first);
-        B.rows = (int)warp_uniform(U.rows);
-        return B;
-      };
-      Boxes ahead{};
-      int pu = u0, ps = 0;
-      auto prefetch = [&]() {
-        if (!RAGGED || pu >= n_units) return;
-        if (ps == 0) ahead = boxes_of(pu);
-        if (!ahead.none && elect_one()) {
-          const int row = ahead.row + (ahead.wide ? 0 : (int)rank * kBox);
-          tma_prefetch_2d(&p.tmap_w, ps * 128, row);
-          if (H == kGated) tma_prefetch_2d(&p.tmap_w, ps * 128, row + g.n / 2);
-          if (ahead.wide) {
-            tma_prefetch_2d(&p.tmap_w, ps * 128, row + kBox);
-            if (H == kGated) tma_prefetch_2d(&p.tmap_w, ps * 128, row + g.n / 2 + kBox);
-          }
-        }
-        __syncwarp();
-        if (++ps == p.kb) ps = 0, pu += du;
-      };
-      for (int j = 0; j < kPrefetch; ++j) prefetch();
       if (g.a_is_new) pdl_wait();
       for (int u = u0; u < n_units && ok; u += du) {
-        const Boxes B = boxes_of(u);
-        const uint32_t bytes = (B.none ? 0 : kPairWStage) + cdiv(B.rows, kPairBox) * kPairBox * 128;
+        const PairUnit U = pair_unit<RAGGED>(g, groups, wp, u, rank);
+        const bool none = U.wide && U.wt >= wp;
+        const int row = (int)warp_uniform(U.group * g.n + U.wt * 2 * kBox);
+        const int first = (int)warp_uniform(U.first), rows = (int)warp_uniform(U.rows);
+        const uint32_t bytes = (none ? 0 : kPairWStage) + cdiv(rows, kPairBox) * kPairBox * 128;
         for (int s = 0; s < p.kb; ++s, ++i) {
           const uint32_t slot = i % kPairSlots;
           ok = __all_sync(0xffffffffu, wait(&empty[slot], ((i / kPairSlots) & 1) ^ 1, ab, 131));
           if (!ok) break;
           if (elect_one()) {
             mbar_arrive_expect_tx(&full[slot], bytes);
-            uint8_t* sw = smem + slot * kPairWStage;
-            if (!B.none) {
-              tma_load_2d(sw, &p.tmap_w, s * 128, B.row, &full[slot]);
-              tma_load_2d(sw + kWStage, &p.tmap_w, s * 128, B.row + kBox, &full[slot]);
+            uint8_t *sw = smem + slot * kPairWStage, *sa = s_a + slot * kPairAStage;
+            if (!none) {
+              tma_load_2d(sw, &p.tmap_w, s * 128, row, &full[slot]);
+              tma_load_2d(sw + kWStage, &p.tmap_w, s * 128, row + kBox, &full[slot]);
               if (H == kGated) {
-                tma_load_2d(sw + kWStage / 2, &p.tmap_w, s * 128, B.row + g.n / 2, &full[slot]);
-                tma_load_2d(sw + kWStage * 3 / 2, &p.tmap_w, s * 128, B.row + g.n / 2 + kBox, &full[slot]);
+                tma_load_2d(sw + kWStage / 2, &p.tmap_w, s * 128, row + g.n / 2, &full[slot]);
+                tma_load_2d(sw + kWStage * 3 / 2, &p.tmap_w, s * 128, row + g.n / 2 + kBox, &full[slot]);
               }
             }
-            if (B.rows > 0) tma_load_2d(s_a + slot * kPairAStage, &p.tmap_a, s * 128, B.first, &full[slot]);
-            if (B.rows > kPairBox)
-              tma_load_2d(s_a + slot * kPairAStage + kPairBox * 128, &p.tmap_a, s * 128, B.first + kPairBox, &full[slot]);
+            if (rows > 0) tma_load_2d(sa, &p.tmap_a, s * 128, first, &full[slot]);
+            if (rows > kPairBox) tma_load_2d(sa + kPairBox * 128, &p.tmap_a, s * 128, first + kPairBox, &full[slot]);
           }
           __syncwarp();
-          prefetch();
         }
       }
       if (ab.raised() && lane == 0) {
