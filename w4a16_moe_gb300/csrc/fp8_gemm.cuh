@@ -25,7 +25,7 @@
 // K.  The partial sums go to the first CTA's shared memory as asynchronous stores that count
 // on its barrier, and it adds them in rank order, so the result does not depend on timing.
 //
-// Measured: 64 groups of 6 rows, N = 2816, K = 2048 60.7 us (372 MB, 6.1 TB/s), of 96 rows 70 us (5.9 TB/s); one row, N = K = 4096
+// Measured: 64 groups of 6 rows, N = 2816, K = 2048 61.9 us (372 MB, 6.0 TB/s), of 96 rows 70 us (5.9 TB/s); one row, N = K = 4096
 // 7.6 us, direct 7.7; eight groups of one row, N = 1536, K = 4096 (50 MB) direct 13.5 us: 96 CTAs of a unit each,
 // whose 32 stages follow one another.
 //

@@ -16,8 +16,8 @@
 // instructions.  A 128 x 128 block is read once and stays in the registers of 512 threads
 // between its maximum and its codes (with 256 threads 145 us for the second line below).
 //
-// Measured: 8192 rows of 4096 bf16 16.8 us (6.0 TB/s), with values too 26.4 (6.4 TB/s); 12288 gathered rows
-// of 2048 10.4; 16 fp32 matrices of 2816 x 2048, values too, 127 us (6.5 TB/s).
+// Measured: 8192 rows of 4096 bf16 16.8 us (6.0 TB/s), with values too 26.0 (6.5 TB/s); 12288 gathered rows
+// of 2048 10.4; 16 fp32 matrices of 2816 x 2048, values too, 128 us (6.5 TB/s).
 
 #include <type_traits>
 

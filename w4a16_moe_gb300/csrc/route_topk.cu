@@ -25,7 +25,7 @@
 //
 // Bound by latency for few tokens (one launch: 2.3 us for 1 token of 128 experts) and by the
 // issue of instructions for many: 16384 tokens of 256 experts in 8 groups, sigmoid with a bias,
-// bf16 21 us (8.4 MB of logits, read once).  A row done again as a whole holds its warp for 5 us,
+// bf16 22 us (8.4 MB of logits, read once).  A row done again as a whole holds its warp for 5 us,
 // which the last ones show: with close groups done so too it was 27.
 
 #include <cuda_bf16.h>
