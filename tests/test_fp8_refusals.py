@@ -134,6 +134,17 @@ def test_a_missing_tensor_is_named(b4, monkeypatch, entry, name):
         call(**{**tensors, name: None})
 
 
+def test_gathering_from_more_rows_than_an_index_reaches(b4):
+    """Every entry of rows names a row of such an x: no bound (a bound of the row count cut to 32 bits would drop some)."""
+    rows = torch.zeros(4, dtype=I32)
+    for make in (b4.Fp8Config, b4.Fp4Config):
+        for n, bound in ((1000, 1000), (2**31 - 1, 2**31 - 1), (2**31, 0), (2**32 + 5, 0)):
+            cfg = make(m=4, k=16)
+            b4._fp4_x(cfg, torch.empty(n, 16, dtype=BF, device="meta"), rows, False, type(cfg._struct))
+            bounded = cfg._gather[1]._obj if cfg._gather[1] is not None else cfg._struct
+            assert bounded.x_rows == bound
+
+
 def test_no_copy_is_multicast():
     """A copy into several CTAs may only read this GPU's memory, which the address of an operand does not tell."""
     csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "w4a16_moe_gb300", "csrc")

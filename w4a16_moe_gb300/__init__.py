@@ -522,7 +522,7 @@ def _fp4_x(cfg, x, rows, ragged, struct=_Fp4Config):
         bounded = cfg._gather
         if bounded[0] != n:
             c = struct.from_buffer_copy(cfg._struct)
-            c.x_rows = n
+            c.x_rows = n if n < 2**31 else 0  # (no entry reaches past more rows than that)
             bounded = cfg._gather = (n, ctypes.byref(c))
         return bounded[1]
     return cfg._ref
